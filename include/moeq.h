@@ -325,6 +325,163 @@ moeq_status moeq_layer_forward_static(const moeq_layer* L, const uint16_t* x, in
 /* Bytes of the fixed per-device workspace of moeq_layer_forward_static. */
 size_t moeq_static_workspace_capacity(void);
 
+/* ------------------------------------------------------------------
+ * Operators around the layer: grouped routing, residual + RMS norm with an
+ * 8-bit output, and the packed-weight matrix product with its epilogue.
+ * They serve decode and prefill alike (any M >= 0; M = 0 launches nothing),
+ * keep nothing between calls and touch only the M rows they are given.
+ * Row strides are in elements, at least the row's length, so rows may be
+ * parts of wider ones.  Sums are fp32 in a fixed order: results are
+ * deterministic.
+ */
+typedef enum { MOEQ_F32 = 0, MOEQ_BF16 = 1, MOEQ_I8 = 2, MOEQ_E4M3 = 3 } moeq_dtype;
+
+typedef enum { MOEQ_SCORE_SOFTMAX = 0, MOEQ_SCORE_SIGMOID = 1 } moeq_score;
+
+typedef struct {
+  int32_t n_experts;    /* E <= 4096 */
+  int32_t top_k;        /* K <= min(32, experts of the kept groups) */
+  int32_t score;        /* moeq_score */
+  int32_t n_groups;     /* <= 32, divides E; 1: no groups */
+  int32_t topk_groups;  /* groups kept, <= n_groups */
+  int32_t group_top;    /* a group ranks by the sum of its 1 or 2 largest values */
+  int32_t renorm;       /* 1: weights divided by the sum of the K chosen scores */
+  float router_scale;   /* logits are multiplied by this first; finite, > 0 */
+  float routed_scale;   /* weights are multiplied by this last; finite */
+} moeq_routing;
+
+/*
+ * Routing with group-limited choice and a bias for balance:
+ *   s = softmax(router_scale * l) or sigmoid(router_scale * l), per token;
+ *   v = s + bias (the bias steers the choice only; without one the order is
+ *   that of the logits themselves);
+ *   the topk_groups groups (of E / n_groups consecutive experts) with the
+ *   largest group value, then the K experts of those with the largest v,
+ *   listed by v descending; ties go to the lower index everywhere;
+ *   w = s_k (/ sum of the K s_k when renorm) * routed_scale.
+ * A group's value is its largest v (group_top 1) or the sum of its two
+ * largest v (group_top 2; without a bias v is s there).  The choice is that
+ * of real arithmetic: where fp32 scores are too close to tell, the token is
+ * routed again in fp64.
+ * A logit of NaN or -inf takes its expert out: it scores 0 and is chosen
+ * only when fewer than K others are left in the kept groups, lowest index
+ * first, with weight 0.  A token whose every logit is out gets weights 0.
+ *   logits: fp32 or bf16 (logit_type) [M][E], rows logit_stride apart;
+ *   bias: nullable fp32 [E], without NaN; idx: int32 [M][K]; w: fp32 [M][K].
+ * idx and w are moeq_expert_ffn's inputs.  Errors: INVALID_ARG, UNSUPPORTED
+ * (sizes, logit_type), ALIGNMENT (pointers off their element), CUDA.
+ */
+moeq_status moeq_route_groups(const moeq_routing* r, const void* logits, int32_t logit_type,
+                              int64_t logit_stride, const float* bias, int32_t M, int32_t* idx,
+                              float* w, void* stream);
+
+typedef struct {
+  const void* x;            /* [M][H] */
+  int32_t x_type;           /* F32 or BF16 */
+  int64_t x_stride;
+  const void* residual;     /* nullable [M][H] */
+  int32_t r_type;           /* F32 or BF16: of residual and r_out */
+  int64_t r_stride;
+  void* r_out;              /* nullable [M][H]; needs residual; may be residual itself */
+  int64_t r_out_stride;
+  const uint16_t* gamma;    /* bf16 [H] */
+  float eps;                /* > 0, finite */
+  uint16_t* y;              /* nullable bf16 [M][H] */
+  int64_t y_stride;
+  void* q;                  /* nullable 8-bit [M][H] */
+  int32_t q_type;           /* I8 or E4M3 */
+  int64_t q_stride;
+  float* q_scales;          /* fp32 [M][1] (q_group 0) or [M][ceil(H / 128)] (128) */
+  int32_t q_group;          /* columns that share a scale: 0 (the row) or 128 */
+} moeq_norm_args;
+
+/*
+ * The step between two blocks of a model, in one pass over the rows:
+ *   r = x + residual, rounded to r_type, also written to r_out (without a
+ *   residual r = x);
+ *   n = r / sqrt((1/H) sum_i r_i^2 + eps) * gamma;
+ *   y = bf16(n);
+ *   q = n / scale rounded to nearest even in int8 [-127, 127] or e4m3,
+ *   scale = max |n| / 127 or / 448 over the row or each 128 columns (the
+ *   last group may be shorter): q * scale stands for n.
+ * At least one of y and q is given.  Codes are those of exact arithmetic on
+ * r and gamma.  A row or group of zeros has scale 0 and codes 0; one that
+ * holds an infinity or NaN has scale NaN and codes 0.  The sum of squares is
+ * an fp32 one: |r| up to 1e18.
+ * r_out may be the residual's own memory (or x's, at the same type and
+ * stride); no other output may overlap an input.
+ * 1 <= H <= 32768.  Any alignment of whole elements is taken; 16-byte aligned
+ * rows (8 bytes for q) are faster.
+ * Errors: INVALID_ARG, UNSUPPORTED (types, q_group, H), ALIGNMENT, CUDA.
+ */
+moeq_status moeq_add_rmsnorm(const moeq_norm_args* n, int32_t M, int32_t H, void* stream);
+
+typedef enum {
+  MOEQ_ACT_NONE = 0,
+  MOEQ_ACT_SILU = 1,
+  MOEQ_ACT_GELU = 2,       /* 0.5 v (1 + erf(v / sqrt(2))) */
+  MOEQ_ACT_GELU_TANH = 3,  /* 0.5 v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) */
+  MOEQ_ACT_RELU = 4,
+  MOEQ_ACT_SIGMOID = 5
+} moeq_act;
+
+typedef struct {
+  const void* x;           /* [M][in_dim], rows 16-byte aligned */
+  int32_t x_type;          /* BF16, I8 or E4M3 */
+  int64_t x_stride;
+  const float* x_scales;   /* I8, E4M3: fp32 [M][1] or [M][ceil(in_dim / 128)] */
+  int32_t x_group;         /* columns that share a scale: 0 (the row) or 128 */
+  const uint16_t* bias;    /* nullable bf16 [out_dim] */
+  int32_t act;             /* moeq_act */
+  const void* mul;         /* nullable [M][out_dim] of out_type */
+  int64_t mul_stride;
+  const void* residual;    /* nullable [M][out_dim] of out_type */
+  int64_t residual_stride;
+  void* y;                 /* [M][out_dim] */
+  int32_t out_type;        /* F32 or BF16 */
+  int64_t y_stride;
+} moeq_linear_args;
+
+/*
+ * y[m][o] = act(sum_i x[m][i] w[o][i] + bias[o]) * mul[m][o] + residual[m][o]
+ * with matrix `expert` of the packed tensor t (every format and bit width of
+ * moeq_dequant, rows of any length), any M: attention projections, the dense
+ * blocks between MoE layers (mul holds the up projection when this call is
+ * the gate's), router logits of a whole prompt.  An I8 or E4M3 x with its
+ * scales is moeq_add_rmsnorm's output.
+ * Sums are fp32 throughout.  Few tokens multiply the codes themselves
+ * (exact products).  Many tokens with a bf16 y take weights rounded to fp16
+ * (relative 2^-11, an eighth of y's own rounding); with an fp32 y the
+ * weights keep 22 bits.  Neither has a range limit: rows are scaled by powers of two.
+ * An x row that holds an infinity or NaN gives a row of unspecified values
+ * and leaves the others untouched.
+ *   y may be mul's or residual's memory (same stride); it may not overlap x.
+ *   ws: device workspace of moeq_linear_workspace_bytes(t, M, x_type,
+ *   out_type) bytes, 256-byte aligned, contents ignored on entry; NULL where
+ *   that is 0 (few tokens).  Calls that may overlap in time need their own.
+ * Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, WORKSPACE, CUDA.
+ */
+moeq_status moeq_linear(const moeq_qtensor* t, int32_t expert, const moeq_linear_args* a,
+                        int32_t M, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of moeq_linear for M tokens (0: none needed, or invalid
+ * arguments).  It grows with M. */
+size_t moeq_linear_workspace_bytes(const moeq_qtensor* t, int32_t M, int32_t x_type,
+                                   int32_t out_type);
+
+/*
+ * moeq_layer_forward with the routing of `r` in the place of the layer's own
+ * (its top_k, renorm and router_scale are not read; n_experts and top_k of
+ * both must agree): moeq_linear on the router, moeq_route_groups with `bias`,
+ * moeq_expert_ffn.  Same buffers and outputs; ws of
+ * moeq_routed_workspace_bytes(L, M, mode) bytes.  Errors: those of the three.
+ */
+moeq_status moeq_layer_forward_routed(const moeq_layer* L, const moeq_routing* r,
+                                      const float* bias, const uint16_t* x, int32_t M, float* y,
+                                      const float* residual, int32_t* idx_out, float* w_out,
+                                      void* ws, size_t ws_bytes, int32_t mode, void* stream);
+size_t moeq_routed_workspace_bytes(const moeq_layer* L, int32_t M, int32_t mode);
+
 /* Reads and clears the device status word of the current device (synchronises
  * `stream`).  *status_out receives MOEQ_OK or the first device error seen. */
 moeq_status moeq_device_status(void* stream, int32_t* status_out);

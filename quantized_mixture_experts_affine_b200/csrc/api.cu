@@ -87,6 +87,10 @@ static moeq_status check_tensor(const moeq_qtensor* t, int64_t n_mats) {
   return MOEQ_OK;
 }
 
+namespace moeq {
+moeq_status tensor_check(const moeq_qtensor* t, int64_t n_mats) { return check_tensor(t, n_mats); }
+}  // namespace moeq
+
 // Decode GEMV limit: a row is cut into at most 8 slices of 512 bytes.
 static int slices_of(const moeq_qtensor& t) {
   const int cpr = t.in_dim / chunk_values(t.bits);
@@ -783,6 +787,14 @@ moeq_status forward_arg_check(const moeq_layer* L, const uint16_t* x, int32_t M,
     return MOEQ_ERR_ALIGNMENT;
   if (residual && !aligned(residual, 16)) return MOEQ_ERR_ALIGNMENT;
   return MOEQ_OK;
+}
+}  // namespace moeq
+
+namespace moeq {
+moeq_status mode_check(const moeq_layer* L, int32_t M, int32_t mode) {
+  mode = resolve_mode(mode, M, L);
+  if (moeq_workspace_bytes(L, M, mode) == 0) return MOEQ_ERR_UNSUPPORTED;
+  return mode == MOEQ_MODE_DECODE ? check_decode_shapes(L) : MOEQ_OK;
 }
 }  // namespace moeq
 

@@ -14,6 +14,14 @@ namespace moeq {
 moeq_status forward_arg_check(const moeq_layer* L, const uint16_t* x, int32_t M, float* y,
                               const float* residual, int32_t mode);
 
+// Whether the layer's shapes run in `mode` (resolved for M > 0 tokens); after
+// forward_arg_check (api.cu).
+moeq_status mode_check(const moeq_layer* L, int32_t M, int32_t mode);
+
+// Shape and format checks of one packed tensor with n_mats (>= 1)
+// addressable matrices (api.cu).
+moeq_status tensor_check(const moeq_qtensor* t, int64_t n_mats);
+
 // Diagnostics (api.cu): launch counter and the optional profiling events.
 void count_launches(int n);
 cudaError_t profile_mark(bool start, cudaStream_t st);

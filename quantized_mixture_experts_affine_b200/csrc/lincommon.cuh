@@ -1,0 +1,80 @@
+// Pieces shared by the linear kernels: code and token conversions to bf16
+// pairs, the epilogue.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "ops.h"
+
+namespace moeq {
+
+__device__ __forceinline__ float act_of(float v, int act) {
+  switch (act) {
+    case MOEQ_ACT_SILU: return v / (1.0f + expf(-v));
+    case MOEQ_ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+    case MOEQ_ACT_GELU_TANH:
+      return 0.5f * v * (1.0f + tanhf(0.79788456080286536f * (v + 0.044715f * v * v * v)));
+    case MOEQ_ACT_RELU: return v > 0.0f ? v : (v != v ? v : 0.0f);
+    case MOEQ_ACT_SIGMOID: return 1.0f / (1.0f + expf(-v));
+    default: return v;
+  }
+}
+
+__device__ __forceinline__ float load_out(const void* p, int type, int64_t at) {
+  return type == MOEQ_F32 ? reinterpret_cast<const float*>(p)[at]
+                          : bf16_bits_to_float(reinterpret_cast<const uint16_t*>(p)[at]);
+}
+__device__ __forceinline__ void store_out(void* p, int type, int64_t at, float v) {
+  if (type == MOEQ_F32) reinterpret_cast<float*>(p)[at] = v;
+  else reinterpret_cast<__nv_bfloat16*>(p)[at] = __float2bfloat16_rn(v);
+}
+
+// One output value from its finished sum.
+__device__ __forceinline__ void finish(const moeq_linear_args& a, int64_t m, int o, float v) {
+  if (a.bias) v += bf16_bits_to_float(a.bias[o]);
+  v = act_of(v, a.act);
+  if (a.mul) v *= load_out(a.mul, a.out_type, m * a.mul_stride + o);
+  if (a.residual) v += load_out(a.residual, a.out_type, m * a.residual_stride + o);
+  store_out(a.y, a.out_type, m * a.y_stride + o, v);
+}
+
+// ------------------------------------------------------------------ bf16 pairs
+// Four bytes (values 0..255, in order) as two bf16 pairs: 2^23 + c as fp32,
+// minus 2^23; the upper half of an integer below 256 is its bf16.
+__device__ __forceinline__ void bytes_to_bf16(uint32_t c, float bias, uint32_t& p0, uint32_t& p1) {
+  const float f0 = __uint_as_float(__byte_perm(c, 0x4B000000u, 0x7440u)) - bias;
+  const float f1 = __uint_as_float(__byte_perm(c, 0x4B000000u, 0x7441u)) - bias;
+  const float f2 = __uint_as_float(__byte_perm(c, 0x4B000000u, 0x7442u)) - bias;
+  const float f3 = __uint_as_float(__byte_perm(c, 0x4B000000u, 0x7443u)) - bias;
+  p0 = __byte_perm(__float_as_uint(f0), __float_as_uint(f1), 0x7632u);
+  p1 = __byte_perm(__float_as_uint(f2), __float_as_uint(f3), 0x7632u);
+}
+
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// Codes below 128, two in the low bits of each half of c: 128 + q is a bf16
+// with q in its mantissa.
+__device__ __forceinline__ uint32_t low_to_bf16(uint32_t c) {
+  return sub_bf16x2(c | 0x43004300u, 0x43004300u);
+}
+
+// Four E4M3 bytes as two bf16 pairs (exact).
+__device__ __forceinline__ void e4m3_to_bf16(uint32_t c, uint32_t& p0, uint32_t& p1) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t f16;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f16) : "h"((uint16_t)(c >> (16 * h))));
+    const __half2 v = *reinterpret_cast<const __half2*>(&f16);
+    const float2 f = __half22float2(v);
+    (h ? p1 : p0) = __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632u);
+  }
+}
+
+}  // namespace moeq

@@ -1,0 +1,31 @@
+// Launchers of the routing, norm and linear operators (k_route.cu, k_norm.cu,
+// k_linear.cu, k_lingemm.cu), called by ops_api.cu after its argument checks.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "moeq.h"
+
+namespace moeq {
+
+cudaError_t launch_route_groups(const moeq_routing& r, const void* logits, int logit_type,
+                                int64_t stride, const float* bias, int M, int32_t* idx, float* w,
+                                cudaStream_t st);
+
+cudaError_t launch_add_rmsnorm(const moeq_norm_args& n, int M, int H, cudaStream_t st);
+
+// One matrix of a packed tensor and the operands around it, as the linear
+// kernels read them.
+struct LinArgs {
+  const uint32_t* w;
+  const uint16_t* scales;  // MX FP4: uint8 exponents
+  const uint16_t* biases;
+  int out_dim, in_dim, bits, G, mx;
+  moeq_linear_args a;
+  int M;
+};
+
+cudaError_t launch_linear_small(const LinArgs& l, cudaStream_t st);
+
+}  // namespace moeq

@@ -127,3 +127,74 @@ def expert_ffn(L: DeviceLayer, x, idx, w, y=None, residual=None, ws=None,
         ws = Workspace(L, M, mode, x.device)
     moeq.moeq_expert_ffn(L.desc, x, M, idx, w, residual, y, ws.buf, ws.bytes, mode, stream)
     return y
+
+
+def _scratch(nbytes: int, device, stream):
+    """A workspace for one call, reusable by others once `stream` is past it."""
+    import torch
+    if isinstance(stream, torch.cuda.Stream):
+        with torch.cuda.stream(stream):
+            return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def route_groups(r: moeq.Routing, logits, bias=None, stream=None):
+    """Routing `r` of logits [M][E]; returns (idx, w)."""
+    import torch
+    M = logits.shape[0]
+    idx = torch.empty((M, r.top_k), dtype=torch.int32, device=logits.device)
+    w = torch.empty((M, r.top_k), dtype=torch.float32, device=logits.device)
+    moeq.moeq_route_groups(r, logits, idx, w, bias, stream)
+    return idx, w
+
+
+def add_rmsnorm(x, gamma, eps: float, residual=None, want_y: bool = True, q_dtype=None,
+                q_group: int = 0, stream=None):
+    """RMS norm of x + residual; returns (r, y, q, q_scales): the new residual
+    stream (None without a residual), the bf16 norm (with want_y) and its codes
+    in q_dtype (torch.int8 or torch.float8_e4m3fn) with their scales."""
+    import torch
+    M, H = x.shape
+    r = torch.empty_like(residual, memory_format=torch.contiguous_format) \
+        if residual is not None else None
+    y = torch.empty((M, H), dtype=torch.bfloat16, device=x.device) if want_y else None
+    q = qs = None
+    if q_dtype is not None:
+        q = torch.empty((M, H), dtype=q_dtype, device=x.device)
+        qs = torch.empty((M, -(-H // q_group) if q_group else 1), dtype=torch.float32,
+                         device=x.device)
+    moeq.moeq_add_rmsnorm(x, gamma, eps, residual, r, y, q, qs, q_group, stream)
+    return r, y, q, qs
+
+
+def linear(t: moeq.QTensor, x, out_dtype=None, expert: int = 0, x_scales=None, x_group: int = 0,
+           bias=None, act: int = moeq.ACT_NONE, mul=None, residual=None, y=None, ws=None,
+           stream=None):
+    """y = act(x W^T + bias) * mul + residual (out_dtype: fp32 or, by default,
+    bf16); returns y.  The workspace is allocated where none is given."""
+    import torch
+    M = x.shape[0]
+    if y is None:
+        y = torch.empty((M, t.out_dim), dtype=out_dtype or torch.bfloat16, device=x.device)
+    if ws is None:
+        need = moeq.moeq_linear_workspace_bytes(t, M, x.dtype, y.dtype)
+        if need:
+            ws = _scratch(need, x.device, stream)
+    moeq.moeq_linear(t, expert, x, y, x_scales, x_group, bias, act, mul, residual, ws, stream)
+    return y
+
+
+def layer_forward_routed(L: DeviceLayer, r: moeq.Routing, x, bias=None, residual=None,
+                         mode: int = moeq.MODE_AUTO, ws=None, stream=None):
+    """y = layer(x) under routing `r`; returns (y, idx, w).  ws: uint8 buffer of
+    moeq_routed_workspace_bytes."""
+    import torch
+    M = x.shape[0]
+    y = torch.empty((M, L.cfg.H), dtype=torch.float32, device=x.device)
+    idx = torch.empty((M, L.cfg.K), dtype=torch.int32, device=x.device)
+    w = torch.empty((M, L.cfg.K), dtype=torch.float32, device=x.device)
+    if ws is None:
+        ws = _scratch(moeq.moeq_routed_workspace_bytes(L.desc, M, mode), x.device, stream)
+    moeq.moeq_layer_forward_routed(L.desc, r, x, M, y, bias, residual, idx, w, ws, ws.numel(),
+                                   mode, stream)
+    return y, idx, w

@@ -28,7 +28,9 @@ EXPORTS = ("moeq_dequant", "moeq_qmv", "moeq_route_topk", "moeq_expert_ffn", "mo
            "moeq_set_profile_events", "moeq_launch_count", "moeq_layer_forward_static",
            "moeq_static_workspace_capacity", "moeq_selftest_wait_timeout",
            "moeq_layer_forward_norm", "moeq_cache_create", "moeq_cache_workspace_bytes",
-           "moeq_cache_forward", "moeq_cache_stats", "moeq_cache_destroy")
+           "moeq_cache_forward", "moeq_cache_stats", "moeq_cache_destroy",
+           "moeq_route_groups", "moeq_add_rmsnorm", "moeq_linear", "moeq_linear_workspace_bytes",
+           "moeq_layer_forward_routed", "moeq_routed_workspace_bytes")
 
 
 class MoeqError(RuntimeError):
@@ -52,6 +54,32 @@ class Layer(C.Structure):
                 ("sh_down", QTensor), ("sh_expert_gate", QTensor), ("hidden", C.c_int32),
                 ("inter", C.c_int32), ("n_experts", C.c_int32), ("top_k", C.c_int32),
                 ("renorm", C.c_int32), ("router_scale", C.c_float)]
+
+
+class Routing(C.Structure):
+    """moeq_routing."""
+    _fields_ = [("n_experts", C.c_int32), ("top_k", C.c_int32), ("score", C.c_int32),
+                ("n_groups", C.c_int32), ("topk_groups", C.c_int32), ("group_top", C.c_int32),
+                ("renorm", C.c_int32), ("router_scale", C.c_float), ("routed_scale", C.c_float)]
+
+
+class NormArgs(C.Structure):
+    """moeq_norm_args."""
+    _fields_ = [("x", C.c_void_p), ("x_type", C.c_int32), ("x_stride", C.c_int64),
+                ("residual", C.c_void_p), ("r_type", C.c_int32), ("r_stride", C.c_int64),
+                ("r_out", C.c_void_p), ("r_out_stride", C.c_int64), ("gamma", C.c_void_p),
+                ("eps", C.c_float), ("y", C.c_void_p), ("y_stride", C.c_int64),
+                ("q", C.c_void_p), ("q_type", C.c_int32), ("q_stride", C.c_int64),
+                ("q_scales", C.c_void_p), ("q_group", C.c_int32)]
+
+
+class LinearArgs(C.Structure):
+    """moeq_linear_args."""
+    _fields_ = [("x", C.c_void_p), ("x_type", C.c_int32), ("x_stride", C.c_int64),
+                ("x_scales", C.c_void_p), ("x_group", C.c_int32), ("bias", C.c_void_p),
+                ("act", C.c_int32), ("mul", C.c_void_p), ("mul_stride", C.c_int64),
+                ("residual", C.c_void_p), ("residual_stride", C.c_int64), ("y", C.c_void_p),
+                ("out_type", C.c_int32), ("y_stride", C.c_int64)]
 
 
 _P = C.c_void_p
@@ -88,9 +116,21 @@ _lib.moeq_version.restype = C.c_char_p
 _lib.moeq_set_profile_events.argtypes = [_P, _P]
 _lib.moeq_set_profile_events.restype = C.c_int
 _lib.moeq_launch_count.restype = C.c_uint64
+_lib.moeq_route_groups.argtypes = [C.POINTER(Routing), _P, C.c_int32, C.c_int64, _P, C.c_int32, _P,
+                                   _P, _P]
+_lib.moeq_add_rmsnorm.argtypes = [C.POINTER(NormArgs), C.c_int32, C.c_int32, _P]
+_lib.moeq_linear.argtypes = [C.POINTER(QTensor), C.c_int32, C.POINTER(LinearArgs), C.c_int32, _P,
+                             C.c_size_t, _P]
+_lib.moeq_linear_workspace_bytes.argtypes = [C.POINTER(QTensor), C.c_int32, C.c_int32, C.c_int32]
+_lib.moeq_linear_workspace_bytes.restype = C.c_size_t
+_lib.moeq_layer_forward_routed.argtypes = [C.POINTER(Layer), C.POINTER(Routing), _P, _P, C.c_int32,
+                                           _P, _P, _P, _P, _P, C.c_size_t, C.c_int32, _P]
+_lib.moeq_routed_workspace_bytes.argtypes = [C.POINTER(Layer), C.c_int32, C.c_int32]
+_lib.moeq_routed_workspace_bytes.restype = C.c_size_t
 for _f in ("moeq_dequant", "moeq_qmv", "moeq_route_topk", "moeq_expert_ffn", "moeq_layer_forward",
            "moeq_layer_forward_static", "moeq_device_status", "moeq_selftest_wait_timeout",
-           "moeq_layer_forward_norm"):
+           "moeq_layer_forward_norm", "moeq_route_groups", "moeq_add_rmsnorm", "moeq_linear",
+           "moeq_layer_forward_routed"):
     getattr(_lib, _f).restype = C.c_int
 
 
@@ -129,6 +169,54 @@ def _check(fn, rc):
 
 
 FMT_AFFINE, FMT_MXFP4 = 0, 1
+F32, BF16, I8, E4M3 = range(4)
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+ACT_NONE, ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_RELU, ACT_SIGMOID = range(6)
+_DTYPES = {}
+
+
+def dtype_code(dtype) -> int:
+    """moeq_dtype of a torch dtype."""
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.float32: F32, torch.bfloat16: BF16, torch.int8: I8,
+                        torch.float8_e4m3fn: E4M3})
+    try:
+        return _DTYPES[dtype]
+    except KeyError:
+        raise MoeqError(f"dtype {dtype}", ERR_UNSUPPORTED) from None
+
+
+def _on_current(name, t) -> None:
+    """Launches go to the current device: its tensors have to be there too."""
+    import torch
+    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {t.device}, not on the current CUDA device")
+
+
+def _rows(name, t, M, n, dtype=None, like=None):
+    """Row stride of a [M][n] tensor whose rows are contiguous, of the given
+    type, on the device of `like`; raises ValueError otherwise."""
+    if t.dim() != 2 or t.shape[0] != M or t.shape[1] != n or (n > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: expected [{M}][{n}] with contiguous rows, got "
+                         f"{tuple(t.shape)} with strides {t.stride()}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if like is not None and t.device != like.device:
+        raise ValueError(f"{name}: on {t.device}, expected {like.device}")
+    return t.stride(0) if M > 1 else n
+
+
+def _dense(name, t, shape, dtype, like):
+    """A contiguous tensor of the given shape and type on the device of `like`."""
+    if tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous() \
+            or t.device != like.device:
+        raise ValueError(f"{name}: expected contiguous {dtype} {shape} on {like.device}, got "
+                         f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+
+
+def _x_scales_shape(M, n, group):
+    return (M, -(-n // group)) if group else (M, 1)
 
 
 def qtensor(w, scales, biases, out_dim, in_dim, bits, group_size=64, n_mats=1,
@@ -155,6 +243,105 @@ def moeq_route_topk(logits, M: int, E: int, K: int, renorm: bool, router_scale: 
     _check("moeq_route_topk", _lib.moeq_route_topk(_ptr(logits), M, E, K, int(renorm),
                                                    float(router_scale), _ptr(idx), _ptr(w),
                                                    _stream(stream)))
+
+
+def routing(n_experts: int, top_k: int, score: int = SCORE_SOFTMAX, n_groups: int = 1,
+            topk_groups: int = 1, group_top: int = 1, renorm: bool = True,
+            router_scale: float = 1.0, routed_scale: float = 1.0) -> Routing:
+    return Routing(n_experts, top_k, score, n_groups, topk_groups, group_top, int(renorm),
+                   router_scale, routed_scale)
+
+
+def moeq_route_groups(r: Routing, logits, idx, w, bias=None, stream=None) -> None:
+    """Routing `r` of logits [M][E] (fp32 or bf16, rows may be strided) into
+    idx int32 [M][K] and w fp32 [M][K]; bias: fp32 [E] or None."""
+    import torch
+    _on_current("logits", logits)
+    M = logits.shape[0]
+    ld = _rows("logits", logits, M, r.n_experts)
+    _dense("idx", idx, (M, r.top_k), torch.int32, logits)
+    _dense("w", w, (M, r.top_k), torch.float32, logits)
+    if bias is not None:
+        _dense("bias", bias, (r.n_experts,), torch.float32, logits)
+    _check("moeq_route_groups",
+           _lib.moeq_route_groups(C.byref(r), logits.data_ptr(), dtype_code(logits.dtype), ld,
+                                  _ptr(bias), M, idx.data_ptr(), w.data_ptr(), _stream(stream)))
+
+
+def moeq_add_rmsnorm(x, gamma, eps: float, residual=None, r_out=None, y=None, q=None,
+                     q_scales=None, q_group: int = 0, stream=None) -> None:
+    """r = x + residual (into r_out), y = bf16 RMS norm of r with weights
+    gamma, q = its int8 or float8_e4m3fn codes with q_scales fp32 [M][1]
+    (q_group 0) or [M][ceil(H / 128)] (q_group 128)."""
+    import torch
+    _on_current("x", x)
+    M, H = x.shape
+    a = NormArgs(x.data_ptr(), dtype_code(x.dtype), _rows("x", x, M, H))
+    _dense("gamma", gamma, (H,), torch.bfloat16, x)
+    a.gamma, a.eps = gamma.data_ptr(), eps
+    if residual is not None:
+        a.residual, a.r_type = residual.data_ptr(), dtype_code(residual.dtype)
+        a.r_stride = _rows("residual", residual, M, H, None, x)
+    if r_out is not None:
+        a.r_out = r_out.data_ptr()
+        a.r_out_stride = _rows("r_out", r_out, M, H,
+                               None if residual is None else residual.dtype, x)
+    if y is not None:
+        a.y, a.y_stride = y.data_ptr(), _rows("y", y, M, H, torch.bfloat16, x)
+    if q is not None:
+        a.q, a.q_type, a.q_group = q.data_ptr(), dtype_code(q.dtype), q_group
+        a.q_stride = _rows("q", q, M, H, None, x)
+        if q_scales is not None:
+            _dense("q_scales", q_scales, _x_scales_shape(M, H, q_group), torch.float32, x)
+            a.q_scales = q_scales.data_ptr()
+    _check("moeq_add_rmsnorm", _lib.moeq_add_rmsnorm(C.byref(a), M, H, _stream(stream)))
+
+
+def moeq_linear_workspace_bytes(t: QTensor, M: int, x_dtype, out_dtype) -> int:
+    return int(_lib.moeq_linear_workspace_bytes(C.byref(t), M, dtype_code(x_dtype),
+                                                dtype_code(out_dtype)))
+
+
+def moeq_linear(t: QTensor, expert: int, x, y, x_scales=None, x_group: int = 0, bias=None,
+                act: int = ACT_NONE, mul=None, residual=None, ws=None, stream=None) -> None:
+    """y = act(x W^T + bias) * mul + residual with matrix `expert` of t.
+    x: bf16, int8 or float8_e4m3fn (with x_scales as moeq_add_rmsnorm writes
+    them) [M][in_dim]; y, mul, residual: fp32 or bf16 [M][out_dim]; ws: uint8
+    buffer of moeq_linear_workspace_bytes."""
+    import torch
+    _on_current("x", x)
+    M, n, o = x.shape[0], t.in_dim, t.out_dim
+    a = LinearArgs(x.data_ptr(), dtype_code(x.dtype), _rows("x", x, M, n))
+    if x_scales is not None:
+        _dense("x_scales", x_scales, _x_scales_shape(M, n, x_group), torch.float32, x)
+        a.x_scales, a.x_group = x_scales.data_ptr(), x_group
+    a.act, a.y, a.out_type = act, y.data_ptr(), dtype_code(y.dtype)
+    a.y_stride = _rows("y", y, M, o, None, x)
+    if bias is not None:
+        _dense("bias", bias, (o,), torch.bfloat16, x)
+        a.bias = bias.data_ptr()
+    if mul is not None:
+        a.mul, a.mul_stride = mul.data_ptr(), _rows("mul", mul, M, o, y.dtype, x)
+    if residual is not None:
+        a.residual = residual.data_ptr()
+        a.residual_stride = _rows("residual", residual, M, o, y.dtype, x)
+    _check("moeq_linear",
+           _lib.moeq_linear(C.byref(t), expert, C.byref(a), M, _ptr(ws),
+                            0 if ws is None else ws.numel(), _stream(stream)))
+
+
+def moeq_routed_workspace_bytes(L: Layer, M: int, mode: int = MODE_AUTO) -> int:
+    return int(_lib.moeq_routed_workspace_bytes(C.byref(L), M, mode))
+
+
+def moeq_layer_forward_routed(L: Layer, r: Routing, x, M: int, y, bias=None, residual=None,
+                              idx_out=None, w_out=None, ws=None, ws_bytes: int = 0,
+                              mode: int = MODE_AUTO, stream=None) -> None:
+    """moeq_layer_forward with routing `r` (and its balance bias)."""
+    _check("moeq_layer_forward_routed",
+           _lib.moeq_layer_forward_routed(C.byref(L), C.byref(r), _ptr(bias), _ptr(x), M, _ptr(y),
+                                          _ptr(residual), _ptr(idx_out), _ptr(w_out), _ptr(ws),
+                                          ws_bytes, mode, _stream(stream)))
 
 
 def moeq_workspace_bytes(L: Layer, M: int, mode: int = MODE_AUTO) -> int:
