@@ -40,6 +40,7 @@ static std::atomic<uint64_t> g_launches{0};
 static thread_local cudaEvent_t t_prof_start = nullptr, t_prof_stop = nullptr;
 
 namespace moeq {
+int* device_status_word() { return status_ptr(); }
 void count_launches(int n) { g_launches.fetch_add((uint64_t)n, std::memory_order_relaxed); }
 cudaError_t profile_mark(bool start, cudaStream_t st) {
   cudaEvent_t e = start ? t_prof_start : t_prof_stop;

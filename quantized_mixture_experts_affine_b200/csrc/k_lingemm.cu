@@ -1,0 +1,472 @@
+// Linear with many tokens: fp16 operands, tcgen05 products.
+//
+// Two launches.  The first (k_lin_prep) lays out the operands: token rows and
+// weight rows as fp16, each row times a power of two that brings its largest
+// magnitude to [2^13, 2^14), so that no bf16 value is out of fp16's range;
+// the powers are undone in the epilogue.  A token value of bf16 or 8 bits is
+// exact in fp16 unless it lies 2^-28 below its row's largest; a weight is
+// rounded once (relative 2^-11; y rounds by up to 2^-8 in bf16).  For an fp32
+// y the weights keep a second fp16 (22 bits), and so do tokens whose scales
+// change along the row; the product is then the sum of the parts' products.
+//
+// The second (k_lin_gemm) is a persistent GEMM on CTA pairs (cta_group::2):
+// D (256 rows of W) x (BN tokens) per pair in TMEM, two accumulators, operands
+// by TMA in the 128-byte swizzle.  W's rows are D's rows, so a lane of the
+// epilogue holds one output column o: bias and row power are one register, and
+// a warp's accesses to y, mul and the residual are 32 neighbours at any
+// alignment and stride.
+#include <cuda.h>
+
+#include "kernels.h"
+#include "lincommon.cuh"
+#include "tc.cuh"
+
+namespace moeq {
+namespace {
+
+constexpr int kTile = 128;  // rows of W per CTA (256 per pair)
+constexpr int kBK = 64;     // columns per stage (128 bytes)
+
+// ------------------------------------------------------------------ operand layout
+struct PrepArgs {
+  LinArgs l;
+  __half* x16;  // [x_parts][M][in_dim]
+  float* fx;    // [M]
+  __half* w16;  // [w_parts][out_dim][in_dim]
+  float* fw;    // [out_dim]
+  int x_parts, w_parts;
+  int x_blocks;  // first blocks of the grid: tokens; the others: weights
+};
+
+__device__ __forceinline__ float pow2(int k) { return __uint_as_float((uint32_t)(k + 127) << 23); }
+
+// Power of two that brings a largest magnitude to [2^13, 2^14) (for tiny
+// ones at most 2^126).
+__device__ __forceinline__ int lift_of(float largest) {
+  const int e = (int)(__float_as_uint(largest) >> 23) - 127;
+  return largest > 0.0f ? min(13 - e, 126) : 0;
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ float finite_abs(float v) {
+  v = fabsf(v);
+  return v < INFINITY ? v : 0.0f;
+}
+
+__device__ __forceinline__ uint32_t half_pair(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Eight values as fp16 at p, and what that rounding left at p + part.
+__device__ __forceinline__ void store_halves(__half* p, int64_t part, bool two,
+                                             const float (&v)[8]) {
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = half_pair(v[2 * i], v[2 * i + 1]);
+  *reinterpret_cast<uint4*>(p) = make_uint4(h[0], h[1], h[2], h[3]);
+  if (!two) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+    h[i] = half_pair(v[2 * i] - f.x, v[2 * i + 1] - f.y);
+  }
+  *reinterpret_cast<uint4*>(p + part) = make_uint4(h[0], h[1], h[2], h[3]);
+}
+
+__device__ __forceinline__ void load_x8(const void* row, int type, int c0, float (&v)[8]) {
+  if (type == MOEQ_BF16) {
+    const uint4 w = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(row) + c0);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(u[i] << 16);
+      v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+    return;
+  }
+  const uint2 w = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint8_t*>(row) + c0);
+  const uint32_t u[2] = {w.x, w.y};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (type == MOEQ_I8) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[4 * i + j] = (float)(int8_t)(u[i] >> (8 * j));
+    } else {
+      uint32_t p0, p1;
+      e4m3_to_bf16(u[i], p0, p1);
+      v[4 * i] = __uint_as_float(p0 << 16);
+      v[4 * i + 1] = __uint_as_float(p0 & 0xFFFF0000u);
+      v[4 * i + 2] = __uint_as_float(p1 << 16);
+      v[4 * i + 3] = __uint_as_float(p1 & 0xFFFF0000u);
+    }
+  }
+}
+
+// Eight codes from column c0 (a multiple of 8) of a packed row as floats
+// (MX FP4: the element values).
+__device__ __forceinline__ void load_codes8(const uint32_t* row, int bits, bool mx, int c0,
+                                            float (&v)[8]) {
+  uint32_t lo, hi = 0u;  // the 8 * bits bits of the run
+  if (bits == 8) {
+    const uint2 w = *reinterpret_cast<const uint2*>(row + c0 / 4);
+    lo = w.x;
+    hi = w.y;
+  } else if (bits == 4) {
+    lo = row[c0 / 8];
+  } else if (bits == 2) {
+    lo = reinterpret_cast<const uint16_t*>(row)[c0 / 8];
+  } else {
+    // 3, 5, 6 bits: the run starts on a byte; it reaches into one more word
+    // at most, unless it ends inside its first
+    const int bit = c0 / 8 * 8 * bits, off = bit & 31, n = 8 * bits;
+    const uint32_t* p = row + (bit >> 5);
+    const uint32_t a = p[0], b = off + n > 32 ? p[1] : 0u, c = off + n > 64 ? p[2] : 0u;
+    lo = __funnelshift_r(a, b, off);
+    hi = __funnelshift_r(b, c, off);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint64_t run = ((uint64_t)hi << 32) | lo;
+    const uint32_t q = (uint32_t)(run >> (i * bits)) & ((1u << bits) - 1u);
+    if (mx) {
+      const uint32_t e = (q >> 1) & 3u, m = q & 1u;
+      const float mag = e ? (1.0f + 0.5f * m) * (float)(1u << (e - 1u)) : 0.5f * m;
+      v[i] = (q & 8u) ? -mag : mag;
+    } else {
+      v[i] = (float)q;
+    }
+  }
+}
+
+// One warp per row.
+__global__ void __launch_bounds__(256) k_lin_prep(const __grid_constant__ PrepArgs p) {
+  tc::grid_dep_launch();
+  const LinArgs& l = p.l;
+  const int lane = threadIdx.x & 31, K = l.in_dim;
+  if ((int)blockIdx.x < p.x_blocks) {
+    const int64_t m = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (m >= l.M) return;
+    const int type = l.a.x_type;
+    const char* row =
+        reinterpret_cast<const char*>(l.a.x) + m * l.a.x_stride * (type == MOEQ_BF16 ? 2 : 1);
+    const bool by128 = type != MOEQ_BF16 && l.a.x_group == 128;
+    const float* xs = l.a.x_scales + m * (by128 ? (K + 127) / 128 : 1);
+    __half* out = p.x16 + m * K;
+    const int64_t part = (int64_t)l.M * K;
+    float f = 1.0f;
+    if (type != MOEQ_BF16 && !by128) {
+      // whole numbers and e4m3 values are fp16 values as they are
+      if (lane == 0) p.fx[m] = xs[0];
+    } else {
+      float largest = 0.0f;
+      for (int c = lane * 8; c < K; c += 256) {
+        float v[8];
+        load_x8(row, type, c, v);
+        const float s = by128 ? xs[c >> 7] : 1.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) largest = fmaxf(largest, finite_abs(v[j] * s));
+      }
+      const int k = lift_of(warp_max(largest));
+      f = pow2(k);
+      if (lane == 0) p.fx[m] = pow2(-k);
+    }
+    for (int c = lane * 8; c < K; c += 256) {
+      float v[8];
+      load_x8(row, type, c, v);
+      const float s = by128 ? xs[c >> 7] : 1.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = (v[j] * s) * f;
+      store_halves(out + c, part, p.x_parts == 2, v);
+    }
+    return;
+  }
+  const int64_t o = ((int64_t)blockIdx.x - p.x_blocks) * 8 + (threadIdx.x >> 5);
+  if (o >= l.out_dim) return;
+  const int groups = K / l.G, shift = l.G == 32 ? 5 : l.G == 64 ? 6 : 7;
+  const uint32_t* row = l.w + o * ((int64_t)K * l.bits / 32);
+  const uint16_t* sc = l.scales + o * groups;
+  const uint8_t* ex = reinterpret_cast<const uint8_t*>(l.scales) + o * groups;
+  const uint16_t* bi = l.mx ? nullptr : l.biases + o * groups;
+  const float qmax = (float)((1u << l.bits) - 1u);
+  float largest = 0.0f;
+  for (int g = lane; g < groups; g += 32)
+    largest = fmaxf(largest,
+                    l.mx ? finite_abs(6.0f * mx_scale(ex[g]))
+                         : finite_abs(fabsf(bf16_bits_to_float(sc[g])) * qmax +
+                                      fabsf(bf16_bits_to_float(bi[g]))));
+  const int k = lift_of(warp_max(largest));
+  const float f = pow2(k);
+  if (lane == 0) p.fw[o] = pow2(-k);
+  __half* out = p.w16 + o * K;
+  for (int c = lane * 8; c < K; c += 256) {
+    float v[8];
+    load_codes8(row, l.bits, l.mx, c, v);
+    const int g = c >> shift;
+    const float s = l.mx ? mx_scale(ex[g]) : bf16_bits_to_float(sc[g]);
+    const float b = l.mx ? 0.0f : bf16_bits_to_float(bi[g]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __fmaf_rn(v[j], s, b) * f;
+    store_halves(out + c, (int64_t)l.out_dim * K, p.w_parts == 2, v);
+  }
+}
+
+// ------------------------------------------------------------------ GEMM
+struct GemmArgs {
+  CUtensorMap tm_w, tm_x;  // [part][row][column], boxes of 64 columns
+  LinArgs l;
+  const float* fx;
+  const float* fw;
+  int k_blocks;   // 64-column blocks of one product
+  int products;   // 1: w x; 2: + (rest of w) x; 3: + w (rest of x)
+  int tiles_o, tiles_m;
+  int* status;
+};
+
+template <int BN>
+struct GemmSmem {
+  static constexpr uint32_t A = kTile * 128, B = BN / 2 * 128;
+  static constexpr int STAGES = BN == 256 ? 6 : 8;
+  static constexpr uint32_t BYTES = STAGES * (A + B) + 1024;
+};
+
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* tmap, int x, int y,
+                                                 int z, uint32_t bar_cluster) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar_cluster)
+      : "memory");
+}
+
+// Warps 0: TMA, 1: MMA (rank 0), 2: TMEM; 4..11: epilogue.
+template <int BN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
+    k_lin_gemm(const __grid_constant__ GemmArgs a) {
+  using S = GemmSmem<BN>;
+  constexpr int ST = S::STAGES;
+  extern __shared__ uint8_t dyn[];
+  __shared__ uint64_t full[ST], empty[ST], tmem_full[2], tmem_empty[2];
+  __shared__ uint32_t tmem_holder;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = tc::cluster_ctarank();
+  const uint32_t base = (tc::smem_u32(dyn) + 1023u) & ~1023u;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ST; ++i) {
+      tc::mbar_init(&full[i], 1);
+      tc::mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&tmem_full[i], 1);
+      tc::mbar_init(&tmem_empty[i], 16);  // eight warps of both CTAs
+    }
+    tc::fence_mbar_init();
+  }
+  if (warp == 2) {
+    tc::tmem_alloc_pair(&tmem_holder, 2 * BN < 32 ? 32 : 2 * BN);
+    tc::tmem_relinquish_pair();
+  }
+  tc::tc_fence_before();
+  tc::cluster_sync();
+  tc::tc_fence_after();
+  const uint32_t tmem = tmem_holder;
+  tc::grid_dep_wait();
+
+  const int unit0 = blockIdx.x >> 1, units = gridDim.x >> 1;
+  const int items = a.tiles_o * a.tiles_m, KB = a.k_blocks;
+
+  if (warp == 0) {
+    uint32_t it = 0;
+    for (int item = unit0; item < items; item += units) {
+      const int o0 = item % a.tiles_o * (2 * kTile) + (int)rank * kTile;
+      const int m0 = item / a.tiles_o * BN + (int)rank * (BN / 2);
+      for (int prod = 0; prod < a.products; ++prod)
+        for (int kb = 0; kb < KB; ++kb, ++it) {
+          const uint32_t s = it % ST, ph = (it / ST) & 1u;
+          if (!tc::mbar_wait(&empty[s], ph ^ 1u, a.status)) goto done;
+          if (lane == 0) {
+            const uint32_t bar = tc::mapa_shared(tc::smem_u32(&full[s]), 0);
+            const uint32_t at = base + s * (S::A + S::B);
+            if (rank == 0) tc::mbar_arrive_expect_tx(&full[s], 2 * (S::A + S::B));
+            tma_load_3d_pair(at, &a.tm_w, kb * kBK, o0, prod == 1 ? 1 : 0, bar);
+            tma_load_3d_pair(at + S::A, &a.tm_x, kb * kBK, m0, prod == 2 ? 1 : 0, bar);
+          }
+          __syncwarp();
+        }
+    }
+    // every release of this CTA's stages has landed before it may exit
+    for (int j = 0; j < ST; ++j, ++it)
+      if (!tc::mbar_wait(&empty[it % ST], ((it / ST) & 1u) ^ 1u, a.status)) goto done;
+  } else if (warp == 1 && rank == 0) {
+    constexpr uint32_t IDESC = tc::idesc_f16_f32(2 * kTile, BN);
+    const int n = KB * a.products;
+    uint32_t it = 0, tile = 0;
+    for (int item = unit0; item < items; item += units, ++tile) {
+      const uint32_t acc = tile & 1u;
+      if (!tc::mbar_wait(&tmem_empty[acc], ((tile >> 1) & 1u) ^ 1u, a.status)) goto done;
+      tc::tc_fence_after();
+      const uint32_t d = tmem + acc * BN;
+      for (int kb = 0; kb < n; ++kb, ++it) {
+        const uint32_t s = it % ST;
+        if (!tc::mbar_wait(&full[s], (it / ST) & 1u, a.status)) goto done;
+        tc::tc_fence_after();
+        if (lane == 0) {
+          const uint32_t at = base + s * (S::A + S::B);
+#pragma unroll
+          for (int kk = 0; kk < kBK / 16; ++kk)
+            tc::mma_f16_pair(d, tc::sw128_kmajor_desc(at + kk * 32),
+                             tc::sw128_kmajor_desc(at + S::A + kk * 32), IDESC, (kb | kk) != 0);
+          tc::mma_commit_pair(&empty[s], 3);
+        }
+        __syncwarp();
+      }
+      if (lane == 0) tc::mma_commit_pair(&tmem_full[acc], 3);
+      __syncwarp();
+    }
+  } else if (warp >= 4) {
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    uint32_t tile = 0;
+    for (int item = unit0; item < items; item += units, ++tile) {
+      const uint32_t acc = tile & 1u;
+      const int o = item % a.tiles_o * (2 * kTile) + (int)rank * kTile + q * 32 + lane;
+      const int m0 = item / a.tiles_o * BN;
+      const bool live = o < a.l.out_dim;
+      const float fw = live ? a.fw[o] : 0.0f;
+      const float bias =
+          live && a.l.a.bias ? bf16_bits_to_float(a.l.a.bias[o]) : 0.0f;
+      if (!tc::mbar_wait(&tmem_full[acc], (tile >> 1) & 1u, a.status)) goto done;
+      tc::tc_fence_after();
+#pragma unroll 1
+      for (int c0 = half * (BN / 2); c0 < (half + 1) * (BN / 2); c0 += 32) {
+        const int nm = min(32, a.l.M - (m0 + c0));
+        if (nm <= 0) break;
+        uint32_t v[32];
+        tc::tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + acc * BN + c0, v);
+        const float fx = lane < nm ? a.fx[m0 + c0 + lane] : 0.0f;
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const float f = __shfl_sync(0xffffffffu, fx, j);
+          if (j < nm && live) {
+            const int64_t m = m0 + c0 + j;
+            float y = act_of(__uint_as_float(v[j]) * fw * f + bias, a.l.a.act);
+            if (a.l.a.mul) y *= load_out(a.l.a.mul, a.l.a.out_type, m * a.l.a.mul_stride + o);
+            if (a.l.a.residual)
+              y += load_out(a.l.a.residual, a.l.a.out_type, m * a.l.a.residual_stride + o);
+            store_out(a.l.a.y, a.l.a.out_type, m * a.l.a.y_stride + o, y);
+          }
+        }
+      }
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive_cluster(tc::mapa_shared(tc::smem_u32(&tmem_empty[acc]), 0));
+    }
+  }
+done:
+  tc::tc_fence_before();
+  tc::cluster_sync();
+  if (warp == 2) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc_pair(tmem, 2 * BN < 32 ? 32 : 2 * BN);
+  }
+}
+
+// [parts][rows][cols] fp16, boxes of 64 columns x `box` rows, 128-byte swizzle;
+// what lies outside reads as zeros.
+bool half_map(CUtensorMap* m, const __half* p, int cols, int64_t rows, int parts, int box) {
+  auto fn = reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(tensor_map_encoder());
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)parts};
+  const cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)cols * 2 * rows};
+  const cuuint32_t boxes[3] = {kBK, (cuuint32_t)box, 1};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<__half*>(p), dims, strides,
+                  boxes, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+struct Layout {
+  size_t x16, fx, w16, fw, total;
+};
+Layout layout(int64_t M, int64_t K, int64_t O, int xp, int wp) {
+  Layout o;
+  o.x16 = 0;
+  o.fx = o.x16 + up256((size_t)(M * K) * 2 * xp);
+  o.w16 = o.fx + up256((size_t)M * 4);
+  o.fw = o.w16 + up256((size_t)(O * K) * 2 * wp);
+  o.total = o.fw + up256((size_t)O * 4);
+  return o;
+}
+int x_parts_of(int x_type, int x_group, int out_type) {
+  return out_type == MOEQ_F32 && x_type != MOEQ_BF16 && x_group == 128 ? 2 : 1;
+}
+
+template <int BN>
+cudaError_t run_gemm(GemmArgs& g, int sms, cudaStream_t st) {
+  constexpr uint32_t bytes = GemmSmem<BN>::BYTES;
+  cudaError_t e = cudaFuncSetAttribute(k_lin_gemm<BN>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e != cudaSuccess) return e;
+  const int64_t items = (int64_t)g.tiles_o * g.tiles_m;
+  const int64_t units = items < sms / 2 ? items : sms / 2;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3((unsigned)(2 * units));
+  c.blockDim = dim3(384);
+  c.dynamicSmemBytes = bytes;
+  c.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, k_lin_gemm<BN>, g);
+}
+
+}  // namespace
+
+size_t linear_gemm_workspace(const moeq_qtensor& t, int M, int x_type, int out_type) {
+  return layout(M, t.in_dim, t.out_dim, x_parts_of(x_type, 128, out_type),
+                out_type == MOEQ_F32 ? 2 : 1)
+      .total;
+}
+
+cudaError_t launch_linear_gemm(const LinArgs& l, void* ws, int* status, cudaStream_t st) {
+  const int sms = sm_count();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  PrepArgs p;
+  p.l = l;
+  p.x_parts = x_parts_of(l.a.x_type, l.a.x_group, l.a.out_type);
+  p.w_parts = l.a.out_type == MOEQ_F32 ? 2 : 1;
+  const Layout lay = layout(l.M, l.in_dim, l.out_dim, p.x_parts, p.w_parts);
+  char* base = (char*)ws;
+  p.x16 = (__half*)(base + lay.x16);
+  p.fx = (float*)(base + lay.fx);
+  p.w16 = (__half*)(base + lay.w16);
+  p.fw = (float*)(base + lay.fw);
+  p.x_blocks = (l.M + 7) / 8;
+  GemmArgs g;
+  const int bn = l.M > 128 ? 256 : 128;
+  if (!half_map(&g.tm_w, p.w16, l.in_dim, l.out_dim, p.w_parts, kTile) ||
+      !half_map(&g.tm_x, p.x16, l.in_dim, l.M, p.x_parts, bn / 2))
+    return cudaErrorNotSupported;
+  g.l = l;
+  g.fx = p.fx;
+  g.fw = p.fw;
+  g.k_blocks = (l.in_dim + kBK - 1) / kBK;
+  g.products = p.w_parts + p.x_parts - 1;
+  g.tiles_o = (l.out_dim + 2 * kTile - 1) / (2 * kTile);
+  g.tiles_m = (l.M + bn - 1) / bn;
+  g.status = status;
+  k_lin_prep<<<p.x_blocks + (l.out_dim + 7) / 8, 256, 0, st>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return bn == 256 ? run_gemm<256>(g, sms, st) : run_gemm<128>(g, sms, st);
+}
+
+}  // namespace moeq

@@ -725,6 +725,8 @@ moeq_status check_prefill(const moeq_layer* L) {
 
 }  // namespace
 
+void* tensor_map_encoder() { return reinterpret_cast<void*>(encode_fn()); }
+
 int sm_count() {
   static std::atomic<int> sms[kMaxDevices];
   int dev;

@@ -22,6 +22,11 @@ moeq_status mode_check(const moeq_layer* L, int32_t M, int32_t mode);
 // addressable matrices (api.cu).
 moeq_status tensor_check(const moeq_qtensor* t, int64_t n_mats);
 
+// cuTensorMapEncodeTiled, or null where the driver does not have it
+// (k_prefill.cu); the current device's status word (api.cu).
+void* tensor_map_encoder();
+int* device_status_word();
+
 // Diagnostics (api.cu): launch counter and the optional profiling events.
 void count_launches(int n);
 cudaError_t profile_mark(bool start, cudaStream_t st);

@@ -28,4 +28,8 @@ struct LinArgs {
 
 cudaError_t launch_linear_small(const LinArgs& l, cudaStream_t st);
 
+// Many tokens: two launches (operand layout, GEMM) over a workspace.
+size_t linear_gemm_workspace(const moeq_qtensor& t, int M, int x_type, int out_type);
+cudaError_t launch_linear_gemm(const LinArgs& l, void* ws, int* status, cudaStream_t st);
+
 }  // namespace moeq

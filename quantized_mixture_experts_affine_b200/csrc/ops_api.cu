@@ -78,6 +78,9 @@ LinArgs lin_args(const moeq_qtensor& t, int expert, const moeq_linear_args& a, i
   return l;
 }
 
+// Up to here the tokens go through the code products (measured in k_linear.cu).
+constexpr int kSmallTokens = 64;
+
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 }  // namespace
@@ -127,7 +130,11 @@ MOEQ_API moeq_status moeq_add_rmsnorm(const moeq_norm_args* n, int32_t M, int32_
 
 MOEQ_API size_t moeq_linear_workspace_bytes(const moeq_qtensor* t, int32_t M, int32_t x_type,
                                             int32_t out_type) {
-  return 0;
+  const bool x8 = x_type == MOEQ_I8 || x_type == MOEQ_E4M3;
+  if (check_matrix(t, 0) != MOEQ_OK || M <= kSmallTokens || !(x8 || x_type == MOEQ_BF16) ||
+      !float_type(out_type))
+    return 0;
+  return linear_gemm_workspace(*t, M, x_type, out_type);
 }
 
 MOEQ_API moeq_status moeq_linear(const moeq_qtensor* t, int32_t expert, const moeq_linear_args* a,
@@ -153,8 +160,12 @@ MOEQ_API moeq_status moeq_linear(const moeq_qtensor* t, int32_t expert, const mo
     if (!ws || ws_bytes < need) return MOEQ_ERR_WORKSPACE;
     if (!on(ws, 256)) return MOEQ_ERR_ALIGNMENT;
   }
+  if (sm_count() <= 0) return MOEQ_ERR_CUDA;  // no current device to size launches for
   const LinArgs l = lin_args(*t, expert, *a, M);
-  return launched(launch_linear_small(l, (cudaStream_t)stream));
+  if (M <= kSmallTokens) return launched(launch_linear_small(l, (cudaStream_t)stream));
+  int* status = device_status_word();
+  if (!status) return MOEQ_ERR_CUDA;
+  return launched(launch_linear_gemm(l, ws, status, (cudaStream_t)stream), 2);
 }
 
 // ------------------------------------------------------------------ the layer with such a router

@@ -157,7 +157,7 @@ def _ptr(t):
 def _stream(s):
     if s is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -187,32 +187,35 @@ def dtype_code(dtype) -> int:
         raise MoeqError(f"dtype {dtype}", ERR_UNSUPPORTED) from None
 
 
-def _on_current(name, t) -> None:
+def _device(name, t) -> int:
     """Launches go to the current device: its tensors have to be there too."""
     import torch
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+    d = t.get_device()
+    if d < 0 or d != torch.cuda.current_device():
         raise ValueError(f"{name}: on {t.device}, not on the current CUDA device")
+    return d
 
 
-def _rows(name, t, M, n, dtype=None, like=None):
+def _rows(name, t, M, n, dtype=None, device=None):
     """Row stride of a [M][n] tensor whose rows are contiguous, of the given
-    type, on the device of `like`; raises ValueError otherwise."""
-    if t.dim() != 2 or t.shape[0] != M or t.shape[1] != n or (n > 1 and t.stride(1) != 1):
+    type and on the given device; raises ValueError otherwise."""
+    if t.shape != (M, n) or (n > 1 and t.stride(1) != 1):
         raise ValueError(f"{name}: expected [{M}][{n}] with contiguous rows, got "
                          f"{tuple(t.shape)} with strides {t.stride()}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
-    if like is not None and t.device != like.device:
-        raise ValueError(f"{name}: on {t.device}, expected {like.device}")
+    if device is not None and t.get_device() != device:
+        raise ValueError(f"{name}: on {t.device}, not on CUDA device {device}")
     return t.stride(0) if M > 1 else n
 
 
-def _dense(name, t, shape, dtype, like):
-    """A contiguous tensor of the given shape and type on the device of `like`."""
-    if tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous() \
-            or t.device != like.device:
-        raise ValueError(f"{name}: expected contiguous {dtype} {shape} on {like.device}, got "
+def _dense(name, t, shape, dtype, device):
+    """Address of a contiguous tensor of the given shape, type and device."""
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous() \
+            or t.get_device() != device:
+        raise ValueError(f"{name}: expected contiguous {dtype} {shape} on device {device}, got "
                          f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+    return t.data_ptr()
 
 
 def _x_scales_shape(M, n, group):
@@ -256,16 +259,15 @@ def moeq_route_groups(r: Routing, logits, idx, w, bias=None, stream=None) -> Non
     """Routing `r` of logits [M][E] (fp32 or bf16, rows may be strided) into
     idx int32 [M][K] and w fp32 [M][K]; bias: fp32 [E] or None."""
     import torch
-    _on_current("logits", logits)
-    M = logits.shape[0]
-    ld = _rows("logits", logits, M, r.n_experts)
-    _dense("idx", idx, (M, r.top_k), torch.int32, logits)
-    _dense("w", w, (M, r.top_k), torch.float32, logits)
-    if bias is not None:
-        _dense("bias", bias, (r.n_experts,), torch.float32, logits)
+    dev = _device("logits", logits)
+    M, E, K = logits.shape[0], r.n_experts, r.top_k
     _check("moeq_route_groups",
-           _lib.moeq_route_groups(C.byref(r), logits.data_ptr(), dtype_code(logits.dtype), ld,
-                                  _ptr(bias), M, idx.data_ptr(), w.data_ptr(), _stream(stream)))
+           _lib.moeq_route_groups(
+               C.byref(r), logits.data_ptr(), dtype_code(logits.dtype),
+               _rows("logits", logits, M, E),
+               None if bias is None else _dense("bias", bias, (E,), torch.float32, dev), M,
+               _dense("idx", idx, (M, K), torch.int32, dev),
+               _dense("w", w, (M, K), torch.float32, dev), _stream(stream)))
 
 
 def moeq_add_rmsnorm(x, gamma, eps: float, residual=None, r_out=None, y=None, q=None,
@@ -274,26 +276,25 @@ def moeq_add_rmsnorm(x, gamma, eps: float, residual=None, r_out=None, y=None, q=
     gamma, q = its int8 or float8_e4m3fn codes with q_scales fp32 [M][1]
     (q_group 0) or [M][ceil(H / 128)] (q_group 128)."""
     import torch
-    _on_current("x", x)
+    dev = _device("x", x)
     M, H = x.shape
     a = NormArgs(x.data_ptr(), dtype_code(x.dtype), _rows("x", x, M, H))
-    _dense("gamma", gamma, (H,), torch.bfloat16, x)
-    a.gamma, a.eps = gamma.data_ptr(), eps
+    a.gamma, a.eps = _dense("gamma", gamma, (H,), torch.bfloat16, dev), eps
     if residual is not None:
         a.residual, a.r_type = residual.data_ptr(), dtype_code(residual.dtype)
-        a.r_stride = _rows("residual", residual, M, H, None, x)
+        a.r_stride = _rows("residual", residual, M, H, None, dev)
     if r_out is not None:
         a.r_out = r_out.data_ptr()
         a.r_out_stride = _rows("r_out", r_out, M, H,
-                               None if residual is None else residual.dtype, x)
+                               None if residual is None else residual.dtype, dev)
     if y is not None:
-        a.y, a.y_stride = y.data_ptr(), _rows("y", y, M, H, torch.bfloat16, x)
+        a.y, a.y_stride = y.data_ptr(), _rows("y", y, M, H, torch.bfloat16, dev)
     if q is not None:
         a.q, a.q_type, a.q_group = q.data_ptr(), dtype_code(q.dtype), q_group
-        a.q_stride = _rows("q", q, M, H, None, x)
+        a.q_stride = _rows("q", q, M, H, None, dev)
         if q_scales is not None:
-            _dense("q_scales", q_scales, _x_scales_shape(M, H, q_group), torch.float32, x)
-            a.q_scales = q_scales.data_ptr()
+            a.q_scales = _dense("q_scales", q_scales, _x_scales_shape(M, H, q_group),
+                                torch.float32, dev)
     _check("moeq_add_rmsnorm", _lib.moeq_add_rmsnorm(C.byref(a), M, H, _stream(stream)))
 
 
@@ -309,25 +310,29 @@ def moeq_linear(t: QTensor, expert: int, x, y, x_scales=None, x_group: int = 0, 
     them) [M][in_dim]; y, mul, residual: fp32 or bf16 [M][out_dim]; ws: uint8
     buffer of moeq_linear_workspace_bytes."""
     import torch
-    _on_current("x", x)
+    dev = _device("x", x)
     M, n, o = x.shape[0], t.in_dim, t.out_dim
     a = LinearArgs(x.data_ptr(), dtype_code(x.dtype), _rows("x", x, M, n))
     if x_scales is not None:
-        _dense("x_scales", x_scales, _x_scales_shape(M, n, x_group), torch.float32, x)
-        a.x_scales, a.x_group = x_scales.data_ptr(), x_group
+        a.x_scales = _dense("x_scales", x_scales, _x_scales_shape(M, n, x_group), torch.float32,
+                            dev)
+        a.x_group = x_group
     a.act, a.y, a.out_type = act, y.data_ptr(), dtype_code(y.dtype)
-    a.y_stride = _rows("y", y, M, o, None, x)
+    a.y_stride = _rows("y", y, M, o, None, dev)
     if bias is not None:
-        _dense("bias", bias, (o,), torch.bfloat16, x)
-        a.bias = bias.data_ptr()
+        a.bias = _dense("bias", bias, (o,), torch.bfloat16, dev)
     if mul is not None:
-        a.mul, a.mul_stride = mul.data_ptr(), _rows("mul", mul, M, o, y.dtype, x)
+        a.mul, a.mul_stride = mul.data_ptr(), _rows("mul", mul, M, o, y.dtype, dev)
     if residual is not None:
         a.residual = residual.data_ptr()
-        a.residual_stride = _rows("residual", residual, M, o, y.dtype, x)
-    _check("moeq_linear",
-           _lib.moeq_linear(C.byref(t), expert, C.byref(a), M, _ptr(ws),
-                            0 if ws is None else ws.numel(), _stream(stream)))
+        a.residual_stride = _rows("residual", residual, M, o, y.dtype, dev)
+    n_ws = 0
+    if ws is not None:
+        n_ws = ws.numel() * ws.element_size()
+        if ws.get_device() != dev or not ws.is_contiguous():
+            raise ValueError(f"ws: expected contiguous on device {dev}, got {ws.device}")
+    _check("moeq_linear", _lib.moeq_linear(C.byref(t), expert, C.byref(a), M, _ptr(ws), n_ws,
+                                           _stream(stream)))
 
 
 def moeq_routed_workspace_bytes(L: Layer, M: int, mode: int = MODE_AUTO) -> int:

@@ -153,6 +153,6 @@ def test_binding_checks_shapes_and_devices():
     with pytest.raises(ValueError):
         moeq._rows("x", x.t(), 256, 2)
     with pytest.raises(ValueError):
-        moeq._rows("x", x, 2, 256, torch.float32)
+        moeq._rows("x", x, 2, 256, torch.float32, -1)
     with pytest.raises(ValueError):
-        moeq._dense("w", x[:, ::2], (2, 128), torch.bfloat16, x)
+        moeq._dense("w", x[:, ::2], (2, 128), torch.bfloat16, -1)
