@@ -15,17 +15,12 @@
 // epilogue holds one output column o: bias and row power are one register, and
 // a warp's accesses to y, mul and the residual are 32 neighbours at any
 // alignment and stride.
-#include <cuda.h>
-
-#include "kernels.h"
-#include "lincommon.cuh"
-#include "tc.cuh"
+#include "lingemm.cuh"
 
 namespace moeq {
 namespace {
 
 constexpr int kTile = 128;  // rows of W per CTA (256 per pair)
-constexpr int kBK = 64;     // columns per stage (128 bytes)
 
 // ------------------------------------------------------------------ operand layout
 struct PrepArgs {
@@ -37,30 +32,6 @@ struct PrepArgs {
   int x_parts, w_parts;
   int x_blocks;  // first blocks of the grid: tokens; the others: weights
 };
-
-__device__ __forceinline__ float pow2(int k) { return __uint_as_float((uint32_t)(k + 127) << 23); }
-
-// Power of two that brings a largest magnitude to [2^13, 2^14) (for tiny
-// ones at most 2^126).
-__device__ __forceinline__ int lift_of(float largest) {
-  const int e = (int)(__float_as_uint(largest) >> 23) - 127;
-  return largest > 0.0f ? min(13 - e, 126) : 0;
-}
-
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
-__device__ __forceinline__ float finite_abs(float v) {
-  v = fabsf(v);
-  return v < INFINITY ? v : 0.0f;
-}
-
-__device__ __forceinline__ uint32_t half_pair(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 
 // Eight values as fp16 at p, and what that rounding left at p + part.
 __device__ __forceinline__ void store_halves(__half* p, int64_t part, bool two,
@@ -348,18 +319,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
         tc::tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + acc * BN + c0, v);
         const float fx = lane < nm ? a.fx[m0 + c0 + lane] : 0.0f;
         tc::tmem_wait_ld();
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float f = __shfl_sync(0xffffffffu, fx, j);
-          if (j < nm && live) {
-            const int64_t m = m0 + c0 + j;
-            float y = act_of(__uint_as_float(v[j]) * fw * f + bias, a.l.a.act);
-            if (a.l.a.mul) y *= load_out(a.l.a.mul, a.l.a.out_type, m * a.l.a.mul_stride + o);
-            if (a.l.a.residual)
-              y += load_out(a.l.a.residual, a.l.a.out_type, m * a.l.a.residual_stride + o);
-            store_out(a.l.a.y, a.l.a.out_type, m * a.l.a.y_stride + o, y);
-          }
-        }
+        const int oc = min(o, a.l.out_dim - 1);
+        if (a.l.a.out_type == MOEQ_F32)
+          finish<float, 32>(a.l.a, m0 + c0, nm, oc, live, fw, bias, fx, v);
+        else
+          finish<uint16_t, 32>(a.l.a, m0 + c0, nm, oc, live, fw, bias, fx, v);
       }
       tc::tc_fence_before();
       __syncwarp();
@@ -375,19 +339,8 @@ done:
   }
 }
 
-// [parts][rows][cols] fp16, boxes of 64 columns x `box` rows, 128-byte swizzle;
-// what lies outside reads as zeros.
-bool half_map(CUtensorMap* m, const __half* p, int cols, int64_t rows, int parts, int box) {
-  auto fn = reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(tensor_map_encoder());
-  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)parts};
-  const cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)cols * 2 * rows};
-  const cuuint32_t boxes[3] = {kBK, (cuuint32_t)box, 1};
-  const cuuint32_t es[3] = {1, 1, 1};
-  return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<__half*>(p), dims, strides,
-                  boxes, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
+// Up to here the weights are unpacked inside the product (k_linfused.cu).
+constexpr int kFusedTokens = 512;
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
@@ -450,6 +403,11 @@ cudaError_t launch_linear_gemm(const LinArgs& l, void* ws, int* status, cudaStre
   p.w16 = (__half*)(base + lay.w16);
   p.fw = (float*)(base + lay.fw);
   p.x_blocks = (l.M + 7) / 8;
+  if (l.M <= kFusedTokens && p.x_parts == 1) {
+    k_lin_prep<<<p.x_blocks, 256, 0, st>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    return e != cudaSuccess ? e : launch_linear_fused(l, p.x16, p.fx, status, st);
+  }
   GemmArgs g;
   const int bn = l.M > 128 ? 256 : 128;
   if (!half_map(&g.tm_w, p.w16, l.in_dim, l.out_dim, p.w_parts, kTile) ||

@@ -11,16 +11,41 @@
 
 namespace moeq {
 
-__device__ __forceinline__ float act_of(float v, int act) {
-  switch (act) {
-    case MOEQ_ACT_SILU: return v / (1.0f + expf(-v));
-    case MOEQ_ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
-    case MOEQ_ACT_GELU_TANH:
-      return 0.5f * v * (1.0f + tanhf(0.79788456080286536f * (v + 0.044715f * v * v * v)));
-    case MOEQ_ACT_RELU: return v > 0.0f ? v : (v != v ? v : 0.0f);
-    case MOEQ_ACT_SIGMOID: return 1.0f / (1.0f + expf(-v));
-    default: return v;
+// The activations use the fast exponential (relative |v| 2^-23 + 2^-22) and
+// division; where their error is largest the value itself is smallest.
+template <int ACT>
+__device__ __forceinline__ float act1(float v) {
+  if (ACT == MOEQ_ACT_SILU) return __fdividef(v, 1.0f + __expf(-v));
+  if (ACT == MOEQ_ACT_GELU) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+  if (ACT == MOEQ_ACT_GELU_TANH) {
+    // 0.5 (1 + tanh(u)) = 1 / (1 + e^(-2u))
+    const float u = 0.79788456080286536f * (v + 0.044715f * v * v * v);
+    return __fdividef(v, 1.0f + __expf(-2.0f * u));
   }
+  if (ACT == MOEQ_ACT_RELU) return v > 0.0f ? v : (v != v ? v : 0.0f);
+  if (ACT == MOEQ_ACT_SIGMOID) return __fdividef(1.0f, 1.0f + __expf(-v));
+  return v;
+}
+template <int N>
+__device__ __forceinline__ void act_all(float (&v)[N], int act) {
+#define MOEQ_ACT_CASE(A)                               \
+  case A:                                              \
+    _Pragma("unroll") for (int i = 0; i < N; ++i) v[i] = act1<A>(v[i]); \
+    break;
+  switch (act) {
+    MOEQ_ACT_CASE(MOEQ_ACT_SILU)
+    MOEQ_ACT_CASE(MOEQ_ACT_GELU)
+    MOEQ_ACT_CASE(MOEQ_ACT_GELU_TANH)
+    MOEQ_ACT_CASE(MOEQ_ACT_RELU)
+    MOEQ_ACT_CASE(MOEQ_ACT_SIGMOID)
+    default: break;
+  }
+#undef MOEQ_ACT_CASE
+}
+__device__ __forceinline__ float act_of(float v, int act) {
+  float a[1] = {v};
+  act_all(a, act);
+  return a[0];
 }
 
 __device__ __forceinline__ float load_out(const void* p, int type, int64_t at) {

@@ -1,0 +1,100 @@
+// Pieces shared by the tcgen05 linear kernels: row powers, the epilogue of an
+// accumulator column, tensor maps.
+#pragma once
+
+#include <cuda.h>
+
+#include "kernels.h"
+#include "lincommon.cuh"
+#include "tc.cuh"
+
+namespace moeq {
+
+constexpr int kBK = 64;  // columns per stage (128 bytes)
+
+__device__ __forceinline__ float pow2(int k) { return __uint_as_float((uint32_t)(k + 127) << 23); }
+
+// Power of two that brings a largest magnitude to [2^13, 2^14) (for tiny
+// ones at most 2^126).
+__device__ __forceinline__ int lift_of(float largest) {
+  const int e = (int)(__float_as_uint(largest) >> 23) - 127;
+  return largest > 0.0f ? min(13 - e, 126) : 0;
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ float finite_abs(float v) {
+  v = fabsf(v);
+  return v < INFINITY ? v : 0.0f;
+}
+
+__device__ __forceinline__ uint32_t half_pair(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// A warp's N tokens from m0 (nm of them real) of output column o: lane j's
+// fx is token j's power.  mul and the residual are read together, before the
+// stores that might overlap them, so that their latency is paid once.
+template <typename T, int N>
+__device__ __forceinline__ void column(const void* p, int64_t stride, int64_t m0, int nm, int o,
+                                       T (&r)[N]) {
+  const T* c = reinterpret_cast<const T*>(p) + m0 * stride + o;
+#pragma unroll
+  for (int j = 0; j < N; ++j) r[j] = j < nm ? c[j * stride] : (T)0;
+}
+__device__ __forceinline__ float as_float(float v) { return v; }
+__device__ __forceinline__ float as_float(uint16_t v) { return bf16_bits_to_float(v); }
+__device__ __forceinline__ void as_out(float v, float* p) { *p = v; }
+__device__ __forceinline__ void as_out(float v, uint16_t* p) {
+  *reinterpret_cast<__nv_bfloat16*>(p) = __float2bfloat16_rn(v);
+}
+
+// T: the type of y, mul and the residual (uint16_t: bf16 bits).
+template <typename T, int N>
+__device__ __forceinline__ void finish(const moeq_linear_args& a, int64_t m0, int nm, int o,
+                                       bool live, float fw, float bias, float fx,
+                                       const uint32_t (&acc)[N]) {
+  T r[N];
+  if (a.residual) column(a.residual, a.residual_stride, m0, nm, o, r);
+  float y[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+    y[j] = __uint_as_float(acc[j]) * fw * __shfl_sync(0xffffffffu, fx, j) + bias;
+  act_all(y, a.act);
+  if (a.mul) {
+    T f[N];
+    column(a.mul, a.mul_stride, m0, nm, o, f);
+#pragma unroll
+    for (int j = 0; j < N; ++j) y[j] *= as_float(f[j]);
+  }
+  if (a.residual) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) y[j] += as_float(r[j]);
+  }
+  T* c = reinterpret_cast<T*>(a.y) + m0 * a.y_stride + o;
+  if (live) {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (j < nm) as_out(y[j], c + j * a.y_stride);
+  }
+}
+
+// [parts][rows][cols] fp16, boxes of 64 columns x `box` rows, 128-byte swizzle;
+// what lies outside reads as zeros.
+inline bool half_map(CUtensorMap* m, const __half* p, int cols, int64_t rows, int parts, int box) {
+  auto fn = reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(tensor_map_encoder());
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)parts};
+  const cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)cols * 2 * rows};
+  const cuuint32_t boxes[3] = {kBK, (cuuint32_t)box, 1};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<__half*>(p), dims, strides,
+                  boxes, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace moeq

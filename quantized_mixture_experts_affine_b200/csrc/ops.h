@@ -2,6 +2,7 @@
 // k_linear.cu, k_lingemm.cu), called by ops_api.cu after its argument checks.
 #pragma once
 
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -31,5 +32,8 @@ cudaError_t launch_linear_small(const LinArgs& l, cudaStream_t st);
 // Many tokens: two launches (operand layout, GEMM) over a workspace.
 size_t linear_gemm_workspace(const moeq_qtensor& t, int M, int x_type, int out_type);
 cudaError_t launch_linear_gemm(const LinArgs& l, void* ws, int* status, cudaStream_t st);
+// The product with the weights unpacked inside it, on tokens laid out in fp16.
+cudaError_t launch_linear_fused(const LinArgs& l, const __half* x16, const float* fx, int* status,
+                                cudaStream_t st);
 
 }  // namespace moeq

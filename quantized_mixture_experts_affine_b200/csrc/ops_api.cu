@@ -79,7 +79,7 @@ LinArgs lin_args(const moeq_qtensor& t, int expert, const moeq_linear_args& a, i
 }
 
 // Up to here the tokens go through the code products (measured in k_linear.cu).
-constexpr int kSmallTokens = 64;
+constexpr int kSmallTokens = 8;
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
