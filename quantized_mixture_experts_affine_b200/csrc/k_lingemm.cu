@@ -78,111 +78,197 @@ __device__ __forceinline__ void load_x8(const void* row, int type, int c0, float
   }
 }
 
-// Eight codes from column c0 (a multiple of 8) of a packed row as floats
-// (MX FP4: the element values).
-__device__ __forceinline__ void load_codes8(const uint32_t* row, int bits, bool mx, int c0,
-                                            float (&v)[8]) {
-  uint32_t lo, hi = 0u;  // the 8 * bits bits of the run
-  if (bits == 8) {
-    const uint2 w = *reinterpret_cast<const uint2*>(row + c0 / 4);
-    lo = w.x;
-    hi = w.y;
-  } else if (bits == 4) {
-    lo = row[c0 / 8];
-  } else if (bits == 2) {
-    lo = reinterpret_cast<const uint16_t*>(row)[c0 / 8];
-  } else {
-    // 3, 5, 6 bits: the run starts on a byte; it reaches into one more word
-    // at most, unless it ends inside its first
-    const int bit = c0 / 8 * 8 * bits, off = bit & 31, n = 8 * bits;
-    const uint32_t* p = row + (bit >> 5);
-    const uint32_t a = p[0], b = off + n > 32 ? p[1] : 0u, c = off + n > 64 ? p[2] : 0u;
-    lo = __funnelshift_r(a, b, off);
-    hi = __funnelshift_r(b, c, off);
-  }
+// Eight codes from column c0 (a multiple of 8) of a packed row, as loaded:
+// the 8 * BITS bits of the run in two words.
+template <int BITS>
+__device__ __forceinline__ uint2 load_run8(const uint32_t* row, int c0) {
+  if (BITS == 8) return *reinterpret_cast<const uint2*>(row + c0 / 4);
+  if (BITS == 4) return make_uint2(row[c0 / 8], 0u);
+  if (BITS == 2) return make_uint2(reinterpret_cast<const uint16_t*>(row)[c0 / 8], 0u);
+  // 3, 5, 6 bits: the run starts on a byte and reaches into the next one or
+  // two words only where it does not end before them
+  const int bit = c0 * BITS, off = bit & 31, n = 8 * BITS;
+  const uint32_t* p = row + (bit >> 5);
+  const uint32_t a = p[0], b = off + n > 32 ? p[1] : 0u, c = off + n > 64 ? p[2] : 0u;
+  return make_uint2(__funnelshift_r(a, b, off), __funnelshift_r(b, c, off));
+}
+
+// Their values times s plus b (MX FP4: element values times s).
+template <int BITS, bool MX>
+__device__ __forceinline__ void run8_values(uint2 w, float s, float b, float (&v)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const uint64_t run = ((uint64_t)hi << 32) | lo;
-    const uint32_t q = (uint32_t)(run >> (i * bits)) & ((1u << bits) - 1u);
-    if (mx) {
-      const uint32_t e = (q >> 1) & 3u, m = q & 1u;
-      const float mag = e ? (1.0f + 0.5f * m) * (float)(1u << (e - 1u)) : 0.5f * m;
-      v[i] = (q & 8u) ? -mag : mag;
+    const int bit = i * BITS;
+    uint32_t q;
+    if (BITS == 8 || bit + BITS <= 32) q = (bit < 32 ? w.x : w.y) >> (bit & 31);
+    else if (bit >= 32) q = w.y >> (bit & 31);
+    else q = __funnelshift_r(w.x, w.y, bit);
+    q &= (1u << BITS) - 1u;
+    if (MX) {
+      // e2m1: exponent and mantissa at fp32's places, scaled by 2^126
+      const float m = __uint_as_float((q & 7u) << 22) * __uint_as_float(0x7E800000u);
+      v[i] = ((q & 8u) ? -m : m) * s;
     } else {
-      v[i] = (float)q;
+      v[i] = __fmaf_rn(__uint_as_float(0x4B000000u | q) - 8388608.0f, s, b);
     }
   }
 }
 
-// One warp per row.
-__global__ void __launch_bounds__(256) k_lin_prep(const __grid_constant__ PrepArgs p) {
-  tc::grid_dep_launch();
+// A row of W by one warp, four runs of a lane in flight.
+template <int BITS, bool MX, bool TWO>
+__device__ __forceinline__ void prep_weights(const PrepArgs& p, int64_t o) {
   const LinArgs& l = p.l;
   const int lane = threadIdx.x & 31, K = l.in_dim;
-  if ((int)blockIdx.x < p.x_blocks) {
-    const int64_t m = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (m >= l.M) return;
-    const int type = l.a.x_type;
-    const char* row =
-        reinterpret_cast<const char*>(l.a.x) + m * l.a.x_stride * (type == MOEQ_BF16 ? 2 : 1);
-    const bool by128 = type != MOEQ_BF16 && l.a.x_group == 128;
-    const float* xs = l.a.x_scales + m * (by128 ? (K + 127) / 128 : 1);
-    __half* out = p.x16 + m * K;
-    const int64_t part = (int64_t)l.M * K;
-    float f = 1.0f;
-    if (type != MOEQ_BF16 && !by128) {
-      // whole numbers and e4m3 values are fp16 values as they are
-      if (lane == 0) p.fx[m] = xs[0];
-    } else {
-      float largest = 0.0f;
-      for (int c = lane * 8; c < K; c += 256) {
-        float v[8];
-        load_x8(row, type, c, v);
-        const float s = by128 ? xs[c >> 7] : 1.0f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) largest = fmaxf(largest, finite_abs(v[j] * s));
-      }
-      const int k = lift_of(warp_max(largest));
-      f = pow2(k);
-      if (lane == 0) p.fx[m] = pow2(-k);
-    }
-    for (int c = lane * 8; c < K; c += 256) {
-      float v[8];
-      load_x8(row, type, c, v);
-      const float s = by128 ? xs[c >> 7] : 1.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = (v[j] * s) * f;
-      store_halves(out + c, part, p.x_parts == 2, v);
-    }
-    return;
-  }
-  const int64_t o = ((int64_t)blockIdx.x - p.x_blocks) * 8 + (threadIdx.x >> 5);
-  if (o >= l.out_dim) return;
   const int groups = K / l.G, shift = l.G == 32 ? 5 : l.G == 64 ? 6 : 7;
-  const uint32_t* row = l.w + o * ((int64_t)K * l.bits / 32);
+  const uint32_t* row = l.w + o * ((int64_t)K * BITS / 32);
   const uint16_t* sc = l.scales + o * groups;
   const uint8_t* ex = reinterpret_cast<const uint8_t*>(l.scales) + o * groups;
-  const uint16_t* bi = l.mx ? nullptr : l.biases + o * groups;
-  const float qmax = (float)((1u << l.bits) - 1u);
+  const uint16_t* bi = MX ? nullptr : l.biases + o * groups;
+  constexpr int U = 4;
+  uint2 w[U];
+  auto fetch = [&](int c0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (c0 + 256 * u < K) w[u] = load_run8<BITS>(row, c0 + 256 * u);
+  };
+  fetch(lane * 8);
   float largest = 0.0f;
   for (int g = lane; g < groups; g += 32)
-    largest = fmaxf(largest,
-                    l.mx ? finite_abs(6.0f * mx_scale(ex[g]))
-                         : finite_abs(fabsf(bf16_bits_to_float(sc[g])) * qmax +
-                                      fabsf(bf16_bits_to_float(bi[g]))));
+    largest = fmaxf(largest, MX ? finite_abs(6.0f * mx_scale(ex[g]))
+                                : finite_abs(fabsf(bf16_bits_to_float(sc[g])) *
+                                                 (float)((1u << BITS) - 1u) +
+                                             fabsf(bf16_bits_to_float(bi[g]))));
   const int k = lift_of(warp_max(largest));
   const float f = pow2(k);
   if (lane == 0) p.fw[o] = pow2(-k);
   __half* out = p.w16 + o * K;
-  for (int c = lane * 8; c < K; c += 256) {
-    float v[8];
-    load_codes8(row, l.bits, l.mx, c, v);
-    const int g = c >> shift;
-    const float s = l.mx ? mx_scale(ex[g]) : bf16_bits_to_float(sc[g]);
-    const float b = l.mx ? 0.0f : bf16_bits_to_float(bi[g]);
+  for (int c0 = lane * 8; c0 < K; c0 += 256 * U) {
+    float s[U], b[U];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = __fmaf_rn(v[j], s, b) * f;
-    store_halves(out + c, (int64_t)l.out_dim * K, p.w_parts == 2, v);
+    for (int u = 0; u < U; ++u) {
+      const int g = min(c0 + 256 * u, K - 8) >> shift;
+      s[u] = (MX ? mx_scale(ex[g]) : bf16_bits_to_float(sc[g])) * f;
+      b[u] = MX ? 0.0f : bf16_bits_to_float(bi[g]) * f;
+    }
+    uint2 x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) x[u] = w[u];
+    fetch(c0 + 256 * U);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (c0 + 256 * u < K) {
+        float v[8];
+        run8_values<BITS, MX>(x[u], s[u], b[u], v);
+        store_halves(out + c0 + 256 * u, (int64_t)l.out_dim * K, TWO, v);
+      }
+  }
+}
+
+// A token row by the whole CTA; up to 8 * NV values of a thread stay in
+// registers between the maximum and the conversion, longer rows are read
+// again (from L1).
+constexpr int NV = 2;
+__device__ __forceinline__ void prep_tokens(const PrepArgs& p, int64_t m) {
+  __shared__ float red[32];
+  const LinArgs& l = p.l;
+  const int K = l.in_dim, T = blockDim.x, type = l.a.x_type;
+  const char* row =
+      reinterpret_cast<const char*>(l.a.x) + m * l.a.x_stride * (type == MOEQ_BF16 ? 2 : 1);
+  const bool by128 = type != MOEQ_BF16 && l.a.x_group == 128;
+  const float* xs = l.a.x_scales + m * (by128 ? (K + 127) / 128 : 1);
+  __half* out = p.x16 + m * K;
+  const int64_t part = (int64_t)l.M * K;
+  auto load = [&](int c, float (&v)[8]) {
+    load_x8(row, type, c, v);
+    if (by128) {
+      const float s = xs[c >> 7];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= s;
+    }
+  };
+  float v[NV][8];
+  float largest = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = 8 * ((int)threadIdx.x + i * T);
+    if (c < K) load(c, v[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+    if (8 * ((int)threadIdx.x + i * T) < K) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) largest = fmaxf(largest, finite_abs(v[i][j]));
+    }
+  const int rest = 8 * ((int)threadIdx.x + NV * T);
+  for (int c = rest; c < K; c += 8 * T) {
+    float u[8];
+    load(c, u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) largest = fmaxf(largest, finite_abs(u[j]));
+  }
+  float f = 1.0f;
+  if (type == MOEQ_BF16 || by128) {
+    largest = warp_max(largest);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = largest;
+    __syncthreads();
+    for (int i = 0; i < T / 32; ++i) largest = fmaxf(largest, red[i]);
+    const int k = lift_of(largest);
+    f = pow2(k);
+    if (threadIdx.x == 0) p.fx[m] = pow2(-k);
+  } else if (threadIdx.x == 0) {
+    // whole numbers and e4m3 values are fp16 values as they are
+    p.fx[m] = xs[0];
+  }
+  auto put = [&](int c, float (&u)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) u[j] *= f;
+    store_halves(out + c, part, p.x_parts == 2, u);
+  };
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = 8 * ((int)threadIdx.x + i * T);
+    if (c < K) put(c, v[i]);
+  }
+  for (int c = rest; c < K; c += 8 * T) {
+    float u[8];
+    load(c, u);
+    put(c, u);
+  }
+}
+
+// The first x_blocks CTAs take a token row each, the others a row of W per
+// warp.
+template <int BITS, bool MX, bool TWO>
+__global__ void __launch_bounds__(256) k_lin_prep(const __grid_constant__ PrepArgs p) {
+  tc::grid_dep_launch();
+  if ((int)blockIdx.x < p.x_blocks) {
+    prep_tokens(p, blockIdx.x);
+    return;
+  }
+  const int64_t o =
+      ((int64_t)blockIdx.x - p.x_blocks) * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (o < p.l.out_dim) prep_weights<BITS, MX, TWO>(p, o);
+}
+
+__global__ void __launch_bounds__(256) k_lin_tokens(const __grid_constant__ PrepArgs p) {
+  tc::grid_dep_launch();
+  prep_tokens(p, blockIdx.x);
+}
+
+template <bool TWO>
+void run_prep(const PrepArgs& p, cudaStream_t st) {
+  const int blocks = p.x_blocks + (p.l.out_dim + 7) / 8;
+  if (p.l.mx) {
+    k_lin_prep<4, true, TWO><<<blocks, 256, 0, st>>>(p);
+    return;
+  }
+  switch (p.l.bits) {
+    case 2: k_lin_prep<2, false, TWO><<<blocks, 256, 0, st>>>(p); break;
+    case 3: k_lin_prep<3, false, TWO><<<blocks, 256, 0, st>>>(p); break;
+    case 4: k_lin_prep<4, false, TWO><<<blocks, 256, 0, st>>>(p); break;
+    case 5: k_lin_prep<5, false, TWO><<<blocks, 256, 0, st>>>(p); break;
+    case 6: k_lin_prep<6, false, TWO><<<blocks, 256, 0, st>>>(p); break;
+    default: k_lin_prep<8, false, TWO><<<blocks, 256, 0, st>>>(p); break;
   }
 }
 
@@ -402,9 +488,9 @@ cudaError_t launch_linear_gemm(const LinArgs& l, void* ws, int* status, cudaStre
   p.fx = (float*)(base + lay.fx);
   p.w16 = (__half*)(base + lay.w16);
   p.fw = (float*)(base + lay.fw);
-  p.x_blocks = (l.M + 7) / 8;
+  p.x_blocks = l.M;
   if (l.M <= kFusedTokens && p.x_parts == 1) {
-    k_lin_prep<<<p.x_blocks, 256, 0, st>>>(p);
+    k_lin_tokens<<<p.x_blocks, 256, 0, st>>>(p);
     const cudaError_t e = cudaGetLastError();
     return e != cudaSuccess ? e : launch_linear_fused(l, p.x16, p.fx, status, st);
   }
@@ -421,7 +507,8 @@ cudaError_t launch_linear_gemm(const LinArgs& l, void* ws, int* status, cudaStre
   g.tiles_o = (l.out_dim + 2 * kTile - 1) / (2 * kTile);
   g.tiles_m = (l.M + bn - 1) / bn;
   g.status = status;
-  k_lin_prep<<<p.x_blocks + (l.out_dim + 7) / 8, 256, 0, st>>>(p);
+  if (p.w_parts == 2) run_prep<true>(p, st);
+  else run_prep<false>(p, st);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return bn == 256 ? run_gemm<256>(g, sms, st) : run_gemm<128>(g, sms, st);

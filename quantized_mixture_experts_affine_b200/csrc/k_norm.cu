@@ -49,8 +49,10 @@ __device__ __forceinline__ void load8(const void* p, int type, int64_t at, int n
     return;
   }
 #pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+  if (n <= 0) return;
+#pragma unroll
   for (int i = 0; i < 8; ++i) {
-    v[i] = 0.0f;
     if (i < n)
       v[i] = type == MOEQ_F32 ? reinterpret_cast<const float*>(p)[at + i]
                               : bf16_bits_to_float(reinterpret_cast<const uint16_t*>(p)[at + i]);
@@ -119,64 +121,148 @@ __device__ __noinline__ uint32_t code_e4m3_64(float r, float g, double a) {
 // fp32 cannot hold top / a below this (and r gamma may have lost bits)
 constexpr float kTinyMax = 1e-28f;
 
-template <int NV>
-__global__ void __launch_bounds__(1024) k_add_rmsnorm(const __grid_constant__ NormArgs a) {
+// The eight codes of a vector from values (r, g) of a group with maximum mk.
+__device__ __forceinline__ uint2 codes8(int type, const float (&r)[8], const float (&g)[8],
+                                        unsigned long long mk) {
+  const float am = __uint_as_float((uint32_t)(mk >> 32));
+  if (!(am < INFINITY)) return make_uint2(0u, 0u);
+  const bool i8 = type == MOEQ_I8;
+  const float f = __fdiv_rn(i8 ? 127.0f : 448.0f, am);
+  float c[8];
+  bool doubt[8], any = false;
+  uint32_t out[2];
+  if (i8) {
+    uint32_t q[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      c[j] = r[j] * g[j] * f;
+      const float v = rintf(c[j]);
+      q[j] = (uint32_t)__float2int_rn(v);
+      // fp32's error of c: 4 roundings, 127 * 4 * 2^-24 < 3.1e-5
+      doubt[j] = fabsf(fabsf(c[j] - v) - 0.5f) < 6e-5f;
+      any |= doubt[j];
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      out[h] = __byte_perm(__byte_perm(q[4 * h], q[4 * h + 1], 0x0040u),
+                           __byte_perm(q[4 * h + 2], q[4 * h + 3], 0x0040u), 0x5410u);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      c[j] = r[j] * g[j] * f;
+      // a border has the fraction bits below e4m3's three at exactly one half;
+      // below 2^-6 (subnormal codes) fp64 decides
+      const uint32_t low = __float_as_uint(c[j]) & 0xFFFFFu;
+      doubt[j] = (low - 0x7FFF0u) <= 0x20u || (fabsf(c[j]) < 0.015625f && c[j] != 0.0f);
+      any |= doubt[j];
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(c[4 * h], c[4 * h + 1]),
+                                                  __NV_SATFINITE, __NV_E4M3);
+      const uint32_t b = __nv_cvt_float2_to_fp8x2(make_float2(c[4 * h + 2], c[4 * h + 3]),
+                                                  __NV_SATFINITE, __NV_E4M3);
+      out[h] = a | b << 16;
+    }
+  }
+  const bool tiny = am < kTinyMax;
+  if (any || tiny) {
+    const double a64 = mag_value(mk);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (doubt[j] || tiny) {
+        const uint32_t k = r[j] * g[j] == 0.0f ? 0u
+                           : i8                ? code_i8_64(r[j], g[j], a64)
+                                               : code_e4m3_64(r[j], g[j], a64);
+        out[j / 4] = (out[j / 4] & ~(255u << (8 * (j & 3)))) | k << (8 * (j & 3));
+      }
+  }
+  return make_uint2(out[0], out[1]);
+}
+
+// Largest |r gamma| of a thread's eight values as a key (see mag_key).  SHORT:
+// r is a bf16, so r gamma is exact in fp32 and nothing is left over.
+template <bool SHORT>
+__device__ __forceinline__ unsigned long long max8(const float (&r)[8], const float (&g)[8]) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    top = max(top, __float_as_uint(r[j] * g[j]) & 0x7FFFFFFFu);  // a NaN is largest
+  if (SHORT) return ((unsigned long long)top << 32) | 0x80000000u;
+  unsigned long long key = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if ((__float_as_uint(r[j] * g[j]) & 0x7FFFFFFFu) == top) {
+      const unsigned long long k = mag_key(r[j], g[j]);
+      key = k > key ? k : key;
+    }
+  return key;
+}
+
+template <bool SHORT, int FIRST>
+__device__ __forceinline__ unsigned long long max_lanes(unsigned long long k) {
+  if (SHORT) {
+    uint32_t t = (uint32_t)(k >> 32);
+    if (FIRST == 16) {
+      t = __reduce_max_sync(0xffffffffu, t);
+    } else {
+#pragma unroll
+      for (int o = FIRST; o > 0; o >>= 1) t = max(t, __shfl_xor_sync(0xffffffffu, t, o));
+    }
+    return ((unsigned long long)t << 32) | 0x80000000u;
+  }
+#pragma unroll
+  for (int o = FIRST; o > 0; o >>= 1) {
+    const unsigned long long p = __shfl_xor_sync(0xffffffffu, k, o);
+    k = p > k ? p : k;
+  }
+  return k;
+}
+
+// MAXT: threads of the largest block of this variant.
+template <int NV, bool SHORT, int MAXT>
+__global__ void __launch_bounds__(MAXT) k_add_rmsnorm(const __grid_constant__ NormArgs a) {
   __shared__ float red[32];
   __shared__ unsigned long long red_max[32];
   const moeq_norm_args& n = a.n;
   const int T = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = T >> 5;
   const int64_t m = blockIdx.x;
-  float r[NV][8];
+  const bool whole = n.q && n.q_group == 0;
+  float r[NV][8], g[NV][8];
   float ss = 0.0f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int v = tid + i * T;
     const int cnt = v < a.vecs ? min(8, a.H - 8 * v) : 0;
+    load8(n.x, n.x_type, m * n.x_stride + 8 * v, cnt, a.vx, r[i]);
+    if (n.residual) {
+      float s[8];
+      load8(n.residual, n.r_type, m * n.r_stride + 8 * v, cnt, a.vr, s);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) r[i][j] = 0.0f;
-    if (cnt > 0) {
-      load8(n.x, n.x_type, m * n.x_stride + 8 * v, cnt, a.vx, r[i]);
-      if (n.residual) {
-        float s[8];
-        load8(n.residual, n.r_type, m * n.r_stride + 8 * v, cnt, a.vr, s);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          r[i][j] += s[j];
-          // the norm is of the stream as it is stored
-          if (n.r_type == MOEQ_BF16) r[i][j] = __bfloat162float(__float2bfloat16_rn(r[i][j]));
-        }
-        if (n.r_out) store8(n.r_out, n.r_type, m * n.r_out_stride + 8 * v, cnt, a.vro, r[i]);
+      for (int j = 0; j < 8; ++j) {
+        r[i][j] += s[j];
+        // the norm is of the stream as it is stored
+        if (n.r_type == MOEQ_BF16) r[i][j] = __bfloat162float(__float2bfloat16_rn(r[i][j]));
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss = __fmaf_rn(r[i][j], r[i][j], ss);
     }
+    load8(n.gamma, MOEQ_BF16, 8 * v, cnt, a.vg, g[i]);
   }
-  // gamma, and the largest |r gamma| of the row for one scale per row
-  float g[NV][8];
   unsigned long long row_max = 0;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int v = tid + i * T;
     const int cnt = v < a.vecs ? min(8, a.H - 8 * v) : 0;
+    if (n.r_out && cnt > 0)
+      store8(n.r_out, n.r_type, m * n.r_out_stride + 8 * v, cnt, a.vro, r[i]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) g[i][j] = 0.0f;
-    if (cnt > 0) load8(n.gamma, MOEQ_BF16, 8 * v, cnt, a.vg, g[i]);
-    if (n.q && n.q_group == 0) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const unsigned long long k = mag_key(r[i][j], g[i][j]);
-        row_max = k > row_max ? k : row_max;
-      }
-    }
-  }
-  ss = warp_sum(ss);
-  if (n.q && n.q_group == 0) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const unsigned long long k = __shfl_xor_sync(0xffffffffu, row_max, o);
+    for (int j = 0; j < 8; ++j) ss = __fmaf_rn(r[i][j], r[i][j], ss);
+    if (whole) {
+      const unsigned long long k = max8<SHORT>(r[i], g[i]);
       row_max = k > row_max ? k : row_max;
     }
   }
+  ss = warp_sum(ss);
+  if (whole) row_max = max_lanes<SHORT, 16>(row_max);
   if (lane == 0) {
     red[warp] = ss;
     red_max[warp] = row_max;
@@ -187,9 +273,8 @@ __global__ void __launch_bounds__(1024) k_add_rmsnorm(const __grid_constant__ No
     ss += red[i];
     row_max = red_max[i] > row_max ? red_max[i] : row_max;
   }
-  const float inv = 1.0f / sqrtf(ss / (float)a.H + n.eps);
+  const float inv = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss, (float)a.H) + n.eps));
 
-  const float top = n.q_type == MOEQ_I8 ? 127.0f : 448.0f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int v = tid + i * T;
@@ -200,63 +285,38 @@ __global__ void __launch_bounds__(1024) k_add_rmsnorm(const __grid_constant__ No
       for (int j = 0; j < 8; ++j) o[j] = r[i][j] * inv * g[i][j];
       store8(n.y, MOEQ_BF16, m * n.y_stride + 8 * v, cnt, a.vy, o);
     }
-    if (!n.q) continue;
-    unsigned long long mk = row_max;
-    if (n.q_group) {  // 16 neighbouring lanes hold 128 columns
-      mk = 0;
+    if (n.q) {
+      // 16 neighbouring lanes hold 128 columns
+      const unsigned long long mk =
+          whole ? row_max : max_lanes<SHORT, 8>(max8<SHORT>(r[i], g[i]));
+      if (cnt > 0) {
+        if (whole ? v == 0 : (v & 15) == 0) {
+          const float am = __uint_as_float((uint32_t)(mk >> 32));
+          n.q_scales[m * a.n_scales + (whole ? 0 : v >> 4)] =
+              am < INFINITY ? __fdiv_rn(am * inv, n.q_type == MOEQ_I8 ? 127.0f : 448.0f)
+                            : __uint_as_float(0x7FC00000u);
+        }
+        const uint2 code = codes8(n.q_type, r[i], g[i], mk);
+        uint8_t* q = reinterpret_cast<uint8_t*>(n.q) + m * n.q_stride + 8 * v;
+        if (a.vq && cnt == 8) {
+          *reinterpret_cast<uint2*>(q) = code;
+        } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const unsigned long long k = mag_key(r[i][j], g[i][j]);
-        mk = k > mk ? k : mk;
+          for (int j = 0; j < 8; ++j)
+            if (j < cnt) q[j] = (uint8_t)((j < 4 ? code.x : code.y) >> (8 * (j & 3)));
+        }
       }
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) {
-        const unsigned long long k = __shfl_xor_sync(0xffffffffu, mk, o);
-        mk = k > mk ? k : mk;
-      }
-    }
-    if (cnt <= 0) continue;
-    const float am = __uint_as_float((uint32_t)(mk >> 32));
-    const bool finite = am < INFINITY;
-    if (n.q_group ? (v & 15) == 0 : v == 0)
-      n.q_scales[m * a.n_scales + (n.q_group ? v >> 4 : 0)] =
-          finite ? am * inv / top : __uint_as_float(0x7FC00000u);
-    const float f = top / am;
-    uint32_t code[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float t = r[i][j] * g[i][j];
-      const float c = t * f;
-      if (!finite || t == 0.0f) {
-        code[j] = 0;
-      } else if (n.q_type == MOEQ_I8) {
-        const float q = rintf(c);
-        // fp32's error of c: 4 roundings, 127 * 4 * 2^-24 < 3.1e-5
-        if (am < kTinyMax || fabsf(fabsf(c - q) - 0.5f) < 6e-5f)
-          code[j] = code_i8_64(r[i][j], g[i][j], mag_value(mk));
-        else
-          code[j] = (uint32_t)(int)q & 255u;
-      } else {
-        // a border has the fraction bits below e4m3's three at exactly one half;
-        // below 2^-6 (subnormal codes) fp64 decides
-        const uint32_t low = __float_as_uint(c) & 0xFFFFFu;
-        if (am < kTinyMax || fabsf(c) < 0.015625f || (low - 0x7FFF0u) <= 0x20u)
-          code[j] = code_e4m3_64(r[i][j], g[i][j], mag_value(mk));
-        else
-          code[j] = __nv_cvt_float_to_fp8(c, __NV_SATFINITE, __NV_E4M3);
-      }
-    }
-    uint8_t* q = reinterpret_cast<uint8_t*>(n.q) + m * n.q_stride + 8 * v;
-    if (a.vq && cnt == 8) {
-      *reinterpret_cast<uint2*>(q) =
-          make_uint2(code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24,
-                     code[4] | code[5] << 8 | code[6] << 16 | code[7] << 24);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < cnt) q[j] = (uint8_t)code[j];
     }
   }
+}
+
+template <bool SHORT>
+void run(const NormArgs& a, int M, cudaStream_t st) {
+  const int warps = (a.vecs + 31) / 32;
+  if (warps <= 16) k_add_rmsnorm<1, SHORT, 512><<<M, warps * 32, 0, st>>>(a);
+  else if (warps <= 32) k_add_rmsnorm<2, SHORT, 512><<<M, (warps + 1) / 2 * 32, 0, st>>>(a);
+  else if (warps <= 64) k_add_rmsnorm<2, SHORT, 1024><<<M, (warps + 1) / 2 * 32, 0, st>>>(a);
+  else k_add_rmsnorm<4, SHORT, 1024><<<M, (warps + 3) / 4 * 32, 0, st>>>(a);
 }
 
 bool wide(const void* p, int64_t stride, int item, int bytes) {
@@ -278,14 +338,9 @@ cudaError_t launch_add_rmsnorm(const moeq_norm_args& n, int M, int H, cudaStream
   a.vg = wide(n.gamma, 0, 2, 16);
   a.vy = wide(n.y, n.y_stride, 2, 16);
   a.vq = wide(n.q, n.q_stride, 1, 8);
-  const int warps = (a.vecs + 31) / 32;
-  if (warps <= 32) {
-    k_add_rmsnorm<1><<<M, warps * 32, 0, st>>>(a);
-  } else if (warps <= 64) {
-    k_add_rmsnorm<2><<<M, (warps + 1) / 2 * 32, 0, st>>>(a);
-  } else {
-    k_add_rmsnorm<4><<<M, (warps + 3) / 4 * 32, 0, st>>>(a);
-  }
+  // a bf16 stream: r gamma has 16 bits
+  if ((n.residual ? n.r_type : n.x_type) == MOEQ_BF16) run<true>(a, M, st);
+  else run<false>(a, M, st);
   return cudaGetLastError();
 }
 

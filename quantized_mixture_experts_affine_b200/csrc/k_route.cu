@@ -29,6 +29,7 @@ struct RouteArgs {
   int bf16;
   int M;
   int lanes_per_group;  // power of two
+  int group_quads;      // registers path: quads per group, a power of two
 };
 
 // Order-preserving keys.  0: dropped or taken; 1: an expert that is out (its
@@ -321,17 +322,422 @@ __device__ bool route_row(const RouteArgs& a, int m, typename Keys<T>::K* keys, 
   return true;
 }
 
-__global__ void __launch_bounds__(256) k_route_groups(const __grid_constant__ RouteArgs a) {
+// ---- registers: up to 512 experts, groups that are a power of two of quads
+// L lanes hold a row (a warp holds 32 / L rows): lane l of them the quads
+// l + L j, experts 4 q .. 4 q + 3.  Same steps as route_row<float>; a group's
+// members are neighbouring lanes, so its two largest keys come from a
+// butterfly, and a pick rescans 4 NQ registers.  With L = 32 a doubt about
+// the picks themselves is settled on the spot: the few experts concerned are
+// scored in fp64, one per lane, and ranked again.
+
+// 1 / (1 + e^-z) and e^d; expf is within 2 ulp, the fast division too.
+__device__ __forceinline__ float fast_numerator(const moeq_routing& r, float l, float mx) {
+  if (r.score == MOEQ_SCORE_SIGMOID) return __fdividef(1.0f, 1.0f + expf(-r.router_scale * l));
+  return l == mx ? 1.0f : expf(r.router_scale * (l - mx));
+}
+
+template <int L>
+__device__ __forceinline__ uint32_t seg_max(uint32_t v) {
+  if (L == 32) return __reduce_max_sync(0xffffffffu, v);
+#pragma unroll
+  for (int o = L >> 1; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+template <int L>
+__device__ __forceinline__ uint32_t seg_min(uint32_t v) {
+  if (L == 32) return __reduce_min_sync(0xffffffffu, v);
+#pragma unroll
+  for (int o = L >> 1; o > 0; o >>= 1) v = min(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+template <int L>
+__device__ __forceinline__ float seg_sum(float v) {
+#pragma unroll
+  for (int o = L >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// The segment's bits of a ballot, from bit 0 on.
+template <int L>
+__device__ __forceinline__ uint32_t seg_ballot(bool p) {
+  const uint32_t b = __ballot_sync(0xffffffffu, p);
+  return L == 32 ? b : (b >> ((threadIdx.x & 31) & ~(L - 1))) & ((1u << (L & 31)) - 1u);
+}
+
+// Every lane of the warp calls it; m: its segment's token (store: whether to
+// write it).  slots: 32 x 3 words of the warp's shared memory.  Returns false
+// in every lane of a segment whose row is not settled (nothing is written).
+template <int L, int NQ, bool GROUPS, bool BIAS>
+__device__ __forceinline__ bool route_regs(const RouteArgs& a, int m, bool store,
+                                           uint32_t* slots) {
+  using KT = Keys<float>;
+  const moeq_routing& r = a.r;
+  const int lane = threadIdx.x & (L - 1), E = r.n_experts;
+  const int64_t row = (int64_t)m * a.stride;
+  const bool softmax = r.score == MOEQ_SCORE_SOFTMAX;
+  float l[NQ][4], b[NQ][4];
+  {
+    const size_t item = a.bf16 ? 2 : 4;
+    const uintptr_t base = (uintptr_t)a.logits + (size_t)row * item;
+    const bool vec = (base & (4 * item - 1)) == 0, bvec = ((uintptr_t)a.bias & 15) == 0;
+#pragma unroll
+    for (int j = 0; j < NQ; ++j) {
+      const int q = lane + L * j;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) l[j][c] = -INFINITY, b[j][c] = 0.0f;
+      if (vec && 4 * q + 4 <= E) {
+        if (a.bf16) {
+          const uint2 v = *reinterpret_cast<const uint2*>(base + (size_t)q * 8);
+          l[j][0] = __uint_as_float(v.x << 16);
+          l[j][1] = __uint_as_float(v.x & 0xFFFF0000u);
+          l[j][2] = __uint_as_float(v.y << 16);
+          l[j][3] = __uint_as_float(v.y & 0xFFFF0000u);
+        } else {
+          const float4 v = *reinterpret_cast<const float4*>(base + (size_t)q * 16);
+          l[j][0] = v.x;
+          l[j][1] = v.y;
+          l[j][2] = v.z;
+          l[j][3] = v.w;
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (4 * q + c < E) l[j][c] = logit_at(a, row, 4 * q + c);
+      }
+      if (BIAS) {
+        if (bvec && 4 * q + 4 <= E) {
+          const float4 v = *reinterpret_cast<const float4*>(a.bias + 4 * q);
+          b[j][0] = v.x;
+          b[j][1] = v.y;
+          b[j][2] = v.z;
+          b[j][3] = v.w;
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (4 * q + c < E) b[j][c] = a.bias[4 * q + c];
+        }
+      }
+    }
+  }
+  float mx = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < NQ; ++j)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) mx = fmaxf(mx, l[j][c]);  // fmaxf passes over NaN
+  mx = KT::value(seg_max<L>(KT::of(mx)));
+
+  float sum = 1.0f;
+  if (softmax && (BIAS || !r.renorm || (GROUPS && r.group_top == 2))) {
+    float z = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NQ; ++j)
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (!is_out(l[j][c])) z += fast_numerator(r, l[j][c], mx);
+    sum = seg_sum<L>(z);
+  }
+  const float inv = __fdividef(1.0f, sum);
+  // Error of a score relative to the largest: expf 2^-22, division 2^-22, the
+  // exponent's and the last roundings under 2^-22 (e^-d d < 0.37), and the
+  // normaliser's additions
+  const float s_max = is_out(mx) ? 0.0f : fast_numerator(r, mx, mx) * inv;
+  const float tol_s = (7.2e-7f + (softmax ? 6e-8f * (4 * NQ + 8) : 0.0f)) * s_max;
+
+  uint32_t k[NQ][4];
+#pragma unroll
+  for (int j = 0; j < NQ; ++j)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int e = 4 * (lane + L * j) + c;
+      const float v = BIAS ? fast_numerator(r, l[j][c], mx) * inv + b[j][c] : l[j][c];
+      k[j][c] = e >= E ? 0u : is_out(l[j][c]) ? 1u : KT::of(v);
+    }
+
+  bool sure = true;
+  if (GROUPS) {
+    const int w = a.group_quads, lg = 31 - __clz(w);  // quads per group, a power of two
+    uint32_t gk[NQ];
+#pragma unroll
+    for (int j = 0; j < NQ; ++j) {
+      const uint32_t h0 = max(k[j][0], k[j][1]), l0 = min(k[j][0], k[j][1]);
+      const uint32_t h1 = max(k[j][2], k[j][3]), l1 = min(k[j][2], k[j][3]);
+      uint32_t k1 = max(h0, h1), k2 = max(min(h0, h1), max(l0, l1));
+      for (int o = w >> 1; o > 0; o >>= 1) {
+        const uint32_t p1 = __shfl_xor_sync(0xffffffffu, k1, o);
+        const uint32_t p2 = __shfl_xor_sync(0xffffffffu, k2, o);
+        k2 = max(min(k1, p1), max(k2, p2));
+        k1 = max(k1, p1);
+      }
+      gk[j] = k1;
+      if (r.group_top == 2 && k1 > 1) {
+        const float v1 = BIAS ? KT::value(k1) : fast_numerator(r, KT::value(k1), mx) * inv;
+        const float v2 = k2 <= 1 ? 0.0f
+                         : BIAS  ? KT::value(k2)
+                                 : fast_numerator(r, KT::value(k2), mx) * inv;
+        gk[j] = KT::of(v1 + v2);
+      }
+    }
+    // lane g: the keys of groups g, g + L, ...
+    constexpr int GP = L == 32 ? 1 : 32 / L;
+    uint32_t mine[GP];
+    int rank[GP];
+#pragma unroll
+    for (int p = 0; p < GP; ++p) {
+      mine[p] = 0;
+      rank[p] = 0;
+      const int at = (lane + L * p) << lg;  // its first quad
+#pragma unroll
+      for (int j = 0; j < NQ; ++j) {
+        const uint32_t v = __shfl_sync(0xffffffffu, gk[j], at & (L - 1), L);
+        if (lane + L * p < r.n_groups && at / L == j) mine[p] = v;
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < GP; ++p)
+      for (int g = 0; g < L && g + L * p < r.n_groups; ++g) {
+        const uint32_t v = __shfl_sync(0xffffffffu, mine[p], g, L);
+#pragma unroll
+        for (int o = 0; o < GP; ++o)
+          rank[o] += (v > mine[o] || (v == mine[o] && g + L * p < lane + L * o)) ? 1 : 0;
+      }
+    uint32_t kept = 0, last = 0, next = 0;
+#pragma unroll
+    for (int p = 0; p < GP; ++p) {
+      const bool in = lane + L * p < r.n_groups;
+      kept |= seg_ballot<L>(in && rank[p] < r.topk_groups) << (L * p & 31);
+      if (in && rank[p] == r.topk_groups - 1) last = mine[p];
+      if (in && rank[p] == r.topk_groups) next = mine[p];
+    }
+    if (BIAS || r.group_top == 2) {
+      const uint32_t kl = seg_max<L>(last), kn = seg_max<L>(next);
+      if (kl > 1 && kn > 1) {
+        // two scores and three roundings on each side
+        const float vl = KT::value(kl), vn = KT::value(kn);
+        if (!(vl - vn > 4.0f * tol_s + 1.8e-7f * (fabsf(vl) + fabsf(vn)))) sure = false;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NQ; ++j)
+      if (!((kept >> (((lane + L * j) >> lg) & 31)) & 1u)) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) k[j][c] = 0;
+      }
+  }
+
+  uint32_t lk = 0;
+  int li = kNoExpert;
+  auto rescan = [&]() {
+    lk = 0;
+    li = kNoExpert;
+#pragma unroll
+    for (int j = 0; j < NQ; ++j)
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (k[j][c] > lk) {
+          lk = k[j][c];
+          li = 4 * (lane + L * j) + c;
+        }
+  };
+  rescan();
+  uint32_t my_k = 0;
+  int my_e = 0;
+  for (int i = 0; i < r.top_k; ++i) {
+    const uint32_t top = seg_max<L>(lk);
+    const int win = (int)seg_min<L>(lk == top ? (uint32_t)li : 0x7fffffffu);
+    if (li == win && win != kNoExpert) {
+#pragma unroll
+      for (int j = 0; j < NQ; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (4 * (lane + L * j) + c == win) k[j][c] = 0;
+      rescan();
+    }
+    if (lane == i) {
+      my_k = top;
+      my_e = win == kNoExpert ? 0 : win;
+    }
+  }
+  const bool mine = lane < r.top_k;
+  bool valid = mine && my_k > 1;
+  // the picks' own logits: with a bias the key does not give them
+  float my_l = -INFINITY, my_b = 0.0f;
+  if (BIAS) {
+    if (valid) {
+      my_l = logit_at(a, row, my_e);
+      my_b = a.bias[my_e];
+    }
+  } else if (valid) {
+    my_l = KT::value(my_k);
+  }
+
+  if (BIAS) {
+    const float v = valid ? KT::value(my_k) : 0.0f;
+    const float vn = __shfl_down_sync(0xffffffffu, v, 1, L);
+    const float ln = __shfl_down_sync(0xffffffffu, my_l, 1, L);
+    const float bn = __shfl_down_sync(0xffffffffu, my_b, 1, L);
+    const bool next_valid = __shfl_down_sync(0xffffffffu, (int)valid, 1, L) && lane < L - 1;
+    const float tol = 2.0f * tol_s + 1.8e-7f * fabsf(v);
+    bool doubt = valid && next_valid && !(v - vn > tol) && !(my_l == ln && my_b == bn);
+    const int last = r.top_k - 1;
+    const bool lv = __shfl_sync(0xffffffffu, (int)valid, last, L);
+    const float border = __shfl_sync(0xffffffffu, v - tol, last, L);
+    const float l_last = __shfl_sync(0xffffffffu, my_l, last, L);
+    const float b_last = __shfl_sync(0xffffffffu, my_b, last, L);
+    uint32_t near = 0;  // bit 4 j + c: an expert left that comes near the last pick
+    if (lv && lk > 1 && !(KT::value(lk) < border)) {
+#pragma unroll
+      for (int j = 0; j < NQ; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (k[j][c] > 1 && !(KT::value(k[j][c]) < border)) {
+            near |= 1u << (4 * j + c);
+            if (!(l[j][c] == l_last && b[j][c] == b_last)) doubt = true;
+          }
+    }
+    if (seg_ballot<L>(doubt)) {
+      if (L < 32) {
+        sure = false;
+      } else if (__all_sync(0xffffffffu, sure)) {
+        // candidates: the picks, and what comes near; one per lane
+        const int count = __popc(near);
+        int at = count;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int p = __shfl_up_sync(0xffffffffu, at, o);
+          if (lane >= o) at += p;
+        }
+        const int n = r.top_k + __shfl_sync(0xffffffffu, at, 31);
+        at += r.top_k - count;
+        if (n > 32) {
+          sure = false;
+        } else {
+          auto put = [&](int p, int e, float lg, float bi) {
+            slots[p] = (uint32_t)e;
+            slots[32 + p] = __float_as_uint(lg);
+            slots[64 + p] = __float_as_uint(bi);
+          };
+          if (mine) put(lane, my_e, my_l, my_b);
+#pragma unroll
+          for (int j = 0; j < NQ; ++j)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (near & (1u << (4 * j + c))) put(at++, 4 * (lane + L * j) + c, l[j][c], b[j][c]);
+          double z = 1.0;
+          if (softmax) {
+            z = 0.0;
+#pragma unroll 1
+            for (int j = 0; j < NQ; ++j) {
+              // (registers are not indexed: the row is read again)
+              for (int c = 0; c < 4; ++c) {
+                const int e = 4 * (lane + L * j) + c;
+                const float le = e < E ? logit_at(a, row, e) : -INFINITY;
+                if (!is_out(le)) z += numerator<double>(r, le, mx);
+              }
+            }
+            z = warp_sum_t(z);
+          }
+          __syncwarp();
+          const bool cand = lane < n;
+          const int e = cand ? (int)slots[lane] : kNoExpert;
+          const float le = cand ? __uint_as_float(slots[32 + lane]) : -INFINITY;
+          const double v64 = is_out(le) ? -INFINITY
+                                        : numerator<double>(r, le, mx) / z +
+                                              (double)__uint_as_float(slots[64 + lane]);
+          int rank = 0;
+          for (int p = 0; p < n; ++p) {
+            const double vp = __shfl_sync(0xffffffffu, v64, p);
+            const int ep = __shfl_sync(0xffffffffu, e, p);
+            rank += (vp > v64 || (vp == v64 && ep < e)) ? 1 : 0;
+          }
+          __syncwarp();
+          if (cand) {
+            slots[rank] = (uint32_t)e;
+            slots[32 + rank] = __float_as_uint(le);
+          }
+          __syncwarp();
+          if (mine) {
+            my_e = (int)slots[lane];
+            my_l = __uint_as_float(slots[32 + lane]);
+            valid = !is_out(my_l);
+          }
+        }
+      }
+    }
+  }
+
+  const float p = valid ? numerator<float>(r, my_l, mx) : 0.0f;
+  float denom = sum;
+  if (r.renorm) denom = seg_sum<L>(p);
+  const bool some = seg_ballot<L>(valid) != 0;
+  if (r.renorm && some && denom < 1e-30f) sure = false;
+  if (seg_ballot<L>(!sure)) return false;
+  if (mine && store) {
+    const int64_t at = (int64_t)m * r.top_k + lane;
+    a.idx[at] = my_e;
+    a.w[at] = denom > 0.0f ? p / denom * r.routed_scale : 0.0f;
+  }
+  return true;
+}
+
+__device__ __noinline__ void route_row64(const RouteArgs& a, int m, uint64_t* mine, float* raw) {
+  __syncwarp();
+  route_row<double>(a, m, reinterpret_cast<unsigned long long*>(mine), raw);
+}
+
+// A warp's slots: 4 nq keys of 8 bytes, then 4 nq logits.
+__device__ __forceinline__ uint64_t* warp_slots(const RouteArgs& a, float*& raw) {
   extern __shared__ uint64_t slots[];
-  const int warp = threadIdx.x >> 5;
-  const int m = blockIdx.x * (blockDim.x >> 5) + warp;
+  const int nq = max((a.r.n_experts + 3) >> 2, 8);
+  uint64_t* mine = slots + (size_t)(threadIdx.x >> 5) * (6 * nq);
+  raw = reinterpret_cast<float*>(mine + 4 * nq);
+  return mine;
+}
+
+// The rows a warp's segments could not settle, with all its lanes.
+template <int NQ, bool GROUPS, bool BIAS>
+__device__ __noinline__ void route_again(const RouteArgs& a, int m, uint64_t* mine, float* raw) {
+  if (!route_regs<32, NQ, GROUPS, BIAS>(a, m, true, reinterpret_cast<uint32_t*>(mine)))
+    route_row64(a, m, mine, raw);
+}
+
+template <int L, int NQ, bool GROUPS, bool BIAS>
+__global__ void __launch_bounds__(256) k_route_regs(const __grid_constant__ RouteArgs a) {
+  constexpr int ROWS = 32 / L;
+  const int lane = threadIdx.x & 31;
+  const int m0 = (blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * ROWS;
+  if (m0 >= a.M) return;
+  float* raw;
+  uint64_t* mine = warp_slots(a, raw);
+  const int m = m0 + lane / L;
+  const bool settled = route_regs<L, NQ, GROUPS, BIAS>(a, min(m, a.M - 1), m < a.M,
+                                                       reinterpret_cast<uint32_t*>(mine));
+  uint32_t left = __ballot_sync(0xffffffffu, !settled && m < a.M && lane % L == 0);
+  if (L == 32) {
+    if (left) route_row64(a, m0, mine, raw);
+    return;
+  }
+  constexpr int NQ32 = NQ * L / 32 > 0 ? NQ * L / 32 : 1;
+  for (; left; left &= left - 1)
+    route_again<NQ32, GROUPS, BIAS>(a, m0 + (__ffs(left) - 1) / L, mine, raw);
+}
+
+// Any number of experts and groups of any size.
+__global__ void __launch_bounds__(256) k_route_any(const __grid_constant__ RouteArgs a) {
+  const int m = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (m >= a.M) return;
-  const int nq = (a.r.n_experts + 3) >> 2;
-  uint64_t* mine = slots + (size_t)warp * (6 * nq);  // 4 nq keys of 8 bytes, 4 nq logits
-  float* raw = reinterpret_cast<float*>(mine + 4 * nq);
-  if (!route_row<float>(a, m, reinterpret_cast<uint32_t*>(mine), raw)) {
-    __syncwarp();
-    route_row<double>(a, m, reinterpret_cast<unsigned long long*>(mine), raw);
+  float* raw;
+  uint64_t* mine = warp_slots(a, raw);
+  if (!route_row<float>(a, m, reinterpret_cast<uint32_t*>(mine), raw)) route_row64(a, m, mine, raw);
+}
+
+template <int L, int NQ>
+void run_regs(const RouteArgs& a, bool groups, int blocks, int threads, size_t smem,
+              cudaStream_t st) {
+  if (groups) {
+    if (a.bias) k_route_regs<L, NQ, true, true><<<blocks, threads, smem, st>>>(a);
+    else k_route_regs<L, NQ, true, false><<<blocks, threads, smem, st>>>(a);
+  } else {
+    if (a.bias) k_route_regs<L, NQ, false, true><<<blocks, threads, smem, st>>>(a);
+    else k_route_regs<L, NQ, false, false><<<blocks, threads, smem, st>>>(a);
   }
 }
 
@@ -351,14 +757,35 @@ cudaError_t launch_route_groups(const moeq_routing& r, const void* logits, int l
   a.M = M;
   a.lanes_per_group = 1;
   while (a.lanes_per_group * 2 * r.n_groups <= 32) a.lanes_per_group *= 2;
-  // 48 bytes per quad of experts and warp: 48 KB hold one row of 4096
   const int nq = (r.n_experts + 3) / 4;
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  int warps = (M + sms - 1) / sms;  // few rows: spread over the SMs first
+  const bool groups = r.topk_groups < r.n_groups;
+  const int gs = r.n_experts / r.n_groups, gq = gs / 4;
+  a.group_quads = gq;
+  const bool regs = nq <= 128 && !(groups && (gs % 4 || gq > 32 || (gq & (gq - 1))));
+  // Many rows of at most 128 (256) experts: four (two) rows share a warp, a
+  // lane holds four quads; the picks sit one per lane.
+  int lanes = 32;
+  if (regs && M > sms * 16) {
+    if (nq <= 32 && r.top_k <= 8 && !(groups && gq > 8)) lanes = 8;
+    else if (nq <= 64 && r.top_k <= 16 && !(groups && gq > 16)) lanes = 16;
+  }
+  const int rows = (M + 32 / lanes - 1) / (32 / lanes);  // warps
+  // 48 bytes per quad of experts and warp (48 KB hold one row of 4096),
+  // 384 at least for a row's candidates
+  const size_t slot = (size_t)(nq < 8 ? 8 : nq) * 48;
+  int warps = (rows + sms - 1) / sms;  // few rows: spread over the SMs first
   if (warps > 8) warps = 8;
-  while (warps > 1 && (size_t)warps * nq * 48 > 48 * 1024) --warps;
-  k_route_groups<<<(M + warps - 1) / warps, warps * 32, (size_t)warps * nq * 48, st>>>(a);
+  while (warps > 1 && warps * slot > 48 * 1024) --warps;
+  const int blocks = (rows + warps - 1) / warps, threads = warps * 32;
+  const size_t smem = warps * slot;
+  if (!regs) k_route_any<<<blocks, threads, smem, st>>>(a);
+  else if (lanes == 8) run_regs<8, 4>(a, groups, blocks, threads, smem, st);
+  else if (lanes == 16) run_regs<16, 4>(a, groups, blocks, threads, smem, st);
+  else if (nq <= 32) run_regs<32, 1>(a, groups, blocks, threads, smem, st);
+  else if (nq <= 64) run_regs<32, 2>(a, groups, blocks, threads, smem, st);
+  else run_regs<32, 4>(a, groups, blocks, threads, smem, st);
   return cudaGetLastError();
 }
 
