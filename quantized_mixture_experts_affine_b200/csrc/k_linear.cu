@@ -1,6 +1,6 @@
 // Linear with few tokens: y = x W^T on the packed codes, exact products.
 //
-// A warp owns 16 MT rows of W and a run of columns; mma.m16n8k16 (bf16,
+// A warp owns 16 rows of W and a run of columns; mma.m16n8k16 (bf16,
 // fp32 sums) multiplies the codes, which bf16 holds exactly (integers to
 // 255, or E2M1 values), with eight tokens at a time.  The codes go from
 // global memory straight into the fragments: the order of the columns
@@ -116,13 +116,11 @@ __device__ __forceinline__ void to_pairs(const uint32_t (&w)[Run<BITS, C>::WORDS
   }
 }
 
-// C tokens values from column c0 as bf16 pairs in the codes' pair order.
-template <int BITS, int C>
-__device__ __forceinline__ void load_x(const void* row, int type, int64_t c0,
-                                       uint32_t (&b)[C / 2]) {
-  uint32_t x[C / 2];
-  if (type == MOEQ_BF16) {
-    const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(row) + c0);
+// A lane's C token values from column c0, as loaded (8-bit: in the first words).
+template <int C>
+__device__ __forceinline__ void load_x(const char* row, bool bf16, int c0, uint32_t (&x)[C / 2]) {
+  if (bf16) {
+    const uint4* p = reinterpret_cast<const uint4*>(row + 2 * (int64_t)c0);
 #pragma unroll
     for (int i = 0; i < C / 8; ++i) {
       const uint4 v = p[i];
@@ -132,18 +130,31 @@ __device__ __forceinline__ void load_x(const void* row, int type, int64_t c0,
       x[4 * i + 3] = v.w;
     }
   } else {
-    const uint2* p = reinterpret_cast<const uint2*>(reinterpret_cast<const uint8_t*>(row) + c0);
+    const uint2* p = reinterpret_cast<const uint2*>(row + c0);
 #pragma unroll
     for (int i = 0; i < C / 8; ++i) {
       const uint2 v = p[i];
-      if (type == MOEQ_I8) {
-        bytes_to_bf16(v.x ^ 0x80808080u, 8388736.0f, x[4 * i], x[4 * i + 1]);
-        bytes_to_bf16(v.y ^ 0x80808080u, 8388736.0f, x[4 * i + 2], x[4 * i + 3]);
-      } else {
-        e4m3_to_bf16(v.x, x[4 * i], x[4 * i + 1]);
-        e4m3_to_bf16(v.y, x[4 * i + 2], x[4 * i + 3]);
-      }
+      x[2 * i] = v.x;
+      x[2 * i + 1] = v.y;
     }
+  }
+}
+
+// The same as bf16 pairs in the codes' pair order.
+template <int BITS, int C>
+__device__ __forceinline__ void x_pairs(const uint32_t (&raw)[C / 2], int type,
+                                        uint32_t (&b)[C / 2]) {
+  uint32_t x[C / 2];
+  if (type == MOEQ_BF16) {
+#pragma unroll
+    for (int i = 0; i < C / 2; ++i) x[i] = raw[i];
+  } else if (type == MOEQ_I8) {
+#pragma unroll
+    for (int i = 0; i < C / 4; ++i)
+      bytes_to_bf16(raw[i] ^ 0x80808080u, 8388736.0f, x[2 * i], x[2 * i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < C / 4; ++i) e4m3_to_bf16(raw[i], x[2 * i], x[2 * i + 1]);
   }
 #pragma unroll
   for (int i = 0; i < C / 8; ++i) {
@@ -159,128 +170,131 @@ __device__ __forceinline__ void load_x(const void* row, int type, int64_t c0,
   }
 }
 
-// grid.x: blocks of 16 MT rows; grid.y: blocks of 8 NT tokens.  The eight
-// warps split the spans; their sums are added in warp order.
-template <int BITS, bool MX, int C, int MT, int NT>
-__global__ void __launch_bounds__(kWarps * 32) k_linear_small(const __grid_constant__ LinArgs l) {
+// grid.x: blocks of 16 rows; grid.y: blocks of 8 NT tokens.  The warps split
+// the spans; their sums are added in warp order.  A warp asks for everything
+// of U spans before it uses the first, so that its run of a 4096-column row
+// costs one trip to memory.
+template <int BITS, bool MX, int C, int NT, int U>
+__global__ void __launch_bounds__(kWarps * 32, 2) k_linear_small(const __grid_constant__ LinArgs l) {
   constexpr int W = Run<BITS, C>::WORDS;
-  constexpr int ROWS = 16 * MT, TOKS = 8 * NT;
-  __shared__ float red[kWarps][ROWS][TOKS + 1];
+  constexpr int TOKS = 8 * NT;
+  __shared__ float red[kWarps][16][TOKS + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int o0 = blockIdx.x * ROWS;
+  const int o0 = blockIdx.x * 16;
   const int64_t m0 = (int64_t)blockIdx.y * TOKS;
   const int spans = l.in_dim / (4 * C);
-  const int sp0 = (int)((int64_t)spans * warp / kWarps);
-  const int sp1 = (int)((int64_t)spans * (warp + 1) / kWarps);
+  const int sp0 = spans * warp / kWarps, sp1 = spans * (warp + 1) / kWarps;
   const int64_t words_per_row = (int64_t)l.in_dim * BITS / 32;
-  const int groups = l.in_dim / l.G;
+  // spans per group: 1, or 2 (64-column spans in groups of 128)
+  const int shift = l.G == 4 * C ? 0 : 1;
+  const int groups = spans >> shift;
+  const bool bf16 = l.a.x_type == MOEQ_BF16;
+  const bool by128 = !bf16 && l.a.x_group == 128;
+  const int xsg = (l.in_dim + 127) / 128;
 
-  const uint32_t* wrow[MT][2];
-  const uint16_t* srow[MT][2];
-  const uint16_t* brow[MT][2];
+  const uint32_t* wrow[2];
+  int64_t srow[2];
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t r = min(o0 + 16 * i + 8 * h + g, l.out_dim - 1);
-      wrow[i][h] = l.w + r * words_per_row;
-      srow[i][h] = MX ? reinterpret_cast<const uint16_t*>(
-                            reinterpret_cast<const uint8_t*>(l.scales) + r * groups)
-                      : l.scales + r * groups;
-      brow[i][h] = MX ? nullptr : l.biases + r * groups;
-    }
+  for (int h = 0; h < 2; ++h) {
+    const int64_t r = min(o0 + 8 * h + g, l.out_dim - 1);
+    wrow[h] = l.w + r * words_per_row;
+    srow[h] = r * groups;
+  }
   const char* xrow[NT];
-  const size_t item = l.a.x_type == MOEQ_BF16 ? 2 : 1;
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const int64_t m = min(m0 + 8 * n + g, (int64_t)l.M - 1);
-    xrow[n] = reinterpret_cast<const char*>(l.a.x) + m * l.a.x_stride * item;
+    xrow[n] = reinterpret_cast<const char*>(l.a.x) + m * l.a.x_stride * (bf16 ? 2 : 1);
   }
-  const bool by128 = l.a.x_type != MOEQ_BF16 && l.a.x_group == 128;
-  const int xsg = (l.in_dim + 127) / 128;
 
-  float y[MT][NT][4] = {};
-  for (int sp = sp0; sp < sp1; ++sp) {
-    const int grp = sp * (4 * C) / l.G;
-    float s[MT][2], b[MT][2];
-    uint32_t a[MT][2][C / 2];
+  float y[NT][4] = {};
+#pragma unroll 1
+  for (int base = sp0; base < sp1; base += U) {
+    uint32_t w[U][2][W], x[U][NT][C / 2];
+    uint32_t s[U][2], b[U][2];
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int u = 0; u < U; ++u) {
+      const int sp = min(base + u, sp1 - 1), grp = sp >> shift;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t w[W];
-        load_run<BITS, C>(wrow[i][h], sp, t, w);
+        load_run<BITS, C>(wrow[h], sp, t, w[u][h]);
         if (MX) {
-          s[i][h] = mx_scale(reinterpret_cast<const uint8_t*>(srow[i][h])[grp]);
+          s[u][h] = reinterpret_cast<const uint8_t*>(l.scales)[srow[h] + grp];
         } else {
-          s[i][h] = bf16_bits_to_float(srow[i][h][grp]);
-          b[i][h] = bf16_bits_to_float(brow[i][h][grp]);
+          s[u][h] = l.scales[srow[h] + grp];
+          b[u][h] = l.biases[srow[h] + grp];
         }
-        to_pairs<BITS, MX, C>(w, a[i][h]);
       }
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      uint32_t x[C / 2];
-      load_x<BITS, C>(xrow[n], l.a.x_type, (int64_t)sp * (4 * C) + t * C, x);
-      float xs[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (!MX) {
-        const uint32_t one = 0x3F803F80u;
+      for (int n = 0; n < NT; ++n) load_x<C>(xrow[n], bf16, sp * (4 * C) + t * C, x[u][n]);
+    }
 #pragma unroll
-        for (int j = 0; j < C / 4; ++j) mma_bf16(xs, one, one, one, one, x[2 * j], x[2 * j + 1]);
-      }
-      float f0 = 1.0f, f1 = 1.0f;
-      if (by128) {
-        const int64_t c = sp * (4 * C) / 128;
-        const int64_t ma = min(m0 + 8 * n + 2 * t, (int64_t)l.M - 1);
-        const int64_t mb = min(m0 + 8 * n + 2 * t + 1, (int64_t)l.M - 1);
-        f0 = l.a.x_scales[ma * xsg + c];
-        f1 = l.a.x_scales[mb * xsg + c];
+    for (int u = 0; u < U; ++u) {
+      if (base + u >= sp1) break;
+      uint32_t a[2][C / 2];
+      float sf[2], bf[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        to_pairs<BITS, MX, C>(w[u][h], a[h]);
+        sf[h] = MX ? mx_scale(s[u][h]) : __uint_as_float(s[u][h] << 16);
+        bf[h] = MX ? 0.0f : __uint_as_float(b[u][h] << 16);
       }
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        float q[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int n = 0; n < NT; ++n) {
+        uint32_t xb[C / 2];
+        x_pairs<BITS, C>(x[u][n], l.a.x_type, xb);
+        float q[4] = {0.0f, 0.0f, 0.0f, 0.0f}, xs[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int j = 0; j < C / 4; ++j)
-          mma_bf16(q, a[i][0][2 * j], a[i][1][2 * j], a[i][0][2 * j + 1], a[i][1][2 * j + 1],
-                   x[2 * j], x[2 * j + 1]);
+        for (int j = 0; j < C / 4; ++j) {
+          mma_bf16(q, a[0][2 * j], a[1][2 * j], a[0][2 * j + 1], a[1][2 * j + 1], xb[2 * j],
+                   xb[2 * j + 1]);
+          if (!MX) {
+            const uint32_t one = 0x3F803F80u;
+            mma_bf16(xs, one, one, one, one, xb[2 * j], xb[2 * j + 1]);
+          }
+        }
+        float f[2] = {1.0f, 1.0f};
+        if (by128) {
+          const int64_t c = (int64_t)(base + u) * (4 * C) >> 7;
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            f[i] = l.a.x_scales[min(m0 + 8 * n + 2 * t + i, (int64_t)l.M - 1) * xsg + c];
+        }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          float v = s[i][k >> 1] * q[k];
-          if (!MX) v = __fmaf_rn(b[i][k >> 1], xs[k], v);
-          y[i][n][k] = by128 ? __fmaf_rn(k & 1 ? f1 : f0, v, y[i][n][k]) : y[i][n][k] + v;
+          float v = sf[k >> 1] * q[k];
+          if (!MX) v = __fmaf_rn(bf[k >> 1], xs[k], v);
+          y[n][k] = by128 ? __fmaf_rn(f[k & 1], v, y[n][k]) : y[n][k] + v;
         }
       }
     }
   }
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        red[warp][16 * i + 8 * (k >> 1) + g][8 * n + 2 * t + (k & 1)] = y[i][n][k];
+    for (int k = 0; k < 4; ++k) red[warp][8 * (k >> 1) + g][8 * n + 2 * t + (k & 1)] = y[n][k];
   __syncthreads();
-  for (int i = threadIdx.x; i < ROWS * TOKS; i += kWarps * 32) {
-    const int row = i % ROWS, tok = i / ROWS;
+  if (threadIdx.x < 16 * TOKS) {
+    const int row = threadIdx.x & 15, tok = threadIdx.x >> 4;
     const int64_t m = m0 + tok;
-    if (m >= l.M || o0 + row >= l.out_dim) continue;
-    float v = 0.0f;
+    if (m < l.M && o0 + row < l.out_dim) {
+      float v = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k) v += red[k][row][tok];
-    if (l.a.x_type != MOEQ_BF16 && l.a.x_group == 0) v *= l.a.x_scales[m];
-    finish(l.a, m, o0 + row, v);
+      for (int k = 0; k < kWarps; ++k) v += red[k][row][tok];
+      if (!bf16 && !by128) v *= l.a.x_scales[m];
+      finish(l.a, m, o0 + row, v);
+    }
   }
 }
 
 template <int BITS, bool MX, int C>
 cudaError_t run(const LinArgs& l, cudaStream_t st) {
-  if (l.M <= 8) {
-    const dim3 grid((l.out_dim + 15) / 16, 1);
-    k_linear_small<BITS, MX, C, 1, 1><<<grid, kWarps * 32, 0, st>>>(l);
-  } else {
-    const dim3 grid((l.out_dim + 31) / 32, (l.M + 15) / 16);
-    k_linear_small<BITS, MX, C, 2, 2><<<grid, kWarps * 32, 0, st>>>(l);
-  }
+  const int blocks = (l.out_dim + 15) / 16;
+  if (l.M <= 8)
+    k_linear_small<BITS, MX, C, 1, 4><<<blocks, kWarps * 32, 0, st>>>(l);
+  else
+    k_linear_small<BITS, MX, C, 2, 2>
+        <<<dim3(blocks, (l.M + 15) / 16), kWarps * 32, 0, st>>>(l);
   return cudaGetLastError();
 }
 

@@ -104,13 +104,11 @@ __device__ __forceinline__ double mag_value(unsigned long long k) {
   return (double)__uint_as_float((uint32_t)(k >> 32)) + (double)rest;
 }
 
-// Codes of one value from fp64 (the value next to a border, or tiny maxima).
-__device__ __noinline__ uint32_t code_i8_64(float r, float g, double a) {
-  const double v = (double)r * (double)g * 127.0 / a;
-  return (uint32_t)(int)rint(fmin(fmax(v, -127.0), 127.0)) & 255u;
-}
-__device__ __noinline__ uint32_t code_e4m3_64(float r, float g, double a) {
-  const double v = (double)r * (double)g * 448.0 / a;
+// Code of one value from fp64: the value next to a border, or a tiny maximum.
+__device__ __forceinline__ uint32_t code64(bool i8, float r, float g, double a) {
+  if (r * g == 0.0f) return 0u;
+  const double v = (double)r * (double)g * (i8 ? 127.0 : 448.0) / a;
+  if (i8) return (uint32_t)(int)rint(fmin(fmax(v, -127.0), 127.0)) & 255u;
   int e = (int)((__double_as_longlong(v) >> 52) & 2047) - 1023;
   if (e < -6) e = -6;
   const double step = __longlong_as_double((long long)(e - 3 + 1023) << 52);
@@ -118,99 +116,82 @@ __device__ __noinline__ uint32_t code_e4m3_64(float r, float g, double a) {
   return __nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
 }
 
+// gamma's eight values from their bf16 pairs.
+__device__ __forceinline__ void unpack8(const uint4& w, float (&g)[8]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    g[2 * i] = __uint_as_float(u[i] << 16);
+    g[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+  }
+}
+
+// `code` with the bytes that differ from `other` (all of them for a tiny
+// maximum) decided in fp64; a: the exact largest |r gamma|.
+__device__ __noinline__ uint2 settle(bool i8, uint2 code, uint2 other, bool tiny, float r0,
+                                     float r1, float r2, float r3, float r4, float r5, float r6,
+                                     float r7, uint4 gp, double a) {
+  const float r[8] = {r0, r1, r2, r3, r4, r5, r6, r7};
+  float g[8];
+  unpack8(gp, g);
+  uint32_t out[2] = {code.x, code.y};
+  const uint32_t diff[2] = {code.x ^ other.x, code.y ^ other.y};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int sh = 8 * (j & 3);
+    if (tiny || ((diff[j / 4] >> sh) & 255u))
+      out[j / 4] = (out[j / 4] & ~(255u << sh)) | code64(i8, r[j], g[j], a) << sh;
+  }
+  return make_uint2(out[0], out[1]);
+}
+
 // fp32 cannot hold top / a below this (and r gamma may have lost bits)
 constexpr float kTinyMax = 1e-28f;
 
-// The eight codes of a vector from values (r, g) of a group with maximum mk.
-__device__ __forceinline__ uint2 codes8(int type, const float (&r)[8], const float (&g)[8],
-                                        unsigned long long mk) {
-  const float am = __uint_as_float((uint32_t)(mk >> 32));
-  if (!(am < INFINITY)) return make_uint2(0u, 0u);
-  const bool i8 = type == MOEQ_I8;
-  const float f = __fdiv_rn(i8 ? 127.0f : 448.0f, am);
-  float c[8];
-  bool doubt[8], any = false;
+// Eight codes of t f in fp32.
+__device__ __forceinline__ uint2 codes8(bool i8, const float (&t)[8], float f) {
   uint32_t out[2];
   if (i8) {
+    // t f + 1.5 2^23 rounds t f to the nearest whole number, in the low bits
     uint32_t q[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      c[j] = r[j] * g[j] * f;
-      const float v = rintf(c[j]);
-      q[j] = (uint32_t)__float2int_rn(v);
-      // fp32's error of c: 4 roundings, 127 * 4 * 2^-24 < 3.1e-5
-      doubt[j] = fabsf(fabsf(c[j] - v) - 0.5f) < 6e-5f;
-      any |= doubt[j];
-    }
+    for (int j = 0; j < 8; ++j) q[j] = __float_as_uint(__fmaf_rn(t[j], f, 12582912.0f));
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       out[h] = __byte_perm(__byte_perm(q[4 * h], q[4 * h + 1], 0x0040u),
                            __byte_perm(q[4 * h + 2], q[4 * h + 3], 0x0040u), 0x5410u);
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      c[j] = r[j] * g[j] * f;
-      // a border has the fraction bits below e4m3's three at exactly one half;
-      // below 2^-6 (subnormal codes) fp64 decides
-      const uint32_t low = __float_as_uint(c[j]) & 0xFFFFFu;
-      doubt[j] = (low - 0x7FFF0u) <= 0x20u || (fabsf(c[j]) < 0.015625f && c[j] != 0.0f);
-      any |= doubt[j];
-    }
-#pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(c[4 * h], c[4 * h + 1]),
+      const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(t[4 * h] * f, t[4 * h + 1] * f),
                                                   __NV_SATFINITE, __NV_E4M3);
-      const uint32_t b = __nv_cvt_float2_to_fp8x2(make_float2(c[4 * h + 2], c[4 * h + 3]),
-                                                  __NV_SATFINITE, __NV_E4M3);
+      const uint32_t b = __nv_cvt_float2_to_fp8x2(
+          make_float2(t[4 * h + 2] * f, t[4 * h + 3] * f), __NV_SATFINITE, __NV_E4M3);
       out[h] = a | b << 16;
     }
-  }
-  const bool tiny = am < kTinyMax;
-  if (any || tiny) {
-    const double a64 = mag_value(mk);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (doubt[j] || tiny) {
-        const uint32_t k = r[j] * g[j] == 0.0f ? 0u
-                           : i8                ? code_i8_64(r[j], g[j], a64)
-                                               : code_e4m3_64(r[j], g[j], a64);
-        out[j / 4] = (out[j / 4] & ~(255u << (8 * (j & 3)))) | k << (8 * (j & 3));
-      }
   }
   return make_uint2(out[0], out[1]);
 }
 
-// Largest |r gamma| of a thread's eight values as a key (see mag_key).  SHORT:
-// r is a bf16, so r gamma is exact in fp32 and nothing is left over.
-template <bool SHORT>
-__device__ __forceinline__ unsigned long long max8(const float (&r)[8], const float (&g)[8]) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j)
-    top = max(top, __float_as_uint(r[j] * g[j]) & 0x7FFFFFFFu);  // a NaN is largest
-  if (SHORT) return ((unsigned long long)top << 32) | 0x80000000u;
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// Largest |r gamma| of a thread's eight values as a key (see mag_key).
+__device__ __forceinline__ unsigned long long max8_key(const float (&r)[8], const float (&g)[8]) {
   unsigned long long key = 0;
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if ((__float_as_uint(r[j] * g[j]) & 0x7FFFFFFFu) == top) {
-      const unsigned long long k = mag_key(r[j], g[j]);
-      key = k > key ? k : key;
-    }
+  for (int j = 0; j < 8; ++j) {
+    const unsigned long long k = mag_key(r[j], g[j]);
+    key = k > key ? k : key;
+  }
   return key;
 }
 
-template <bool SHORT, int FIRST>
-__device__ __forceinline__ unsigned long long max_lanes(unsigned long long k) {
-  if (SHORT) {
-    uint32_t t = (uint32_t)(k >> 32);
-    if (FIRST == 16) {
-      t = __reduce_max_sync(0xffffffffu, t);
-    } else {
-#pragma unroll
-      for (int o = FIRST; o > 0; o >>= 1) t = max(t, __shfl_xor_sync(0xffffffffu, t, o));
-    }
-    return ((unsigned long long)t << 32) | 0x80000000u;
-  }
+template <int FIRST>
+__device__ __forceinline__ unsigned long long lanes_max(unsigned long long k) {
 #pragma unroll
   for (int o = FIRST; o > 0; o >>= 1) {
     const unsigned long long p = __shfl_xor_sync(0xffffffffu, k, o);
@@ -218,105 +199,184 @@ __device__ __forceinline__ unsigned long long max_lanes(unsigned long long k) {
   }
   return k;
 }
+template <int FIRST>
+__device__ __forceinline__ float lanes_max(float k) {
+#pragma unroll
+  for (int o = FIRST; o > 0; o >>= 1) k = max_nan(k, __shfl_xor_sync(0xffffffffu, k, o));
+  return k;
+}
 
-// MAXT: threads of the largest block of this variant.
-template <int NV, bool SHORT, int MAXT>
+// NV: vectors of a thread.  XT, RT: moeq_dtype of x and of the residual (RT
+// kNone: there is none), for rows of whole, aligned vectors; kAny: any.
+// MAXT: threads of the largest block.
+constexpr int kAny = -1, kNone = -2;
+
+template <int NV, int XT, int RT, int MAXT>
 __global__ void __launch_bounds__(MAXT) k_add_rmsnorm(const __grid_constant__ NormArgs a) {
-  __shared__ float red[32];
-  __shared__ unsigned long long red_max[32];
+  constexpr bool ANY = XT == kAny;
+  __shared__ float red[32], red_max[32];
+  __shared__ unsigned long long red_key[32];
   const moeq_norm_args& n = a.n;
   const int T = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = T >> 5;
   const int64_t m = blockIdx.x;
-  const bool whole = n.q && n.q_group == 0;
-  float r[NV][8], g[NV][8];
-  float ss = 0.0f;
+  const int xt = ANY ? n.x_type : XT, rt = ANY ? n.r_type : RT;
+  const bool res = ANY ? n.residual != nullptr : RT != kNone;
+  // r gamma of a bf16 stream (8 + 8 bits) is exact in fp32
+  const bool exact = (res ? rt : xt) == MOEQ_BF16;
+  const bool whole = n.q && n.q_group == 0, i8 = n.q_type == MOEQ_I8;
+  auto count = [&](int i) -> int {
+    const int v = tid + i * T;
+    return v >= a.vecs ? 0 : ANY ? min(8, a.H - 8 * v) : 8;
+  };
+  float r[NV][8];
+  uint4 gp[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int v = tid + i * T;
-    const int cnt = v < a.vecs ? min(8, a.H - 8 * v) : 0;
-    load8(n.x, n.x_type, m * n.x_stride + 8 * v, cnt, a.vx, r[i]);
-    if (n.residual) {
-      float s[8];
-      load8(n.residual, n.r_type, m * n.r_stride + 8 * v, cnt, a.vr, s);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        r[i][j] += s[j];
-        // the norm is of the stream as it is stored
-        if (n.r_type == MOEQ_BF16) r[i][j] = __bfloat162float(__float2bfloat16_rn(r[i][j]));
-      }
-    }
-    load8(n.gamma, MOEQ_BF16, 8 * v, cnt, a.vg, g[i]);
+    const int v = tid + i * T, cnt = count(i);
+    load8(n.x, xt, m * n.x_stride + 8 * v, cnt, !ANY || a.vx, r[i]);
   }
-  unsigned long long row_max = 0;
+  float s[NV][8];
+  if (res) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      load8(n.residual, rt, m * n.r_stride + 8 * (tid + i * T), count(i), !ANY || a.vr, s[i]);
+  }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int v = tid + i * T;
-    const int cnt = v < a.vecs ? min(8, a.H - 8 * v) : 0;
-    if (n.r_out && cnt > 0)
-      store8(n.r_out, n.r_type, m * n.r_out_stride + 8 * v, cnt, a.vro, r[i]);
+    const int v = tid + i * T, cnt = count(i);
+    gp[i] = make_uint4(0u, 0u, 0u, 0u);
+    if ((!ANY || a.vg) && cnt == 8) {
+      gp[i] = *reinterpret_cast<const uint4*>(n.gamma + 8 * v);
+    } else if (ANY) {
+      uint32_t h[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[j] = j < cnt ? n.gamma[8 * v + j] : 0u;
+      gp[i] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16,
+                         h[6] | h[7] << 16);
+    }
+  }
+  if (res) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) r[i][j] += s[i][j];
+      // the norm is of the stream as it is stored
+      if (rt == MOEQ_BF16) {
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          const uint32_t p = bf16_pair(r[i][j], r[i][j + 1]);
+          r[i][j] = __uint_as_float(p << 16);
+          r[i][j + 1] = __uint_as_float(p & 0xFFFF0000u);
+        }
+      }
+      const int cnt = count(i);
+      if (n.r_out && cnt > 0)
+        store8(n.r_out, rt, m * n.r_out_stride + 8 * (tid + i * T), cnt, !ANY || a.vro, r[i]);
+    }
+  }
+  float ss = 0.0f, row_max = 0.0f;
+  unsigned long long row_key = 0;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) ss = __fmaf_rn(r[i][j], r[i][j], ss);
     if (whole) {
-      const unsigned long long k = max8<SHORT>(r[i], g[i]);
-      row_max = k > row_max ? k : row_max;
+      float g[8];
+      unpack8(gp[i], g);
+      if (exact) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) row_max = max_nan(row_max, fabsf(r[i][j] * g[j]));
+      } else {
+        const unsigned long long k = max8_key(r[i], g);
+        row_key = k > row_key ? k : row_key;
+      }
     }
   }
   ss = warp_sum(ss);
-  if (whole) row_max = max_lanes<SHORT, 16>(row_max);
-  if (lane == 0) {
-    red[warp] = ss;
-    red_max[warp] = row_max;
+  if (whole) {
+    if (exact) row_max = lanes_max<16>(row_max);
+    else row_key = lanes_max<16>(row_key);
   }
-  __syncthreads();
-  ss = 0.0f;
-  for (int i = 0; i < nw; ++i) {
-    ss += red[i];
-    row_max = red_max[i] > row_max ? red_max[i] : row_max;
+  if (nw > 1) {
+    if (lane == 0) {
+      red[warp] = ss;
+      red_max[warp] = row_max;
+      red_key[warp] = row_key;
+    }
+    __syncthreads();
+    ss = 0.0f;
+    for (int i = 0; i < nw; ++i) ss += red[i];
+    if (whole) {
+      if (exact) {
+        for (int i = 0; i < nw; ++i) row_max = max_nan(row_max, red_max[i]);
+      } else {
+        for (int i = 0; i < nw; ++i) row_key = red_key[i] > row_key ? red_key[i] : row_key;
+      }
+    }
   }
+  if (whole && !exact) row_max = __uint_as_float((uint32_t)(row_key >> 32));
   const float inv = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss, (float)a.H) + n.eps));
+  const float top = i8 ? 127.0f : 448.0f;
 
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int v = tid + i * T;
-    const int cnt = v < a.vecs ? min(8, a.H - 8 * v) : 0;
+    const int v = tid + i * T, cnt = count(i);
+    float g[8];
+    unpack8(gp[i], g);
     if (n.y && cnt > 0) {
       float o[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = r[i][j] * inv * g[i][j];
-      store8(n.y, MOEQ_BF16, m * n.y_stride + 8 * v, cnt, a.vy, o);
+      for (int j = 0; j < 8; ++j) o[j] = r[i][j] * inv * g[j];
+      store8(n.y, MOEQ_BF16, m * n.y_stride + 8 * v, cnt, !ANY || a.vy, o);
     }
-    if (n.q) {
-      // 16 neighbouring lanes hold 128 columns
-      const unsigned long long mk =
-          whole ? row_max : max_lanes<SHORT, 8>(max8<SHORT>(r[i], g[i]));
-      if (cnt > 0) {
-        if (whole ? v == 0 : (v & 15) == 0) {
-          const float am = __uint_as_float((uint32_t)(mk >> 32));
-          n.q_scales[m * a.n_scales + (whole ? 0 : v >> 4)] =
-              am < INFINITY ? __fdiv_rn(am * inv, n.q_type == MOEQ_I8 ? 127.0f : 448.0f)
-                            : __uint_as_float(0x7FC00000u);
-        }
-        const uint2 code = codes8(n.q_type, r[i], g[i], mk);
-        uint8_t* q = reinterpret_cast<uint8_t*>(n.q) + m * n.q_stride + 8 * v;
-        if (a.vq && cnt == 8) {
-          *reinterpret_cast<uint2*>(q) = code;
-        } else {
+    if (!n.q) continue;
+    float t[8], am = row_max;
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (j < cnt) q[j] = (uint8_t)((j < 4 ? code.x : code.y) >> (8 * (j & 3)));
-        }
+    for (int j = 0; j < 8; ++j) t[j] = r[i][j] * g[j];
+    if (!whole) {  // 16 neighbouring lanes hold 128 columns
+      am = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) am = max_nan(am, fabsf(t[j]));
+      am = lanes_max<8>(am);
+    }
+    // t f is off by 4 roundings at most (2^-22 relative); where moving it by
+    // 2^-20 either way changes a code, fp64 decides
+    const float f = __fdiv_rn(top, am);
+    uint2 code = codes8(i8, t, f * (1.0f + 9.5367431640625e-7f));
+    const uint2 other = codes8(i8, t, f * (1.0f - 9.5367431640625e-7f));
+    const bool finite = am < INFINITY, tiny = am < kTinyMax;
+    const bool doubt = finite && (tiny || code.x != other.x || code.y != other.y);
+    unsigned long long key = row_key;
+    if (!exact && !whole && __any_sync(0xffffffffu, doubt)) key = lanes_max<8>(max8_key(r[i], g));
+    if (doubt)
+      code = settle(i8, code, other, tiny, r[i][0], r[i][1], r[i][2], r[i][3], r[i][4], r[i][5],
+                    r[i][6], r[i][7], gp[i], exact ? (double)am : mag_value(key));
+    if (!finite) code = make_uint2(0u, 0u);
+    if (cnt > 0) {
+      if (whole ? v == 0 : (v & 15) == 0)
+        n.q_scales[m * a.n_scales + (whole ? 0 : v >> 4)] =
+            finite ? __fdiv_rn(am * inv, top) : __uint_as_float(0x7FC00000u);
+      uint8_t* q = reinterpret_cast<uint8_t*>(n.q) + m * n.q_stride + 8 * v;
+      if (!ANY || (a.vq && cnt == 8)) {
+        *reinterpret_cast<uint2*>(q) = code;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < cnt) q[j] = (uint8_t)((j < 4 ? code.x : code.y) >> (8 * (j & 3)));
       }
     }
   }
 }
 
-template <bool SHORT>
-void run(const NormArgs& a, int M, cudaStream_t st) {
+template <int XT, int RT>
+void run(const NormArgs& a, int M, int sms, cudaStream_t st) {
   const int warps = (a.vecs + 31) / 32;
-  if (warps <= 16) k_add_rmsnorm<1, SHORT, 512><<<M, warps * 32, 0, st>>>(a);
-  else if (warps <= 32) k_add_rmsnorm<2, SHORT, 512><<<M, (warps + 1) / 2 * 32, 0, st>>>(a);
-  else if (warps <= 64) k_add_rmsnorm<2, SHORT, 1024><<<M, (warps + 1) / 2 * 32, 0, st>>>(a);
-  else k_add_rmsnorm<4, SHORT, 1024><<<M, (warps + 3) / 4 * 32, 0, st>>>(a);
+  // Many rows: two vectors a thread, so that the reductions and addresses are
+  // paid less often; few rows: as many threads as vectors, for the latency.
+  if (warps <= 16 && M < 4 * sms)
+    k_add_rmsnorm<1, XT, RT, 512><<<M, warps * 32, 0, st>>>(a);
+  else if (warps <= 32) k_add_rmsnorm<2, XT, RT, 512><<<M, (warps + 1) / 2 * 32, 0, st>>>(a);
+  else k_add_rmsnorm<4, XT, RT, 1024><<<M, (warps + 3) / 4 * 32, 0, st>>>(a);
 }
 
 bool wide(const void* p, int64_t stride, int item, int bytes) {
@@ -338,9 +398,17 @@ cudaError_t launch_add_rmsnorm(const moeq_norm_args& n, int M, int H, cudaStream
   a.vg = wide(n.gamma, 0, 2, 16);
   a.vy = wide(n.y, n.y_stride, 2, 16);
   a.vq = wide(n.q, n.q_stride, 1, 8);
-  // a bf16 stream: r gamma has 16 bits
-  if ((n.residual ? n.r_type : n.x_type) == MOEQ_BF16) run<true>(a, M, st);
-  else run<false>(a, M, st);
+  const int sms = sm_count();
+  const bool vec = H % 8 == 0 && a.vx && a.vg && (!n.residual || a.vr) && (!n.r_out || a.vro) &&
+                   (!n.y || a.vy) && (!n.q || a.vq);
+  const bool xb = n.x_type == MOEQ_BF16, rb = n.r_type == MOEQ_BF16;
+  if (!vec) run<kAny, kAny>(a, M, sms, st);
+  else if (!n.residual && xb) run<MOEQ_BF16, kNone>(a, M, sms, st);
+  else if (!n.residual) run<MOEQ_F32, kNone>(a, M, sms, st);
+  else if (xb && rb) run<MOEQ_BF16, MOEQ_BF16>(a, M, sms, st);
+  else if (xb) run<MOEQ_BF16, MOEQ_F32>(a, M, sms, st);
+  else if (rb) run<MOEQ_F32, MOEQ_BF16>(a, M, sms, st);
+  else run<MOEQ_F32, MOEQ_F32>(a, M, sms, st);
   return cudaGetLastError();
 }
 
