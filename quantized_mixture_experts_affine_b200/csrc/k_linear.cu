@@ -23,48 +23,6 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Words that hold a lane's C codes: its run may start inside a word when the
-// width does not divide 32.
-template <int BITS, int C>
-struct Run {
-  static constexpr int BITLEN = BITS * C;
-  static constexpr int WORDS = BITLEN % 32 == 0 ? BITLEN / 32 : BITLEN / 32 + 1;
-};
-
-// Loads lane t's run of C codes of the span that starts at bit 4 C BITS sp of
-// the row, in its first words from bit 0 on.  The words read lie in the span.
-template <int BITS, int C>
-__device__ __forceinline__ void load_run(const uint32_t* row, int sp, int t,
-                                         uint32_t (&w)[Run<BITS, C>::WORDS]) {
-  constexpr int BL = Run<BITS, C>::BITLEN, W = Run<BITS, C>::WORDS;
-  if (BL % 32 == 0) {
-    const uint32_t* p = row + (int64_t)sp * (4 * W) + t * W;
-    if (W == 4) {
-      const uint4 v = *reinterpret_cast<const uint4*>(p);
-      w[0] = v.x;
-      w[1] = v.y;
-      w[2] = v.z;
-      w[W - 1] = v.w;
-    } else if (W == 2) {
-      const uint2 v = *reinterpret_cast<const uint2*>(p);
-      w[0] = v.x;
-      w[W - 1] = v.y;
-    } else {
-#pragma unroll
-      for (int i = 0; i < W; ++i) w[i] = p[i];
-    }
-    return;
-  }
-  const int bit = t * BL, first = bit >> 5, off = bit & 31;
-  const uint32_t* p = row + (int64_t)sp * (4 * BL / 32) + first;
-  const int last = 4 * BL / 32 - 1 - first;  // words of the span behind the first
-  uint32_t raw[W + 1];
-#pragma unroll
-  for (int i = 0; i <= W; ++i) raw[i] = i <= last && 32 * i < off + BL ? p[i] : 0u;
-#pragma unroll
-  for (int i = 0; i < W; ++i) w[i] = __funnelshift_r(raw[i], raw[i + 1], off);
-}
-
 // The run as bf16 pairs.  Pair order: widths of 2 and 4 bits (and MX) pair
 // values i and i + 4 of each eight, the others neighbours.
 template <int BITS>
@@ -207,6 +165,20 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_linear_small(const __grid_co
     xrow[n] = reinterpret_cast<const char*>(l.a.x) + m * l.a.x_stride * (bf16 ? 2 : 1);
   }
 
+  // The run's codes and scales into L2 while the first loads are on their way,
+  // and what the epilogue needs: nothing later waits for DRAM.
+  if (sp1 > sp0 + U) {
+    const char* p = reinterpret_cast<const char*>(wrow[t >> 1] + (int64_t)sp0 * (C * BITS / 8));
+    const char* e = p + (int64_t)(sp1 - sp0) * (C * BITS / 2);
+    for (const char* c = p + 128 * (t & 1); c < e; c += 256)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(c));
+  }
+  const int erow = threadIdx.x & 15, etok = threadIdx.x >> 4;
+  const int64_t em = m0 + etok;
+  const bool mine = threadIdx.x < 16 * TOKS && em < l.M && o0 + erow < l.out_dim;
+  Epilogue ep;
+  if (mine) ep.load(l.a, em, o0 + erow);
+
   float y[NT][4] = {};
 #pragma unroll 1
   for (int base = sp0; base < sp1; base += U) {
@@ -274,16 +246,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_linear_small(const __grid_co
 #pragma unroll
     for (int k = 0; k < 4; ++k) red[warp][8 * (k >> 1) + g][8 * n + 2 * t + (k & 1)] = y[n][k];
   __syncthreads();
-  if (threadIdx.x < 16 * TOKS) {
-    const int row = threadIdx.x & 15, tok = threadIdx.x >> 4;
-    const int64_t m = m0 + tok;
-    if (m < l.M && o0 + row < l.out_dim) {
-      float v = 0.0f;
+  if (mine) {
+    float v = 0.0f;
 #pragma unroll
-      for (int k = 0; k < kWarps; ++k) v += red[k][row][tok];
-      if (!bf16 && !by128) v *= l.a.x_scales[m];
-      finish(l.a, m, o0 + row, v);
-    }
+    for (int k = 0; k < kWarps; ++k) v += red[k][erow][etok];
+    if (!bf16 && !by128) v *= ep.x_scale;
+    ep.finish(l.a, em, o0 + erow, v);
   }
 }
 

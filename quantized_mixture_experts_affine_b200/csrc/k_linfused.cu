@@ -25,9 +25,13 @@ struct FusedLinArgs {
   CUtensorMap tm_x;  // fp16 tokens, boxes of 64 columns x n rows
   LinArgs l;
   const float* fx;
+  const float* fw;
   int n;        // tokens per CTA, a multiple of 16, at most 256
   int stages;
+  int per;       // 64-column blocks of a stage
+  int own_sums;  // the partial sums have a place behind the stages
   int k_blocks;
+  int log2_split, log2_group, tmem_cols;
   int* status;
 };
 
@@ -41,107 +45,208 @@ __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ float lds_f32(uint32_t a) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
 __device__ __forceinline__ void sts128(uint32_t a, const uint32_t (&v)[4]) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v[0]), "r"(v[1]),
                "r"(v[2]), "r"(v[3])
                : "memory");
 }
-__device__ __forceinline__ float ld_cluster(uint32_t a) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-  return v;
+__device__ __forceinline__ void st_cluster(uint32_t a, uint32_t v) {
+  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 
-// The 32 codes in BITS words, as bytes in order (MX: 2 e2m1 + 12).
-template <int BITS, bool MX>
-__device__ __forceinline__ void to_bytes(const uint32_t (&w)[BITS], uint32_t (&c)[8]) {
-  if (BITS == 8) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = w[i < BITS ? i : 0];
-  } else if (BITS == 4) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t e = w[i < BITS ? i : 0] & 0x0F0F0F0Fu;
-      uint32_t o = (w[i < BITS ? i : 0] >> 4) & 0x0F0F0F0Fu;
-      if (MX) {
-        e = mx_q8(e);
-        o = mx_q8(o);
-      }
-      c[2 * i] = __byte_perm(e, o, 0x5140u);
-      c[2 * i + 1] = __byte_perm(e, o, 0x7362u);
-    }
-  } else if (BITS == 2) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t v = (w[i / 4] >> (8 * (i & 3))) & 255u;
-      const uint32_t x = (v | (v << 12)) & 0x000F000Fu;
-      c[i] = (x | (x << 6)) & 0x03030303u;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      constexpr int GB = 4 * BITS % 32;
-      const int bit = 4 * BITS * i, k = bit / 32, off = bit % 32;
-      const uint32_t hi = k + 1 < BITS ? w[k + 1 < BITS ? k + 1 : 0] : 0u;
-      c[i] = Chunk<BITS>::spread4(__funnelshift_r(w[k], hi, off) & ((1u << GB) - 1u));
-    }
-  }
+// 32 lanes x 16 columns of TMEM.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
 }
 
+// 32 lanes x 8 columns of TMEM.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                 "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+
+// Four codes of a 16-code run (from 4 i on) as bytes in order.
 template <int BITS>
-__device__ __forceinline__ void load32(const uint32_t* p, bool ok, uint32_t (&w)[BITS]) {
+__device__ __forceinline__ uint32_t bytes4(const uint32_t (&w)[Run<BITS, 16>::WORDS], int i) {
+  constexpr int W = Run<BITS, 16>::WORDS;
+  if (BITS == 8) return w[i < W ? i : 0];
+  const int bit = 4 * BITS * i, k = bit / 32, off = bit % 32;
+  const uint32_t lo = w[k < W ? k : 0], hi = k + 1 < W ? w[k + 1 < W ? k + 1 : 0] : 0u;
+  const uint32_t v = __funnelshift_r(lo, hi, off);
+  if (BITS == 4) {
+    const uint32_t x = (v & 0xFFu) | ((v & 0xFF00u) << 8);  // two codes per half
+    return (x & 0x000F000Fu) | ((x & 0x00F000F0u) << 4);
+  }
+  if (BITS == 2) {
+    const uint32_t x = (v & 0xFu) | ((v & 0xF0u) << 12);
+    return (x & 0x00030003u) | ((x & 0x000C000Cu) << 6);
+  }
+  constexpr int GB = 4 * BITS % 32;
+  return Chunk<BITS>::spread4(v & ((1u << GB) - 1u));
+}
+
+// Codes 8 i .. 8 i + 7 of a run as fp16 values q s + b, one rounding, in the
+// columns' order of the tokens' layout: widths of 2 and 4 bits pair columns j
+// and j + 4, which lets one mask cut both out of a word (1024 + 2^k q is an
+// fp16 with q in its mantissa), the others neighbours.
+template <int BITS, bool MX>
+__device__ __forceinline__ void halves8(const uint32_t (&w)[Run<BITS, 16>::WORDS], int i,
+                                        uint32_t s, uint32_t b, uint32_t (&v)[4]) {
+  constexpr int W = Run<BITS, 16>::WORDS;
+  if (MX) {
+    const uint32_t x = w[i < W ? i : 0];
+    // sign, exponent and mantissa at fp16's places: e2m1 / 2^14, exactly
+    v[0] = ((x << 12) & 0x80008000u) | ((x << 9) & 0x0E000E00u);
+    v[1] = ((x << 8) & 0x80008000u) | ((x << 5) & 0x0E000E00u);
+    v[2] = ((x << 4) & 0x80008000u) | ((x << 1) & 0x0E000E00u);
+    v[3] = (x & 0x80008000u) | ((x >> 3) & 0x0E000E00u);
 #pragma unroll
-  for (int i = 0; i < BITS; ++i) w[i] = 0u;
-  if (!ok) return;
-  if (BITS % 4 == 0) {
-#pragma unroll
-    for (int i = 0; i < BITS / 4; ++i) {
-      const uint4 v = reinterpret_cast<const uint4*>(p)[i];
-      w[4 * i] = v.x;
-      w[4 * i + 1] = v.y;
-      w[4 * i + 2] = v.z;
-      w[4 * i + 3] = v.w;
-    }
+    for (int j = 0; j < 4; ++j) v[j] = hmul2(hmul2(v[j], 0x74007400u), s);
+    return;
+  }
+  uint32_t q[4];
+  if (BITS == 4) {
+    const uint32_t x = w[i < W ? i : 0], y = x >> 8;
+    q[0] = hsub2((x & 0x000F000Fu) | 0x64006400u, 0x64006400u);
+    q[1] = hfma2((x & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD400D400u);  // / 16 - 64
+    q[2] = hsub2((y & 0x000F000Fu) | 0x64006400u, 0x64006400u);
+    q[3] = hfma2((y & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD400D400u);
   } else if (BITS == 2) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    w[0] = v.x;
-    w[1] = v.y;
+    const uint32_t x = __byte_perm(w[0], 0u, i ? 0x4342u : 0x4140u);
+    q[0] = hsub2((x & 0x00030003u) | 0x64006400u, 0x64006400u);
+    q[1] = hfma2((x & 0x000C000Cu) | 0x64006400u, 0x34003400u, 0xDC00DC00u);  // / 4 - 256
+    q[2] = hfma2((x & 0x00300030u) | 0x64006400u, 0x2C002C00u, 0xD400D400u);
+    q[3] = hfma2((x & 0x00C000C0u) | 0x64006400u, 0x24002400u, 0xCC00CC00u);  // / 64 - 16
   } else {
 #pragma unroll
-    for (int i = 0; i < BITS; ++i) w[i] = p[i];
+    for (int j = 0; j < 4; ++j)
+      q[j] = hsub2(__byte_perm(bytes4<BITS>(w, 2 * i + j / 2), 0x64646464u,
+                               (j & 1) ? 0x4342u : 0x4140u),
+                   0x64006400u);
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = hfma2(q[j], s, b);
+}
+
+// The same in fp32, as two fp16 each: the rounded value and what it left.
+template <int BITS, bool MX>
+__device__ __forceinline__ void halves8_two(const uint32_t (&w)[Run<BITS, 16>::WORDS], int i,
+                                            float s, float b, uint32_t (&hi)[4],
+                                            uint32_t (&lo)[4]) {
+  constexpr bool SPLIT = BITS == 4 || BITS == 2;
+  uint32_t c[2] = {bytes4<BITS>(w, 2 * i), bytes4<BITS>(w, 2 * i + 1)};
+  if (MX) {
+    // 2 e2m1 + 12, times s / 2, less 6 s: exact
+    c[0] = mx_q8(c[0]);
+    c[1] = mx_q8(c[1]);
+    b = -6.0f * s;
+    s *= 0.5f;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int p0 = SPLIT ? j : 2 * j, p1 = SPLIT ? j + 4 : 2 * j + 1;
+    const float w0 = __fmaf_rn((float)((c[p0 / 4] >> (8 * (p0 & 3))) & 255u), s, b);
+    const float w1 = __fmaf_rn((float)((c[p1 / 4] >> (8 * (p1 & 3))) & 255u), s, b);
+    const __half2 r = __floats2half2_rn(w0, w1);
+    const float2 f = __half22float2(r);
+    const __half2 d = __floats2half2_rn(w0 - f.x, w1 - f.y);
+    hi[j] = *reinterpret_cast<const uint32_t*>(&r);
+    lo[j] = *reinterpret_cast<const uint32_t*>(&d);
   }
 }
 
-// Warps 0: TMA, 1: MMA, 2: TMEM; 4..11: weights, then the epilogue.
+constexpr int kUnpackers = 16;  // warps
+constexpr int kThreads = 128 + 32 * kUnpackers;
+
+// Warps 0: TMA, 1: MMA, 2: TMEM; 4..19: weights, then the epilogue.
 template <int BITS, bool MX, bool TWO>
-__global__ void __launch_bounds__(384, 1) k_lin_fused(const __grid_constant__ FusedLinArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) k_lin_fused(const __grid_constant__ FusedLinArgs a) {
   extern __shared__ uint8_t dyn[];
   constexpr int kMaxStages = 8;
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], tmem_full;
   __shared__ uint32_t tmem_holder;
-  __shared__ float fws[kRows];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = tc::cluster_ctarank();
-  uint32_t split;
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(split));
+  const int lsplit = a.log2_split;
   const uint32_t base = (tc::smem_u32(dyn) + 1023u) & ~1023u;
-  const int ST = a.stages, N = a.n;
-  const uint32_t A1 = kRows * 128, A = TWO ? 2 * A1 : A1, STAGE = A + (uint32_t)N * 128;
+  // a stage: `per` blocks of 64 columns, each a tile of weights (two for TWO)
+  // and one of tokens
+  const int ST = a.stages, N = a.n, per = a.per;
+  constexpr uint32_t A1 = kRows * 128, A = TWO ? 2 * A1 : A1;
+  const uint32_t BLOCK = A + (uint32_t)N * 128, STAGE = BLOCK * per;
   const LinArgs& l = a.l;
-  const int o0 = (int)(blockIdx.x / split) * kRows;
+  const int o0 = (int)(blockIdx.x >> lsplit) * kRows;
   const int m0 = (int)blockIdx.y * N;
-  const int kb0 = (int)((int64_t)a.k_blocks * rank / split);
-  const int kb1 = (int)((int64_t)a.k_blocks * (rank + 1) / split);
+  const int kb0 = (a.k_blocks * (int)rank) >> lsplit;
+  const int kb1 = (a.k_blocks * (int)(rank + 1)) >> lsplit;
+  const int nt = N >> lsplit;  // tokens this CTA finishes, from n0
+  const int n0 = m0 + (lsplit ? nt * (int)rank : 0);
+
+  // ---- weights: four threads per row take 16 columns of each block; the
+  // first blocks' codes are asked for before anything else
+  constexpr int W = Run<BITS, 16>::WORDS, D = 4;
+  uint32_t raw[D][W], rs[D], rb[D];
+  const int t = threadIdx.x - 128, r = t >> 2, part = t & 3;
+  const int64_t wo = min(o0 + r, l.out_dim - 1);
+  const int shift = a.log2_group, groups = l.in_dim >> shift;
+  const uint32_t* row = l.w + wo * (l.in_dim / 32 * BITS);
+  const uint16_t* sc = l.scales + wo * groups;
+  const uint8_t* ex = reinterpret_cast<const uint8_t*>(l.scales) + wo * groups;
+  const uint16_t* bi = MX ? nullptr : l.biases + wo * groups;
+  auto fetch = [&](int kb, int d) {
+    const int c = kb * kBK + 16 * part;
+    rs[d] = rb[d] = 0u;
+#pragma unroll
+    for (int i = 0; i < W; ++i) raw[d][i] = 0u;
+    if (kb < kb1 && c < l.in_dim) {
+      load_run<BITS, 16>(row, kb, part, raw[d]);
+      rs[d] = MX ? (uint32_t)ex[c >> shift] : (uint32_t)sc[c >> shift];
+      if (!MX) rb[d] = (uint32_t)bi[c >> shift];
+    }
+  };
+  if (warp >= 4) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) fetch(kb0 + d, d);
+    // the rest of the run, and what the epilogue reads, into L2
+    const char* p = reinterpret_cast<const char*>(row + (int64_t)kb0 * 2 * BITS);
+    const char* e = reinterpret_cast<const char*>(row) +
+                    min((int64_t)kb1 * 8 * BITS, (int64_t)l.in_dim * BITS / 8);
+#pragma unroll 1
+    for (const char* c = p + 128 * part; c < e; c += 512)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(c));
+    const int size = l.a.out_type == MOEQ_F32 ? 4 : 2, col = o0 + part * (128 / size);
+    if (l.a.residual && r < nt && n0 + r < l.M && col < l.out_dim)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(
+          reinterpret_cast<const char*>(l.a.residual) +
+          ((int64_t)(n0 + r) * l.a.residual_stride + col) * size));
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
-      tc::mbar_init(&full[i], 1 + 8);
+      tc::mbar_init(&full[i], 1 + kUnpackers);
       tc::mbar_init(&empty[i], 1);
     }
     tc::mbar_init(&tmem_full, 1);
     tc::fence_mbar_init();
   }
-  uint32_t cols = 32;
-  while (cols < (uint32_t)N) cols *= 2;
+  const uint32_t cols = (uint32_t)a.tmem_cols;
   if (warp == 2) {
     tc::tmem_alloc(&tmem_holder, cols);
     tc::tmem_relinquish();
@@ -149,17 +254,24 @@ __global__ void __launch_bounds__(384, 1) k_lin_fused(const __grid_constant__ Fu
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
+  // (waited for before anything is written to another CTA: it runs by then)
+  if (lsplit) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   const uint32_t tmem = tmem_holder;
 
   bool ok = true;
+  tc::grid_dep_wait();  // the tokens and all powers of two
   if (warp == 0) {
-    tc::grid_dep_wait();
     uint32_t s = 0, ph = 1;
-    for (int kb = kb0; kb < kb1 && ok; ++kb) {
-      ok = tc::mbar_wait(&empty[s], ph, a.status);
+#pragma unroll 1
+    for (int kb = kb0; kb < kb1 && ok; kb += per) {
+      const int n = min(per, kb1 - kb);
+      ok = wait_bar(&empty[s], ph, a.status);
       if (ok && lane == 0) {
-        tc::mbar_arrive_expect_tx(&full[s], (uint32_t)N * 128);
-        tc::tma_load_3d(base + s * STAGE + A, &a.tm_x, kb * kBK, m0, 0, &full[s]);
+        tc::mbar_arrive_expect_tx(&full[s], (uint32_t)(n * N) * 128);
+#pragma unroll 1
+        for (int i = 0; i < n; ++i)
+          tc::tma_load_3d(base + s * STAGE + i * BLOCK + A, &a.tm_x, (kb + i) * kBK, m0, 0,
+                          &full[s]);
       }
       __syncwarp();
       if (++s == (uint32_t)ST) s = 0, ph ^= 1;
@@ -167,18 +279,23 @@ __global__ void __launch_bounds__(384, 1) k_lin_fused(const __grid_constant__ Fu
   } else if (warp == 1) {
     const uint32_t idesc = tc::idesc_f16_f32(kRows, N);
     uint32_t s = 0, ph = 0;
-    for (int kb = kb0; kb < kb1 && ok; ++kb) {
-      ok = tc::mbar_wait(&full[s], ph, a.status);
+#pragma unroll 1
+    for (int kb = kb0; kb < kb1 && ok; kb += per) {
+      const int n = min(per, kb1 - kb);
+      ok = wait_bar(&full[s], ph, a.status);
       tc::tc_fence_after();
       if (ok && lane == 0) {
-        const uint32_t at = base + s * STAGE;
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+          const uint32_t at = base + s * STAGE + i * BLOCK;
 #pragma unroll
-        for (int h = 0; h < (TWO ? 2 : 1); ++h)
+          for (int p = 0; p < (TWO ? 2 : 1); ++p)
 #pragma unroll
-          for (int kk = 0; kk < kBK / 16; ++kk)
-            tc::mma_f16(tmem, tc::sw128_kmajor_desc(at + h * A1 + kk * 32),
-                        tc::sw128_kmajor_desc(at + A + kk * 32), idesc,
-                        (kb > kb0) || ((h | kk) != 0));
+            for (int kk = 0; kk < kBK / 16; ++kk)
+              tc::mma_f16(tmem, tc::sw128_kmajor_desc(at + p * A1 + kk * 32),
+                          tc::sw128_kmajor_desc(at + A + kk * 32), idesc,
+                          (kb + i > kb0) || ((p | kk) != 0));
+        }
         tc::mma_commit(&empty[s]);
       }
       __syncwarp();
@@ -187,170 +304,119 @@ __global__ void __launch_bounds__(384, 1) k_lin_fused(const __grid_constant__ Fu
     if (lane == 0) tc::mma_commit(&tmem_full);
     __syncwarp();
   } else if (warp >= 4) {
-    const int t = threadIdx.x - 128, r = t >> 1, h = t & 1;
-    const int64_t o = min(o0 + r, l.out_dim - 1);
-    const uint32_t* row = l.w + o * ((int64_t)l.in_dim * BITS / 32);
-    const int groups = l.in_dim / l.G, shift = l.G == 32 ? 5 : l.G == 64 ? 6 : 7;
-    const uint16_t* sc = l.scales + o * groups;
-    const uint8_t* ex = reinterpret_cast<const uint8_t*>(l.scales) + o * groups;
-    const uint16_t* bi = MX ? nullptr : l.biases + o * groups;
-    {
-      // the run's codes into L2, a line per request
-      const char* p = reinterpret_cast<const char*>(row + (int64_t)kb0 * 2 * BITS);
-      const char* e = reinterpret_cast<const char*>(row) +
-                      min((int64_t)kb1 * 8 * BITS, (int64_t)l.in_dim * BITS / 8);
-      for (const char* c = p + 128 * h; c < e; c += 256)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(c));
-    }
-    // the run's largest magnitude
-    const int g0 = (kb0 * kBK) >> shift, g1 = min((kb1 * kBK + l.G - 1) >> shift, groups);
-    float largest = 0.0f;
-    for (int g = g0 + h; g < g1; g += 2)
-      largest = fmaxf(largest, MX ? finite_abs(6.0f * mx_scale(ex[g]))
-                                  : finite_abs(fabsf(bf16_bits_to_float(sc[g])) *
-                                                   (float)((1u << BITS) - 1u) +
-                                               fabsf(bf16_bits_to_float(bi[g]))));
-    largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, 1));
-    const int k = lift_of(largest);
-    const float f = pow2(k);
-    if (h == 0) fws[r] = pow2(-k);
-
-    constexpr int D = BITS == 8 ? 3 : 4;  // blocks of codes in flight
-    uint32_t raw[D][BITS];
-    float fs[D], fb[D];
-    auto fetch = [&](int kb, int d) {
-      const int c = kb * kBK + 32 * h;
-      const bool in = kb < kb1 && c < l.in_dim;
-      load32<BITS>(row + (int64_t)(c / 32) * BITS, in, raw[d]);
-      const int g = in ? c >> shift : 0;
-      fs[d] = MX ? mx_scale(ex[g]) * 0.5f : bf16_bits_to_float(sc[g]);
-      fb[d] = MX ? -12.0f * fs[d] : bf16_bits_to_float(bi[g]);
-      if (!in) fs[d] = fb[d] = 0.0f;
-    };
-#pragma unroll
-    for (int d = 0; d < D; ++d) fetch(kb0 + d, d);
-    uint32_t s = 0, ph = 1;
+    // 2^k of the row, from 2^-k
+    const float lift = __uint_as_float((254u << 23) - __float_as_uint(a.fw[wo]));
+    const uint32_t o1 = tc::sw128_offset(r, 2 * part), o2 = tc::sw128_offset(r, 2 * part + 1);
+    uint32_t s = 0, ph = 1, at = base;
+    int in = 0;  // blocks of this stage written
+#pragma unroll 1
     for (int kb = kb0; kb < kb1 && ok; kb += D) {
 #pragma unroll
       for (int d = 0; d < D; ++d) {
         if (kb + d >= kb1) break;
-        ok = ok && tc::mbar_wait(&empty[s], ph, a.status);
-        uint32_t c[8];
-        to_bytes<BITS, MX>(raw[d], c);
-        const float s32 = fs[d] * f, b32 = fb[d] * f;
-        const uint32_t at = base + s * STAGE;
+        if (in == 0) ok = ok && wait_bar(&empty[s], ph, a.status);
+        const float s32 = (MX ? mx_scale(rs[d]) : __uint_as_float(rs[d] << 16)) * lift;
+        const float b32 = MX ? 0.0f : __uint_as_float(rb[d] << 16) * lift;
         if (ok) {
           if (TWO) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t hi[4], lo[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const uint32_t q = c[2 * i + j / 2] >> (16 * (j & 1));
-                const float w0 = __fmaf_rn((float)(q & 255u), s32, b32);
-                const float w1 = __fmaf_rn((float)((q >> 8) & 255u), s32, b32);
-                const __half2 p = __floats2half2_rn(w0, w1);
-                const float2 b = __half22float2(p);
-                const __half2 q2 = __floats2half2_rn(w0 - b.x, w1 - b.y);
-                hi[j] = *reinterpret_cast<const uint32_t*>(&p);
-                lo[j] = *reinterpret_cast<const uint32_t*>(&q2);
-              }
-              sts128(at + tc::sw128_offset(r, 4 * h + i), hi);
-              sts128(at + A1 + tc::sw128_offset(r, 4 * h + i), lo);
-            }
+            uint32_t hi[4], lo[4];
+            halves8_two<BITS, MX>(raw[d], 0, s32, b32, hi, lo);
+            sts128(at + o1, hi);
+            sts128(at + A1 + o1, lo);
+            halves8_two<BITS, MX>(raw[d], 1, s32, b32, hi, lo);
+            sts128(at + o2, hi);
+            sts128(at + A1 + o2, lo);
           } else {
             const __half2 s2 = __float2half2_rn(s32), b2 = __float2half2_rn(b32);
             const uint32_t su = *reinterpret_cast<const uint32_t*>(&s2);
             const uint32_t bu = *reinterpret_cast<const uint32_t*>(&b2);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t v[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                // 1024 + q is an fp16 with q in its mantissa
-                const uint32_t q =
-                    __byte_perm(c[2 * i + j / 2], 0x64646464u, (j & 1) ? 0x4342u : 0x4140u);
-                v[j] = hfma2(hsub2(q, 0x64006400u), su, bu);
-              }
-              sts128(at + tc::sw128_offset(r, 4 * h + i), v);
-            }
+            uint32_t v[4];
+            halves8<BITS, MX>(raw[d], 0, su, bu, v);
+            sts128(at + o1, v);
+            halves8<BITS, MX>(raw[d], 1, su, bu, v);
+            sts128(at + o2, v);
           }
         }
+        at += BLOCK;
         fetch(kb + d + D, d);
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&full[s]);
-        if (++s == (uint32_t)ST) s = 0, ph ^= 1;
+        if (++in == per || kb + d + 1 == kb1) {
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&full[s]);
+          in = 0;
+          if (++s == (uint32_t)ST) s = 0, ph ^= 1;
+          at = base + s * STAGE;
+        }
       }
     }
   }
 
-  // ---- epilogue: warp q + 4 j holds rows 32 q.., every second share of tokens
-  const int q = warp & 3, half = (warp - 4) >> 2;
+  // ---- epilogue: warp 4 + q + 4 j holds rows 32 q.. of every fourth share of
+  // the tokens
+  const int q = warp & 3, share = (warp - 4) >> 2;
   const int o = o0 + q * 32 + lane;
   const bool live = o < l.out_dim;
   const int oc = min(o, l.out_dim - 1);
-  if (warp >= 4) {
-    tc::grid_dep_wait();  // the tokens' powers
-    ok = tc::mbar_wait(&tmem_full, 0, a.status);
-  }
+  const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16);
+  const float bias = warp >= 4 && live && l.a.bias ? bf16_bits_to_float(l.a.bias[oc]) : 0.0f;
+  const float fw = a.fw[oc];
+  if (warp >= 4) ok = wait_bar(&tmem_full, 0, a.status) && ok;
   tc::tc_fence_after();
-  __syncthreads();  // fws; every product has been waited for
-  const float bias = live && l.a.bias ? bf16_bits_to_float(l.a.bias[oc]) : 0.0f;
-  const float fw = warp >= 4 ? fws[q * 32 + lane] : 0.0f;
-  if (split == 1) {
+  // where a token's sums are added up
+  const uint32_t sums = base + (a.own_sums ? (uint32_t)ST * STAGE : 0u);
+  if (lsplit) {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    // each partial sum goes to the rank that finishes its token:
+    // [source rank][token of that rank][row].  Where the sums take the stages'
+    // place every CTA has to be done with them.
+    if (!a.own_sums) tc::cluster_sync();
     if (warp >= 4 && ok)
-      for (int c0 = half * 32; c0 < N; c0 += 64) {
-        const int nm = min(min(32, N - c0), l.M - (m0 + c0));
-        if (nm <= 0) break;
-        uint32_t v[32];
-        tc::tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + c0, v);
-        const float fx = lane < nm ? a.fx[m0 + c0 + lane] : 0.0f;
+#pragma unroll 1
+      for (int c0 = share * 16; c0 < N; c0 += 64) {
+        uint32_t v[16];
+        tmem_ld16(acc + c0, v);
+        int dst = 0, tl = c0;
+        while (tl >= nt) tl -= nt, ++dst;
         tc::tmem_wait_ld();
-        if (l.a.out_type == MOEQ_F32)
-          finish<float, 32>(l.a, m0 + c0, nm, oc, live, fw, bias, fx, v);
-        else
-          finish<uint16_t, 32>(l.a, m0 + c0, nm, oc, live, fw, bias, fx, v);
-      }
-  } else {
-    // partial sums to shared memory, [token][row]
-    float* part = reinterpret_cast<float*>(dyn + (base - tc::smem_u32(dyn)));
-    if (warp >= 4 && ok)
-      for (int c0 = half * 32; c0 < N; c0 += 64) {
-        uint32_t v[32];
-        tc::tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + c0, v);
-        tc::tmem_wait_ld();
+        const uint32_t to = sums + (uint32_t)(((int)rank * nt * kRows + q * 32 + lane) * 4);
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (c0 + j < N) part[(c0 + j) * kRows + q * 32 + lane] = __uint_as_float(v[j]) * fw;
+        for (int j = 0; j < 16; ++j) {
+          st_cluster(tc::mapa_shared(to, (uint32_t)dst) + (uint32_t)(tl * (kRows * 4)),
+                     __float_as_uint(__uint_as_float(v[j]) * fw));
+          if (++tl == nt) tl = 0, ++dst;
+        }
       }
     tc::cluster_sync();
-    if (warp >= 4) {
-      const int n0 = (int)((uint32_t)N * rank / split), n1 = (int)((uint32_t)N * (rank + 1) / split);
-      const uint32_t mine = base + (uint32_t)(q * 32 + lane) * 4;
-      for (int c0 = n0 + half * 8; c0 < n1; c0 += 16) {
-        const int nm = min(min(8, n1 - c0), l.M - (m0 + c0));
-        if (nm <= 0) break;
+  }
+  if (warp >= 4 && ok) {
+    const uint32_t mine = sums + (uint32_t)(q * 32 + lane) * 4;
+#pragma unroll 1
+    for (int c0 = share * 8; c0 < nt; c0 += 32) {
+      const int nm = min(min(8, nt - c0), l.M - (n0 + c0));
+      if (nm <= 0) break;
+      uint32_t v[8];
+      if (lsplit) {
         float sum[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
-        for (uint32_t p = 0; p < split; ++p) {
-          const uint32_t from = tc::mapa_shared(mine, p);
+#pragma unroll 1
+        for (int p = 0; p < 1 << lsplit; ++p)
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if (j < nm) sum[j] += ld_cluster(from + (uint32_t)(c0 + j) * (kRows * 4));
-        }
-        const float fx = lane < nm ? a.fx[m0 + c0 + lane] : 0.0f;
-        uint32_t v[8];
+            if (j < nm) sum[j] += lds_f32(mine + (uint32_t)((p * nt + c0 + j) * (kRows * 4)));
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = __float_as_uint(sum[j]);
-        if (l.a.out_type == MOEQ_F32)
-          finish<float, 8>(l.a, m0 + c0, nm, oc, live, 1.0f, bias, fx, v);
-        else
-          finish<uint16_t, 8>(l.a, m0 + c0, nm, oc, live, 1.0f, bias, fx, v);
+      } else {
+        tmem_ld8(acc + c0, v);
+        tc::tmem_wait_ld();
       }
+      const float fx = lane < nm ? a.fx[n0 + c0 + lane] : 0.0f;
+      const float f = lsplit ? 1.0f : fw;
+      if (l.a.out_type == MOEQ_F32)
+        finish<float, 8>(l.a, n0 + c0, nm, oc, live, f, bias, fx, v);
+      else
+        finish<uint16_t, 8>(l.a, n0 + c0, nm, oc, live, f, bias, fx, v);
     }
-    tc::cluster_sync();  // a peer may still read this CTA's sums
   }
   tc::tc_fence_before();
   __syncthreads();
@@ -369,7 +435,7 @@ cudaError_t run(const FusedLinArgs& a, int split, int tiles_o, int tiles_m, uint
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t c = {};
   c.gridDim = dim3((unsigned)(tiles_o * split), (unsigned)tiles_m);
-  c.blockDim = dim3(384);
+  c.blockDim = dim3(kThreads);
   c.dynamicSmemBytes = bytes;
   c.stream = st;
   cudaLaunchAttribute at[2];
@@ -400,12 +466,13 @@ cudaError_t run_format(const FusedLinArgs& a, int split, int to, int tm, uint32_
 
 }  // namespace
 
-cudaError_t launch_linear_fused(const LinArgs& l, const __half* x16, const float* fx, int* status,
-                                cudaStream_t st) {
+cudaError_t launch_linear_fused(const LinArgs& l, const __half* x16, const float* fx,
+                                const float* fw, int* status, cudaStream_t st) {
   const int sms = sm_count();
   FusedLinArgs a;
   a.l = l;
   a.fx = fx;
+  a.fw = fw;
   a.status = status;
   const int tiles_m = (l.M + 255) / 256;
   a.n = ((l.M + tiles_m - 1) / tiles_m + 15) / 16 * 16;
@@ -414,13 +481,24 @@ cudaError_t launch_linear_fused(const LinArgs& l, const __half* x16, const float
   // as many CTAs as SMs, four blocks of columns each at least
   int split = 1;
   while (split < 8 && 2 * split * tiles_o * tiles_m <= sms && a.k_blocks >= 8 * split) split *= 2;
+  a.log2_split = split == 8 ? 3 : split == 4 ? 2 : split == 2 ? 1 : 0;
+  a.log2_group = l.G == 32 ? 5 : l.G == 64 ? 6 : 7;
+  a.tmem_cols = 32;
+  while (a.tmem_cols < a.n) a.tmem_cols *= 2;
   const bool two = l.a.out_type == MOEQ_F32;
-  const uint32_t stage = (two ? 2 : 1) * kRows * 128 + (uint32_t)a.n * 128;
-  a.stages = (int)(200 * 1024 / stage);
-  if (a.stages > 8) a.stages = 8;
-  uint32_t bytes = (uint32_t)a.stages * stage;
-  const uint32_t sums = (uint32_t)a.n * kRows * 4;  // fits: n is at most 256
-  if (bytes < sums) bytes = sums;
+  const uint32_t block = (two ? 2 : 1) * kRows * 128 + (uint32_t)a.n * 128;
+  const uint32_t sums = split > 1 ? (uint32_t)a.n * kRows * 4 : 0u;
+  // Two stages at least; as many blocks in each (up to four) as fit, so that
+  // the waits and fences around a stage are paid seldom.
+  const uint32_t room = 224 * 1024;
+  a.own_sums = room >= sums + 4 * block;
+  const uint32_t left = room - (a.own_sums ? sums : 0u);
+  a.per = left >= 8 * block ? 4 : left >= 4 * block ? 2 : 1;
+  a.stages = (int)(left / (block * a.per));
+  if (a.stages > 4) a.stages = 4;
+  uint32_t bytes = (uint32_t)a.stages * a.per * block;
+  if (a.own_sums) bytes += sums;
+  else if (bytes < sums) bytes = sums;  // at most 128 KB
   if (!half_map(&a.tm_x, x16, l.in_dim, l.M, 1, a.n)) return cudaErrorNotSupported;
   return two ? run_format<true>(a, split, tiles_o, tiles_m, bytes + 1024, st)
              : run_format<false>(a, split, tiles_o, tiles_m, bytes + 1024, st);

@@ -31,7 +31,13 @@ struct PrepArgs {
   float* fw;    // [out_dim]
   int x_parts, w_parts;
   int x_blocks;  // first blocks of the grid: tokens; the others: weights
+  int x_split;   // 1: columns of each eight in the order 0 4 1 5 2 6 3 7
 };
+
+__device__ __forceinline__ uint32_t half_pair(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
 
 // Eight values as fp16 at p, and what that rounding left at p + part.
 __device__ __forceinline__ void store_halves(__half* p, int64_t part, bool two,
@@ -134,10 +140,9 @@ __device__ __forceinline__ void prep_weights(const PrepArgs& p, int64_t o) {
   fetch(lane * 8);
   float largest = 0.0f;
   for (int g = lane; g < groups; g += 32)
-    largest = fmaxf(largest, MX ? finite_abs(6.0f * mx_scale(ex[g]))
-                                : finite_abs(fabsf(bf16_bits_to_float(sc[g])) *
-                                                 (float)((1u << BITS) - 1u) +
-                                             fabsf(bf16_bits_to_float(bi[g]))));
+    largest = fmaxf(largest, MX ? 6.0f * mx_scale(ex[g])
+                                : fabsf(bf16_bits_to_float(sc[g])) * (float)((1u << BITS) - 1u) +
+                                      fabsf(bf16_bits_to_float(bi[g])));
   const int k = lift_of(warp_max(largest));
   const float f = pow2(k);
   if (lane == 0) p.fw[o] = pow2(-k);
@@ -197,14 +202,14 @@ __device__ __forceinline__ void prep_tokens(const PrepArgs& p, int64_t m) {
   for (int i = 0; i < NV; ++i)
     if (8 * ((int)threadIdx.x + i * T) < K) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) largest = fmaxf(largest, finite_abs(v[i][j]));
+      for (int j = 0; j < 8; ++j) largest = fmaxf(largest, fabsf(v[i][j]));
     }
   const int rest = 8 * ((int)threadIdx.x + NV * T);
   for (int c = rest; c < K; c += 8 * T) {
     float u[8];
     load(c, u);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) largest = fmaxf(largest, finite_abs(u[j]));
+    for (int j = 0; j < 8; ++j) largest = fmaxf(largest, fabsf(u[j]));
   }
   float f = 1.0f;
   if (type == MOEQ_BF16 || by128) {
@@ -222,6 +227,11 @@ __device__ __forceinline__ void prep_tokens(const PrepArgs& p, int64_t m) {
   auto put = [&](int c, float (&u)[8]) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) u[j] *= f;
+    if (p.x_split) {
+      const float w[8] = {u[0], u[4], u[1], u[5], u[2], u[6], u[3], u[7]};
+      store_halves(out + c, part, p.x_parts == 2, w);
+      return;
+    }
     store_halves(out + c, part, p.x_parts == 2, u);
   };
 #pragma unroll
@@ -250,9 +260,33 @@ __global__ void __launch_bounds__(256) k_lin_prep(const __grid_constant__ PrepAr
   if (o < p.l.out_dim) prep_weights<BITS, MX, TWO>(p, o);
 }
 
+// 2^-k of a weight row, by one warp.
+__device__ __forceinline__ float row_lift(const LinArgs& l, int64_t o) {
+  const int lane = threadIdx.x & 31, groups = l.in_dim / l.G;
+  const uint16_t* sc = l.scales + o * groups;
+  const uint8_t* ex = reinterpret_cast<const uint8_t*>(l.scales) + o * groups;
+  const uint16_t* bi = l.biases + o * groups;
+  const float qmax = (float)((1u << l.bits) - 1u);
+  float largest = 0.0f;
+#pragma unroll 2
+  for (int g = lane; g < groups; g += 32)
+    largest = fmaxf(largest, l.mx ? 6.0f * mx_scale(ex[g])
+                                  : fabsf(bf16_bits_to_float(sc[g])) * qmax +
+                                        fabsf(bf16_bits_to_float(bi[g])));
+  return pow2(-lift_of(warp_max(largest)));
+}
+
+// Tokens as above, but of the weights the powers only.
 __global__ void __launch_bounds__(256) k_lin_tokens(const __grid_constant__ PrepArgs p) {
   tc::grid_dep_launch();
-  prep_tokens(p, blockIdx.x);
+  if ((int)blockIdx.x < p.x_blocks) {
+    prep_tokens(p, blockIdx.x);
+    return;
+  }
+  const int64_t o = ((int64_t)blockIdx.x - p.x_blocks) * 8 + (threadIdx.x >> 5);
+  if (o >= p.l.out_dim) return;
+  const float f = row_lift(p.l, o);
+  if ((threadIdx.x & 31) == 0) p.fw[o] = f;
 }
 
 template <bool TWO>
@@ -344,7 +378,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
       for (int prod = 0; prod < a.products; ++prod)
         for (int kb = 0; kb < KB; ++kb, ++it) {
           const uint32_t s = it % ST, ph = (it / ST) & 1u;
-          if (!tc::mbar_wait(&empty[s], ph ^ 1u, a.status)) goto done;
+          if (!wait_bar(&empty[s], ph ^ 1u, a.status)) goto done;
           if (lane == 0) {
             const uint32_t bar = tc::mapa_shared(tc::smem_u32(&full[s]), 0);
             const uint32_t at = base + s * (S::A + S::B);
@@ -357,19 +391,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     }
     // every release of this CTA's stages has landed before it may exit
     for (int j = 0; j < ST; ++j, ++it)
-      if (!tc::mbar_wait(&empty[it % ST], ((it / ST) & 1u) ^ 1u, a.status)) goto done;
+      if (!wait_bar(&empty[it % ST], ((it / ST) & 1u) ^ 1u, a.status)) goto done;
   } else if (warp == 1 && rank == 0) {
     constexpr uint32_t IDESC = tc::idesc_f16_f32(2 * kTile, BN);
     const int n = KB * a.products;
     uint32_t it = 0, tile = 0;
     for (int item = unit0; item < items; item += units, ++tile) {
       const uint32_t acc = tile & 1u;
-      if (!tc::mbar_wait(&tmem_empty[acc], ((tile >> 1) & 1u) ^ 1u, a.status)) goto done;
+      if (!wait_bar(&tmem_empty[acc], ((tile >> 1) & 1u) ^ 1u, a.status)) goto done;
       tc::tc_fence_after();
       const uint32_t d = tmem + acc * BN;
       for (int kb = 0; kb < n; ++kb, ++it) {
         const uint32_t s = it % ST;
-        if (!tc::mbar_wait(&full[s], (it / ST) & 1u, a.status)) goto done;
+        if (!wait_bar(&full[s], (it / ST) & 1u, a.status)) goto done;
         tc::tc_fence_after();
         if (lane == 0) {
           const uint32_t at = base + s * (S::A + S::B);
@@ -395,7 +429,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
       const float fw = live ? a.fw[o] : 0.0f;
       const float bias =
           live && a.l.a.bias ? bf16_bits_to_float(a.l.a.bias[o]) : 0.0f;
-      if (!tc::mbar_wait(&tmem_full[acc], (tile >> 1) & 1u, a.status)) goto done;
+      if (!wait_bar(&tmem_full[acc], (tile >> 1) & 1u, a.status)) goto done;
       tc::tc_fence_after();
 #pragma unroll 1
       for (int c0 = half * (BN / 2); c0 < (half + 1) * (BN / 2); c0 += 32) {
@@ -489,10 +523,12 @@ cudaError_t launch_linear_gemm(const LinArgs& l, void* ws, int* status, cudaStre
   p.w16 = (__half*)(base + lay.w16);
   p.fw = (float*)(base + lay.fw);
   p.x_blocks = l.M;
+  p.x_split = 0;
   if (l.M <= kFusedTokens && p.x_parts == 1) {
-    k_lin_tokens<<<p.x_blocks, 256, 0, st>>>(p);
+    p.x_split = l.bits == 2 || l.bits == 4;
+    k_lin_tokens<<<p.x_blocks + (l.out_dim + 7) / 8, 256, 0, st>>>(p);
     const cudaError_t e = cudaGetLastError();
-    return e != cudaSuccess ? e : launch_linear_fused(l, p.x16, p.fx, status, st);
+    return e != cudaSuccess ? e : launch_linear_fused(l, p.x16, p.fx, p.fw, status, st);
   }
   GemmArgs g;
   const int bn = l.M > 128 ? 256 : 128;

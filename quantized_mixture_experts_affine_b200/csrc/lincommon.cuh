@@ -57,13 +57,64 @@ __device__ __forceinline__ void store_out(void* p, int type, int64_t at, float v
   else reinterpret_cast<__nv_bfloat16*>(p)[at] = __float2bfloat16_rn(v);
 }
 
-// One output value from its finished sum.
-__device__ __forceinline__ void finish(const moeq_linear_args& a, int64_t m, int o, float v) {
-  if (a.bias) v += bf16_bits_to_float(a.bias[o]);
-  v = act_of(v, a.act);
-  if (a.mul) v *= load_out(a.mul, a.out_type, m * a.mul_stride + o);
-  if (a.residual) v += load_out(a.residual, a.out_type, m * a.residual_stride + o);
-  store_out(a.y, a.out_type, m * a.y_stride + o, v);
+// One output value: what it needs besides its sum, read ahead, and the rest.
+struct Epilogue {
+  float bias = 0.0f, mul = 1.0f, residual = 0.0f, x_scale = 1.0f;
+  __device__ __forceinline__ void load(const moeq_linear_args& a, int64_t m, int o) {
+    if (a.bias) bias = bf16_bits_to_float(a.bias[o]);
+    if (a.mul) mul = load_out(a.mul, a.out_type, m * a.mul_stride + o);
+    if (a.residual) residual = load_out(a.residual, a.out_type, m * a.residual_stride + o);
+    if (a.x_type != MOEQ_BF16 && a.x_group == 0) x_scale = a.x_scales[m];
+  }
+  __device__ __forceinline__ void finish(const moeq_linear_args& a, int64_t m, int o,
+                                         float v) const {
+    v = act_of(v + bias, a.act);
+    if (a.mul) v *= mul;
+    store_out(a.y, a.out_type, m * a.y_stride + o, v + residual);
+  }
+};
+
+// ------------------------------------------------------------------ code runs
+// Words that hold a lane's C codes: its run may start inside a word when the
+// width does not divide 32.
+template <int BITS, int C>
+struct Run {
+  static constexpr int BITLEN = BITS * C;
+  static constexpr int WORDS = BITLEN % 32 == 0 ? BITLEN / 32 : BITLEN / 32 + 1;
+};
+
+// Loads lane t's run of C codes of the span that starts at bit 4 C BITS sp of
+// the row, in its first words from bit 0 on.  The words read lie in the span.
+template <int BITS, int C>
+__device__ __forceinline__ void load_run(const uint32_t* row, int sp, int t,
+                                         uint32_t (&w)[Run<BITS, C>::WORDS]) {
+  constexpr int BL = Run<BITS, C>::BITLEN, W = Run<BITS, C>::WORDS;
+  if (BL % 32 == 0) {
+    const uint32_t* p = row + (int64_t)sp * (4 * W) + t * W;
+    if (W == 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p);
+      w[0] = v.x;
+      w[1] = v.y;
+      w[2] = v.z;
+      w[W - 1] = v.w;
+    } else if (W == 2) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      w[0] = v.x;
+      w[W - 1] = v.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) w[i] = p[i];
+    }
+    return;
+  }
+  const int bit = t * BL, first = bit >> 5, off = bit & 31;
+  const uint32_t* p = row + (int64_t)sp * (4 * BL / 32) + first;
+  const int last = 4 * BL / 32 - 1 - first;  // words of the span behind the first
+  uint32_t raw[W + 1];
+#pragma unroll
+  for (int i = 0; i <= W; ++i) raw[i] = i <= last && 32 * i < off + BL ? p[i] : 0u;
+#pragma unroll
+  for (int i = 0; i < W; ++i) w[i] = __funnelshift_r(raw[i], raw[i + 1], off);
 }
 
 // ------------------------------------------------------------------ bf16 pairs

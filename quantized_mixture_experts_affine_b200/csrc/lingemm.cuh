@@ -12,6 +12,15 @@ namespace moeq {
 
 constexpr int kBK = 64;  // columns per stage (128 bytes)
 
+// tc::mbar_wait with the waiting out of line: these kernels run for a few
+// microseconds, and fetching their instructions is much of that.
+static __device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, int* status) {
+  return tc::mbar_wait(bar, parity, status);
+}
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, int* status) {
+  return tc::mbar_try_wait(bar, parity) || wait_on(bar, parity, status);
+}
+
 __device__ __forceinline__ float pow2(int k) { return __uint_as_float((uint32_t)(k + 127) << 23); }
 
 // Power of two that brings a largest magnitude to [2^13, 2^14) (for tiny
@@ -26,16 +35,6 @@ __device__ __forceinline__ float warp_max(float v) {
   for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
-__device__ __forceinline__ float finite_abs(float v) {
-  v = fabsf(v);
-  return v < INFINITY ? v : 0.0f;
-}
-
-__device__ __forceinline__ uint32_t half_pair(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 // A warp's N tokens from m0 (nm of them real) of output column o: lane j's
 // fx is token j's power.  mul and the residual are read together, before the
 // stores that might overlap them, so that their latency is paid once.
