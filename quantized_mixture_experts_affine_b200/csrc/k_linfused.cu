@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lin_fused(const __grid_constant
   constexpr int kMaxStages = 8;
   __shared__ uint64_t full[kMaxStages], empty[kMaxStages], tmem_full;
   __shared__ uint32_t tmem_holder;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const uint32_t rank = tc::cluster_ctarank();
   const int lsplit = a.log2_split;
   const uint32_t base = (tc::smem_u32(dyn) + 1023u) & ~1023u;
@@ -277,31 +277,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_lin_fused(const __grid_constant
       if (++s == (uint32_t)ST) s = 0, ph ^= 1;
     }
   } else if (warp == 1) {
-    const uint32_t idesc = tc::idesc_f16_f32(kRows, N);
-    uint32_t s = 0, ph = 0;
+    const uint32_t idesc = tc::idesc_f16_f32(kRows, N), on = elect_one();
+    uint32_t s = 0, ph = 0, more = 0;
 #pragma unroll 1
     for (int kb = kb0; kb < kb1 && ok; kb += per) {
       const int n = min(per, kb1 - kb);
       ok = wait_bar(&full[s], ph, a.status);
       tc::tc_fence_after();
-      if (ok && lane == 0) {
+      if (!ok) break;
+      uint32_t at = base + s * STAGE;
 #pragma unroll 1
-        for (int i = 0; i < n; ++i) {
-          const uint32_t at = base + s * STAGE + i * BLOCK;
+      for (int i = 0; i < n; ++i) {
+        const uint64_t dw = tc::sw128_kmajor_desc(at), dx = tc::sw128_kmajor_desc(at + A);
 #pragma unroll
-          for (int p = 0; p < (TWO ? 2 : 1); ++p)
+        for (int p = 0; p < (TWO ? 2 : 1); ++p)
 #pragma unroll
-            for (int kk = 0; kk < kBK / 16; ++kk)
-              tc::mma_f16(tmem, tc::sw128_kmajor_desc(at + p * A1 + kk * 32),
-                          tc::sw128_kmajor_desc(at + A + kk * 32), idesc,
-                          (kb + i > kb0) || ((p | kk) != 0));
-        }
-        tc::mma_commit(&empty[s]);
+          for (int kk = 0; kk < kBK / 16; ++kk) {
+            mma_if<false>(on, tmem, dw + p * (A1 >> 4) + 2 * kk, dx + 2 * kk, idesc, more);
+            more = 1;
+          }
+        at += BLOCK;
       }
+      if (on) tc::mma_commit(&empty[s]);
       __syncwarp();
       if (++s == (uint32_t)ST) s = 0, ph ^= 1;
     }
-    if (lane == 0) tc::mma_commit(&tmem_full);
+    if (on) tc::mma_commit(&tmem_full);
     __syncwarp();
   } else if (warp >= 4) {
     // 2^k of the row, from 2^-k

@@ -343,7 +343,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
   extern __shared__ uint8_t dyn[];
   __shared__ uint64_t full[ST], empty[ST], tmem_full[2], tmem_empty[2];
   __shared__ uint32_t tmem_holder;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
   const uint32_t rank = tc::cluster_ctarank();
   const uint32_t base = (tc::smem_u32(dyn) + 1023u) & ~1023u;
   if (threadIdx.x == 0) {
@@ -395,6 +395,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
   } else if (warp == 1 && rank == 0) {
     constexpr uint32_t IDESC = tc::idesc_f16_f32(2 * kTile, BN);
     const int n = KB * a.products;
+    const uint32_t on = elect_one();
     uint32_t it = 0, tile = 0;
     for (int item = unit0; item < items; item += units, ++tile) {
       const uint32_t acc = tile & 1u;
@@ -405,17 +406,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
         const uint32_t s = it % ST;
         if (!wait_bar(&full[s], (it / ST) & 1u, a.status)) goto done;
         tc::tc_fence_after();
-        if (lane == 0) {
-          const uint32_t at = base + s * (S::A + S::B);
+        const uint64_t da = tc::sw128_kmajor_desc(base + s * (S::A + S::B));
+        const uint64_t db = tc::sw128_kmajor_desc(base + s * (S::A + S::B) + S::A);
 #pragma unroll
-          for (int kk = 0; kk < kBK / 16; ++kk)
-            tc::mma_f16_pair(d, tc::sw128_kmajor_desc(at + kk * 32),
-                             tc::sw128_kmajor_desc(at + S::A + kk * 32), IDESC, (kb | kk) != 0);
-          tc::mma_commit_pair(&empty[s], 3);
-        }
+        for (int kk = 0; kk < kBK / 16; ++kk)
+          mma_if<true>(on, d, da + 2 * kk, db + 2 * kk, IDESC, (kb | kk) != 0);
+        if (on) tc::mma_commit_pair(&empty[s], 3);
         __syncwarp();
       }
-      if (lane == 0) tc::mma_commit_pair(&tmem_full[acc], 3);
+      if (on) tc::mma_commit_pair(&tmem_full[acc], 3);
       __syncwarp();
     }
   } else if (warp >= 4) {
