@@ -211,17 +211,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_lin_fused(const __grid_constant
   const uint16_t* sc = l.scales + wo * groups;
   const uint8_t* ex = reinterpret_cast<const uint8_t*>(l.scales) + wo * groups;
   const uint16_t* bi = MX ? nullptr : l.biases + wo * groups;
+  // blocks in which this thread's columns exist (a row may end in mid-block);
+  // elsewhere s = b = 0 make the weights zeros
+  const int end = kb1 - (kb1 * kBK > l.in_dim && part >= 2 ? 1 : 0);
+  const int group0 = 16 * part;
   auto fetch = [&](int kb, int d) {
-    const int c = kb * kBK + 16 * part;
     rs[d] = rb[d] = 0u;
-#pragma unroll
-    for (int i = 0; i < W; ++i) raw[d][i] = 0u;
-    if (kb < kb1 && c < l.in_dim) {
+    if (kb < end) {
       load_run<BITS, 16>(row, kb, part, raw[d]);
-      rs[d] = MX ? (uint32_t)ex[c >> shift] : (uint32_t)sc[c >> shift];
-      if (!MX) rb[d] = (uint32_t)bi[c >> shift];
+      const int g = (kb * kBK + group0) >> shift;
+      rs[d] = MX ? (uint32_t)ex[g] : (uint32_t)sc[g];
+      if (!MX) rb[d] = (uint32_t)bi[g];
     }
   };
+#pragma unroll
+  for (int d = 0; d < D; ++d)
+#pragma unroll
+    for (int i = 0; i < W; ++i) raw[d][i] = 0u;
   if (warp >= 4) {
 #pragma unroll
     for (int d = 0; d < D; ++d) fetch(kb0 + d, d);
@@ -309,42 +315,42 @@ __global__ void __launch_bounds__(kThreads, 1) k_lin_fused(const __grid_constant
     const float lift = __uint_as_float((254u << 23) - __float_as_uint(a.fw[wo]));
     const uint32_t o1 = tc::sw128_offset(r, 2 * part), o2 = tc::sw128_offset(r, 2 * part + 1);
     uint32_t s = 0, ph = 1, at = base;
-    int in = 0;  // blocks of this stage written
 #pragma unroll 1
     for (int kb = kb0; kb < kb1 && ok; kb += D) {
 #pragma unroll
       for (int d = 0; d < D; ++d) {
         if (kb + d >= kb1) break;
-        if (in == 0) ok = ok && wait_bar(&empty[s], ph, a.status);
+        // (blocks of a stage: 1, 2 or 4, a divisor of D)
+        if ((d & (per - 1)) == 0 && !wait_bar(&empty[s], ph, a.status)) {
+          ok = false;
+          break;
+        }
         const float s32 = (MX ? mx_scale(rs[d]) : __uint_as_float(rs[d] << 16)) * lift;
         const float b32 = MX ? 0.0f : __uint_as_float(rb[d] << 16) * lift;
-        if (ok) {
-          if (TWO) {
-            uint32_t hi[4], lo[4];
-            halves8_two<BITS, MX>(raw[d], 0, s32, b32, hi, lo);
-            sts128(at + o1, hi);
-            sts128(at + A1 + o1, lo);
-            halves8_two<BITS, MX>(raw[d], 1, s32, b32, hi, lo);
-            sts128(at + o2, hi);
-            sts128(at + A1 + o2, lo);
-          } else {
-            const __half2 s2 = __float2half2_rn(s32), b2 = __float2half2_rn(b32);
-            const uint32_t su = *reinterpret_cast<const uint32_t*>(&s2);
-            const uint32_t bu = *reinterpret_cast<const uint32_t*>(&b2);
-            uint32_t v[4];
-            halves8<BITS, MX>(raw[d], 0, su, bu, v);
-            sts128(at + o1, v);
-            halves8<BITS, MX>(raw[d], 1, su, bu, v);
-            sts128(at + o2, v);
-          }
+        if (TWO) {
+          uint32_t hi[4], lo[4];
+          halves8_two<BITS, MX>(raw[d], 0, s32, b32, hi, lo);
+          sts128(at + o1, hi);
+          sts128(at + A1 + o1, lo);
+          halves8_two<BITS, MX>(raw[d], 1, s32, b32, hi, lo);
+          sts128(at + o2, hi);
+          sts128(at + A1 + o2, lo);
+        } else {
+          const __half2 s2 = __float2half2_rn(s32), b2 = __float2half2_rn(b32);
+          const uint32_t su = *reinterpret_cast<const uint32_t*>(&s2);
+          const uint32_t bu = *reinterpret_cast<const uint32_t*>(&b2);
+          uint32_t v[4];
+          halves8<BITS, MX>(raw[d], 0, su, bu, v);
+          sts128(at + o1, v);
+          halves8<BITS, MX>(raw[d], 1, su, bu, v);
+          sts128(at + o2, v);
         }
         at += BLOCK;
         fetch(kb + d + D, d);
-        if (++in == per || kb + d + 1 == kb1) {
+        if (((d + 1) & (per - 1)) == 0 || kb + d + 1 == kb1) {
           tc::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&full[s]);
-          in = 0;
           if (++s == (uint32_t)ST) s = 0, ph ^= 1;
           at = base + s * STAGE;
         }
