@@ -26,11 +26,12 @@ struct FusedLinArgs {
   LinArgs l;
   const float* fx;
   const float* fw;
+  const uint32_t* sb;  // [group][out_dim] (s, b) as fp16, times the row's 2^k
   int n;        // tokens per CTA, a multiple of 16, at most 256
   int stages;
   int per;       // 64-column blocks of a stage
   int own_sums;  // the partial sums have a place behind the stages
-  int k_blocks;
+  int k_runs;  // 256-column runs of a row, the last one padded
   int log2_split, log2_group, tmem_cols;
   int* status;
 };
@@ -83,36 +84,60 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
                : "r"(taddr));
 }
 
-// Four codes of a 16-code run (from 4 i on) as bytes in order.
+// A thread's run: 64 neighbouring codes of a row, 2 BITS words.
 template <int BITS>
-__device__ __forceinline__ uint32_t bytes4(const uint32_t (&w)[Run<BITS, 16>::WORDS], int i) {
-  constexpr int W = Run<BITS, 16>::WORDS;
-  if (BITS == 8) return w[i < W ? i : 0];
-  const int bit = 4 * BITS * i, k = bit / 32, off = bit % 32;
-  const uint32_t lo = w[k < W ? k : 0], hi = k + 1 < W ? w[k + 1 < W ? k + 1 : 0] : 0u;
-  const uint32_t v = __funnelshift_r(lo, hi, off);
-  if (BITS == 4) {
-    const uint32_t x = (v & 0xFFu) | ((v & 0xFF00u) << 8);  // two codes per half
-    return (x & 0x000F000Fu) | ((x & 0x00F000F0u) << 4);
+struct Codes {
+  static constexpr int W = 2 * BITS;
+  uint32_t w[W];
+  // half: the row ends after 32 codes (widths of 4 and 8 bits)
+  __device__ __forceinline__ void load(const uint32_t* p, bool half) {
+    if (W % 4 == 0) {
+#pragma unroll
+      for (int i = 0; i < W / 4; ++i) {
+        if ((BITS == 4 || BITS == 8) && i >= W / 8 && half) break;
+        const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+        w[4 * i] = v.x;
+        w[4 * i + 1] = v.y;
+        w[4 * i + 2] = v.z;
+        w[4 * i + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < W / 2; ++i) {
+        const uint2 v = reinterpret_cast<const uint2*>(p)[i];
+        w[2 * i] = v.x;
+        w[2 * i + 1] = v.y;
+      }
+    }
   }
-  if (BITS == 2) {
-    const uint32_t x = (v & 0xFu) | ((v & 0xF0u) << 12);
-    return (x & 0x00030003u) | ((x & 0x000C000Cu) << 6);
+  // Codes 4 i .. 4 i + 3 as bytes in order.
+  __device__ __forceinline__ uint32_t bytes4(int i) const {
+    if (BITS == 8) return w[i];
+    const int bit = 4 * BITS * i, k = bit / 32, off = bit % 32;
+    const uint32_t v = __funnelshift_r(w[k], k + 1 < W ? w[k + 1 < W ? k + 1 : 0] : 0u, off);
+    if (BITS == 4) {
+      const uint32_t x = (v & 0xFFu) | ((v & 0xFF00u) << 8);  // two codes per half
+      return (x & 0x000F000Fu) | ((x & 0x00F000F0u) << 4);
+    }
+    if (BITS == 2) {
+      const uint32_t x = (v & 0xFu) | ((v & 0xF0u) << 12);
+      return (x & 0x00030003u) | ((x & 0x000C000Cu) << 6);
+    }
+    constexpr int GB = 4 * BITS % 32;
+    return Chunk<BITS>::spread4(v & ((1u << GB) - 1u));
   }
-  constexpr int GB = 4 * BITS % 32;
-  return Chunk<BITS>::spread4(v & ((1u << GB) - 1u));
-}
+};
 
 // Codes 8 i .. 8 i + 7 of a run as fp16 values q s + b, one rounding, in the
 // columns' order of the tokens' layout: widths of 2 and 4 bits pair columns j
 // and j + 4, which lets one mask cut both out of a word (1024 + 2^k q is an
 // fp16 with q in its mantissa), the others neighbours.
 template <int BITS, bool MX>
-__device__ __forceinline__ void halves8(const uint32_t (&w)[Run<BITS, 16>::WORDS], int i,
-                                        uint32_t s, uint32_t b, uint32_t (&v)[4]) {
-  constexpr int W = Run<BITS, 16>::WORDS;
+__device__ __forceinline__ void halves8(const Codes<BITS>& c, int i, uint32_t s, uint32_t b,
+                                        uint32_t (&v)[4]) {
+  constexpr int W = Codes<BITS>::W;
   if (MX) {
-    const uint32_t x = w[i < W ? i : 0];
+    const uint32_t x = c.w[i < W ? i : 0];
     // sign, exponent and mantissa at fp16's places: e2m1 / 2^14, exactly
     v[0] = ((x << 12) & 0x80008000u) | ((x << 9) & 0x0E000E00u);
     v[1] = ((x << 8) & 0x80008000u) | ((x << 5) & 0x0E000E00u);
@@ -124,13 +149,13 @@ __device__ __forceinline__ void halves8(const uint32_t (&w)[Run<BITS, 16>::WORDS
   }
   uint32_t q[4];
   if (BITS == 4) {
-    const uint32_t x = w[i < W ? i : 0], y = x >> 8;
+    const uint32_t x = c.w[i < W ? i : 0], y = x >> 8;
     q[0] = hsub2((x & 0x000F000Fu) | 0x64006400u, 0x64006400u);
     q[1] = hfma2((x & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD400D400u);  // / 16 - 64
     q[2] = hsub2((y & 0x000F000Fu) | 0x64006400u, 0x64006400u);
     q[3] = hfma2((y & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, 0xD400D400u);
   } else if (BITS == 2) {
-    const uint32_t x = __byte_perm(w[0], 0u, i ? 0x4342u : 0x4140u);
+    const uint32_t x = __byte_perm(c.w[i / 2 < W ? i / 2 : 0], 0u, (i & 1) ? 0x4342u : 0x4140u);
     q[0] = hsub2((x & 0x00030003u) | 0x64006400u, 0x64006400u);
     q[1] = hfma2((x & 0x000C000Cu) | 0x64006400u, 0x34003400u, 0xDC00DC00u);  // / 4 - 256
     q[2] = hfma2((x & 0x00300030u) | 0x64006400u, 0x2C002C00u, 0xD400D400u);
@@ -138,8 +163,7 @@ __device__ __forceinline__ void halves8(const uint32_t (&w)[Run<BITS, 16>::WORDS
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      q[j] = hsub2(__byte_perm(bytes4<BITS>(w, 2 * i + j / 2), 0x64646464u,
-                               (j & 1) ? 0x4342u : 0x4140u),
+      q[j] = hsub2(__byte_perm(c.bytes4(2 * i + j / 2), 0x64646464u, (j & 1) ? 0x4342u : 0x4140u),
                    0x64006400u);
   }
 #pragma unroll
@@ -148,11 +172,10 @@ __device__ __forceinline__ void halves8(const uint32_t (&w)[Run<BITS, 16>::WORDS
 
 // The same in fp32, as two fp16 each: the rounded value and what it left.
 template <int BITS, bool MX>
-__device__ __forceinline__ void halves8_two(const uint32_t (&w)[Run<BITS, 16>::WORDS], int i,
-                                            float s, float b, uint32_t (&hi)[4],
-                                            uint32_t (&lo)[4]) {
+__device__ __forceinline__ void halves8_two(const Codes<BITS>& codes, int i, float s, float b,
+                                            uint32_t (&hi)[4], uint32_t (&lo)[4]) {
   constexpr bool SPLIT = BITS == 4 || BITS == 2;
-  uint32_t c[2] = {bytes4<BITS>(w, 2 * i), bytes4<BITS>(w, 2 * i + 1)};
+  uint32_t c[2] = {codes.bytes4(2 * i), codes.bytes4(2 * i + 1)};
   if (MX) {
     // 2 e2m1 + 12, times s / 2, less 6 s: exact
     c[0] = mx_q8(c[0]);
@@ -163,8 +186,10 @@ __device__ __forceinline__ void halves8_two(const uint32_t (&w)[Run<BITS, 16>::W
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int p0 = SPLIT ? j : 2 * j, p1 = SPLIT ? j + 4 : 2 * j + 1;
-    const float w0 = __fmaf_rn((float)((c[p0 / 4] >> (8 * (p0 & 3))) & 255u), s, b);
-    const float w1 = __fmaf_rn((float)((c[p1 / 4] >> (8 * (p1 & 3))) & 255u), s, b);
+    // 2^23 + q is an fp32 with q in its mantissa
+    const float q0 = __uint_as_float(__byte_perm(c[p0 / 4], 0x4B000000u, 0x7440u + (p0 & 3)));
+    const float q1 = __uint_as_float(__byte_perm(c[p1 / 4], 0x4B000000u, 0x7440u + (p1 & 3)));
+    const float w0 = __fmaf_rn(q0 - 8388608.0f, s, b), w1 = __fmaf_rn(q1 - 8388608.0f, s, b);
     const __half2 r = __floats2half2_rn(w0, w1);
     const float2 f = __half22float2(r);
     const __half2 d = __floats2half2_rn(w0 - f.x, w1 - f.y);
@@ -195,48 +220,37 @@ __global__ void __launch_bounds__(kThreads, 1) k_lin_fused(const __grid_constant
   const LinArgs& l = a.l;
   const int o0 = (int)(blockIdx.x >> lsplit) * kRows;
   const int m0 = (int)blockIdx.y * N;
-  const int kb0 = (a.k_blocks * (int)rank) >> lsplit;
-  const int kb1 = (a.k_blocks * (int)(rank + 1)) >> lsplit;
+  const int kb0 = 4 * ((a.k_runs * (int)rank) >> lsplit);
+  const int kb1 = 4 * ((a.k_runs * (int)(rank + 1)) >> lsplit);
   const int nt = N >> lsplit;  // tokens this CTA finishes, from n0
   const int n0 = m0 + (lsplit ? nt * (int)rank : 0);
 
-  // ---- weights: four threads per row take 16 columns of each block; the
-  // first blocks' codes are asked for before anything else
-  constexpr int W = Run<BITS, 16>::WORDS, D = 4;
-  uint32_t raw[D][W], rs[D], rb[D];
+  // ---- weights: of each 256 columns four threads per row take 64 neighbours,
+  // 16 of them into each of the four 64-column blocks (the tokens' columns
+  // are laid out to match), so that a thread's codes come in wide loads and
+  // one or two scales serve all of them.  The first codes are asked for
+  // before anything else.
   const int t = threadIdx.x - 128, r = t >> 2, part = t & 3;
   const int64_t wo = min(o0 + r, l.out_dim - 1);
-  const int shift = a.log2_group, groups = l.in_dim >> shift;
-  const uint32_t* row = l.w + wo * (l.in_dim / 32 * BITS);
-  const uint16_t* sc = l.scales + wo * groups;
-  const uint8_t* ex = reinterpret_cast<const uint8_t*>(l.scales) + wo * groups;
-  const uint16_t* bi = MX ? nullptr : l.biases + wo * groups;
-  // blocks in which this thread's columns exist (a row may end in mid-block);
-  // elsewhere s = b = 0 make the weights zeros
-  const int end = kb1 - (kb1 * kBK > l.in_dim && part >= 2 ? 1 : 0);
-  const int group0 = 16 * part;
-  auto fetch = [&](int kb, int d) {
-    rs[d] = rb[d] = 0u;
-    if (kb < end) {
-      load_run<BITS, 16>(row, kb, part, raw[d]);
-      const int g = (kb * kBK + group0) >> shift;
-      rs[d] = MX ? (uint32_t)ex[g] : (uint32_t)sc[g];
-      if (!MX) rb[d] = (uint32_t)bi[g];
-    }
+  const int shift = a.log2_group;
+  const uint32_t* row = l.w + wo * (l.in_dim / 32 * BITS) + part * Codes<BITS>::W;
+  Codes<BITS> raw[2];
+  auto fetch = [&](int kb, Codes<BITS>& c) {
+    const int left = l.in_dim - (kb * kBK + 64 * part);
+    if (kb < kb1 && left > 0) c.load(row + (kb >> 2) * (8 * BITS), left < 64);
   };
-#pragma unroll
-  for (int d = 0; d < D; ++d)
-#pragma unroll
-    for (int i = 0; i < W; ++i) raw[d][i] = 0u;
   if (warp >= 4) {
 #pragma unroll
-    for (int d = 0; d < D; ++d) fetch(kb0 + d, d);
+    for (int d = 0; d < 2; ++d) {
+#pragma unroll
+      for (int i = 0; i < Codes<BITS>::W; ++i) raw[d].w[i] = 0u;
+      fetch(kb0 + 4 * d, raw[d]);
+    }
     // the rest of the run, and what the epilogue reads, into L2
-    const char* p = reinterpret_cast<const char*>(row + (int64_t)kb0 * 2 * BITS);
-    const char* e = reinterpret_cast<const char*>(row) +
-                    min((int64_t)kb1 * 8 * BITS, (int64_t)l.in_dim * BITS / 8);
+    const char* p = reinterpret_cast<const char*>(row + (kb0 >> 2) * (8 * BITS));
+    const char* e = p + min((kb1 - kb0) * 8 * BITS, (l.in_dim - kb0 * kBK) / 8 * BITS);
 #pragma unroll 1
-    for (const char* c = p + 128 * part; c < e; c += 512)
+    for (const char* c = p + 64 * BITS; c < e; c += 32 * BITS)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(c));
     const int size = l.a.out_type == MOEQ_F32 ? 4 : 2, col = o0 + part * (128 / size);
     if (l.a.residual && r < nt && n0 + r < l.M && col < l.out_dim)
@@ -270,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lin_fused(const __grid_constant
     uint32_t s = 0, ph = 1;
 #pragma unroll 1
     for (int kb = kb0; kb < kb1 && ok; kb += per) {
-      const int n = min(per, kb1 - kb);
+      const int n = per;
       ok = wait_bar(&empty[s], ph, a.status);
       if (ok && lane == 0) {
         tc::mbar_arrive_expect_tx(&full[s], (uint32_t)(n * N) * 128);
@@ -287,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lin_fused(const __grid_constant
     uint32_t s = 0, ph = 0, more = 0;
 #pragma unroll 1
     for (int kb = kb0; kb < kb1 && ok; kb += per) {
-      const int n = min(per, kb1 - kb);
+      const int n = per;
       ok = wait_bar(&full[s], ph, a.status);
       tc::tc_fence_after();
       if (!ok) break;
@@ -311,49 +325,64 @@ __global__ void __launch_bounds__(kThreads, 1) k_lin_fused(const __grid_constant
     if (on) tc::mma_commit(&tmem_full);
     __syncwarp();
   } else if (warp >= 4) {
-    // 2^k of the row, from 2^-k
-    const float lift = __uint_as_float((254u << 23) - __float_as_uint(a.fw[wo]));
     const uint32_t o1 = tc::sw128_offset(r, 2 * part), o2 = tc::sw128_offset(r, 2 * part + 1);
+    const uint32_t* sb = a.sb + wo;  // s and b of a group and row, times the row's 2^k
+    auto scales = [&](int kb, uint32_t (&v)[2]) {
+      const int col = kb * kBK + 64 * part;
+      v[0] = v[1] = 0u;  // beyond the row: zeros
+      if (kb < kb1 && col < l.in_dim) v[0] = v[1] = sb[(int64_t)(col >> shift) * l.out_dim];
+      if (shift == 5) {
+        v[1] = 0u;
+        if (kb < kb1 && col + 32 < l.in_dim) v[1] = sb[(int64_t)((col + 32) >> 5) * l.out_dim];
+      }
+    };
+    uint32_t sbw[2][2];
+    scales(kb0, sbw[0]);
+    scales(kb0 + 4, sbw[1]);
     uint32_t s = 0, ph = 1, at = base;
 #pragma unroll 1
-    for (int kb = kb0; kb < kb1 && ok; kb += D) {
+    for (int kb = kb0; kb < kb1 && ok; kb += 8) {
 #pragma unroll
-      for (int d = 0; d < D; ++d) {
-        if (kb + d >= kb1) break;
-        // (blocks of a stage: 1, 2 or 4, a divisor of D)
-        if ((d & (per - 1)) == 0 && !wait_bar(&empty[s], ph, a.status)) {
-          ok = false;
-          break;
+      for (int d = 0; d < 2; ++d) {
+        const int k4 = kb + 4 * d;
+        if (k4 >= kb1 || !ok) break;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          // (blocks of a stage: 1, 2 or 4)
+          if ((j & (per - 1)) == 0 && !wait_bar(&empty[s], ph, a.status)) {
+            ok = false;
+            break;
+          }
+          const uint32_t w = sbw[d][j >> 1];
+          const uint32_t su = __byte_perm(w, 0u, 0x1010u), bu = __byte_perm(w, 0u, 0x3232u);
+          if (TWO) {
+            const __half2 h = *reinterpret_cast<const __half2*>(&w);
+            const float2 f = __half22float2(h);
+            uint32_t hi[4], lo[4];
+            halves8_two<BITS, MX>(raw[d], 2 * j, f.x, f.y, hi, lo);
+            sts128(at + o1, hi);
+            sts128(at + A1 + o1, lo);
+            halves8_two<BITS, MX>(raw[d], 2 * j + 1, f.x, f.y, hi, lo);
+            sts128(at + o2, hi);
+            sts128(at + A1 + o2, lo);
+          } else {
+            uint32_t v[4];
+            halves8<BITS, MX>(raw[d], 2 * j, su, bu, v);
+            sts128(at + o1, v);
+            halves8<BITS, MX>(raw[d], 2 * j + 1, su, bu, v);
+            sts128(at + o2, v);
+          }
+          at += BLOCK;
+          if (((j + 1) & (per - 1)) == 0) {
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&full[s]);
+            if (++s == (uint32_t)ST) s = 0, ph ^= 1;
+            at = base + s * STAGE;
+          }
         }
-        const float s32 = (MX ? mx_scale(rs[d]) : __uint_as_float(rs[d] << 16)) * lift;
-        const float b32 = MX ? 0.0f : __uint_as_float(rb[d] << 16) * lift;
-        if (TWO) {
-          uint32_t hi[4], lo[4];
-          halves8_two<BITS, MX>(raw[d], 0, s32, b32, hi, lo);
-          sts128(at + o1, hi);
-          sts128(at + A1 + o1, lo);
-          halves8_two<BITS, MX>(raw[d], 1, s32, b32, hi, lo);
-          sts128(at + o2, hi);
-          sts128(at + A1 + o2, lo);
-        } else {
-          const __half2 s2 = __float2half2_rn(s32), b2 = __float2half2_rn(b32);
-          const uint32_t su = *reinterpret_cast<const uint32_t*>(&s2);
-          const uint32_t bu = *reinterpret_cast<const uint32_t*>(&b2);
-          uint32_t v[4];
-          halves8<BITS, MX>(raw[d], 0, su, bu, v);
-          sts128(at + o1, v);
-          halves8<BITS, MX>(raw[d], 1, su, bu, v);
-          sts128(at + o2, v);
-        }
-        at += BLOCK;
-        fetch(kb + d + D, d);
-        if (((d + 1) & (per - 1)) == 0 || kb + d + 1 == kb1) {
-          tc::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&full[s]);
-          if (++s == (uint32_t)ST) s = 0, ph ^= 1;
-          at = base + s * STAGE;
-        }
+        fetch(k4 + 8, raw[d]);
+        scales(k4 + 8, sbw[d]);
       }
     }
   }
@@ -474,20 +503,22 @@ cudaError_t run_format(const FusedLinArgs& a, int split, int to, int tm, uint32_
 }  // namespace
 
 cudaError_t launch_linear_fused(const LinArgs& l, const __half* x16, const float* fx,
-                                const float* fw, int* status, cudaStream_t st) {
+                                const float* fw, const uint32_t* sb, int* status,
+                                cudaStream_t st) {
   const int sms = sm_count();
   FusedLinArgs a;
   a.l = l;
   a.fx = fx;
   a.fw = fw;
+  a.sb = sb;
   a.status = status;
   const int tiles_m = (l.M + 255) / 256;
   a.n = ((l.M + tiles_m - 1) / tiles_m + 15) / 16 * 16;
-  a.k_blocks = (l.in_dim + kBK - 1) / kBK;
+  a.k_runs = (l.in_dim + 255) / 256;
   const int tiles_o = (l.out_dim + kRows - 1) / kRows;
-  // as many CTAs as SMs, four blocks of columns each at least
+  // as many CTAs as SMs, a run of columns each at least
   int split = 1;
-  while (split < 8 && 2 * split * tiles_o * tiles_m <= sms && a.k_blocks >= 8 * split) split *= 2;
+  while (split < 8 && 2 * split * tiles_o * tiles_m <= sms && a.k_runs >= 2 * split) split *= 2;
   a.log2_split = split == 8 ? 3 : split == 4 ? 2 : split == 2 ? 1 : 0;
   a.log2_group = l.G == 32 ? 5 : l.G == 64 ? 6 : 7;
   a.tmem_cols = 32;
@@ -506,7 +537,7 @@ cudaError_t launch_linear_fused(const LinArgs& l, const __half* x16, const float
   uint32_t bytes = (uint32_t)a.stages * a.per * block;
   if (a.own_sums) bytes += sums;
   else if (bytes < sums) bytes = sums;  // at most 128 KB
-  if (!half_map(&a.tm_x, x16, l.in_dim, l.M, 1, a.n)) return cudaErrorNotSupported;
+  if (!half_map(&a.tm_x, x16, 256 * a.k_runs, l.M, 1, a.n)) return cudaErrorNotSupported;
   return two ? run_format<true>(a, split, tiles_o, tiles_m, bytes + 1024, st)
              : run_format<false>(a, split, tiles_o, tiles_m, bytes + 1024, st);
 }

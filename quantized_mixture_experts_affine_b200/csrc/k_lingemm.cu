@@ -31,7 +31,12 @@ struct PrepArgs {
   float* fw;    // [out_dim]
   int x_parts, w_parts;
   int x_blocks;  // first blocks of the grid: tokens; the others: weights
-  int x_split;   // 1: columns of each eight in the order 0 4 1 5 2 6 3 7
+  // For the product that unpacks the weights itself: rows padded with zeros
+  // to x_row columns, eights of columns moved as its threads take them
+  // (64 neighbours of 256 go to four blocks of 64), and with x_split each
+  // eight in the order 0 4 1 5 2 6 3 7; and the weights' scales.
+  int x_row, x_runs, x_split;
+  uint32_t* sb;  // [group][out_dim]
 };
 
 __device__ __forceinline__ uint32_t half_pair(float a, float b) {
@@ -181,8 +186,8 @@ __device__ __forceinline__ void prep_tokens(const PrepArgs& p, int64_t m) {
       reinterpret_cast<const char*>(l.a.x) + m * l.a.x_stride * (type == MOEQ_BF16 ? 2 : 1);
   const bool by128 = type != MOEQ_BF16 && l.a.x_group == 128;
   const float* xs = l.a.x_scales + m * (by128 ? (K + 127) / 128 : 1);
-  __half* out = p.x16 + m * K;
-  const int64_t part = (int64_t)l.M * K;
+  __half* out = p.x16 + m * p.x_row;
+  const int64_t part = (int64_t)l.M * p.x_row;
   auto load = [&](int c, float (&v)[8]) {
     load_x8(row, type, c, v);
     if (by128) {
@@ -227,10 +232,13 @@ __device__ __forceinline__ void prep_tokens(const PrepArgs& p, int64_t m) {
   auto put = [&](int c, float (&u)[8]) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) u[j] *= f;
-    if (p.x_split) {
-      const float w[8] = {u[0], u[4], u[1], u[5], u[2], u[6], u[3], u[7]};
-      store_halves(out + c, part, p.x_parts == 2, w);
-      return;
+    if (p.x_runs) {
+      c = (c & ~255) | (c & 0x30) << 2 | (c & 0xC0) >> 2 | (c & 8);
+      if (p.x_split) {
+        const float w[8] = {u[0], u[4], u[1], u[5], u[2], u[6], u[3], u[7]};
+        store_halves(out + c, part, false, w);
+        return;
+      }
     }
     store_halves(out + c, part, p.x_parts == 2, u);
   };
@@ -242,6 +250,10 @@ __device__ __forceinline__ void prep_tokens(const PrepArgs& p, int64_t m) {
   for (int c = rest; c < K; c += 8 * T) {
     float u[8];
     load(c, u);
+    put(c, u);
+  }
+  for (int c = K + 8 * (int)threadIdx.x; c < p.x_row; c += 8 * T) {
+    float u[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     put(c, u);
   }
 }
@@ -276,17 +288,32 @@ __device__ __forceinline__ float row_lift(const LinArgs& l, int64_t o) {
   return pow2(-lift_of(warp_max(largest)));
 }
 
-// Tokens as above, but of the weights the powers only.
+// Tokens as above, but of the weights the powers and scales only: eight rows
+// per CTA, transposed through shared memory.
 __global__ void __launch_bounds__(256) k_lin_tokens(const __grid_constant__ PrepArgs p) {
   tc::grid_dep_launch();
   if ((int)blockIdx.x < p.x_blocks) {
     prep_tokens(p, blockIdx.x);
     return;
   }
-  const int64_t o = ((int64_t)blockIdx.x - p.x_blocks) * 8 + (threadIdx.x >> 5);
-  if (o >= p.l.out_dim) return;
-  const float f = row_lift(p.l, o);
-  if ((threadIdx.x & 31) == 0) p.fw[o] = f;
+  __shared__ uint32_t tile[32][9];
+  const LinArgs& l = p.l;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, groups = l.in_dim / l.G;
+  const int o0 = ((int)blockIdx.x - p.x_blocks) * 8;
+  const int64_t o = min(o0 + warp, l.out_dim - 1);
+  const float f = row_lift(l, o), up = __fdividef(1.0f, f);
+  if (lane == 0) p.fw[o] = f;
+  const int g8 = threadIdx.x >> 3, r8 = threadIdx.x & 7;
+  for (int g0 = 0; g0 < groups; g0 += 32) {
+    const int64_t g = o * groups + min(g0 + lane, groups - 1);
+    const float s = l.mx ? mx_scale(reinterpret_cast<const uint8_t*>(l.scales)[g])
+                         : bf16_bits_to_float(l.scales[g]);
+    tile[lane][warp] = half_pair(s * up, l.mx ? 0.0f : bf16_bits_to_float(l.biases[g]) * up);
+    __syncthreads();
+    if (g0 + g8 < groups && o0 + r8 < l.out_dim)
+      p.sb[(int64_t)(g0 + g8) * l.out_dim + o0 + r8] = tile[g8][r8];
+    __syncthreads();
+  }
 }
 
 template <bool TWO>
@@ -475,6 +502,18 @@ Layout layout(int64_t M, int64_t K, int64_t O, int xp, int wp) {
   o.total = o.fw + up256((size_t)O * 4);
   return o;
 }
+struct FusedLayout {
+  size_t x16, fx, fw, sb, total;
+};
+FusedLayout fused_layout(int64_t M, int64_t K, int64_t O, int G) {
+  FusedLayout o;
+  o.x16 = 0;
+  o.fx = o.x16 + up256((size_t)(M * ((K + 255) / 256 * 256)) * 2);
+  o.fw = o.fx + up256((size_t)M * 4);
+  o.sb = o.fw + up256((size_t)O * 4);
+  o.total = o.sb + up256((size_t)(O * (K / G)) * 4);
+  return o;
+}
 int x_parts_of(int x_type, int x_group, int out_type) {
   return out_type == MOEQ_F32 && x_type != MOEQ_BF16 && x_group == 128 ? 2 : 1;
 }
@@ -503,9 +542,13 @@ cudaError_t run_gemm(GemmArgs& g, int sms, cudaStream_t st) {
 }  // namespace
 
 size_t linear_gemm_workspace(const moeq_qtensor& t, int M, int x_type, int out_type) {
-  return layout(M, t.in_dim, t.out_dim, x_parts_of(x_type, 128, out_type),
-                out_type == MOEQ_F32 ? 2 : 1)
-      .total;
+  // (an x of 8 bits with an fp32 y: by its x_group it takes either way)
+  const int xp = x_parts_of(x_type, 128, out_type);
+  const size_t fused = fused_layout(M, t.in_dim, t.out_dim, t.group_size).total;
+  const size_t gemm =
+      layout(M, t.in_dim, t.out_dim, xp, out_type == MOEQ_F32 ? 2 : 1).total;
+  if (M > kFusedTokens) return gemm;
+  return xp == 1 || fused > gemm ? fused : gemm;
 }
 
 cudaError_t launch_linear_gemm(const LinArgs& l, void* ws, int* status, cudaStream_t st) {
@@ -522,12 +565,20 @@ cudaError_t launch_linear_gemm(const LinArgs& l, void* ws, int* status, cudaStre
   p.w16 = (__half*)(base + lay.w16);
   p.fw = (float*)(base + lay.fw);
   p.x_blocks = l.M;
-  p.x_split = 0;
+  p.x_row = l.in_dim;
+  p.x_runs = p.x_split = 0;
   if (l.M <= kFusedTokens && p.x_parts == 1) {
+    const FusedLayout fl = fused_layout(l.M, l.in_dim, l.out_dim, l.G);
+    p.x16 = (__half*)(base + fl.x16);
+    p.fx = (float*)(base + fl.fx);
+    p.fw = (float*)(base + fl.fw);
+    p.sb = (uint32_t*)(base + fl.sb);
+    p.x_row = (l.in_dim + 255) / 256 * 256;
+    p.x_runs = 1;
     p.x_split = l.bits == 2 || l.bits == 4;
     k_lin_tokens<<<p.x_blocks + (l.out_dim + 7) / 8, 256, 0, st>>>(p);
     const cudaError_t e = cudaGetLastError();
-    return e != cudaSuccess ? e : launch_linear_fused(l, p.x16, p.fx, p.fw, status, st);
+    return e != cudaSuccess ? e : launch_linear_fused(l, p.x16, p.fx, p.fw, p.sb, status, st);
   }
   GemmArgs g;
   const int bn = l.M > 128 ? 256 : 128;

@@ -33,8 +33,10 @@ cudaError_t launch_linear_small(const LinArgs& l, cudaStream_t st);
 size_t linear_gemm_workspace(const moeq_qtensor& t, int M, int x_type, int out_type);
 cudaError_t launch_linear_gemm(const LinArgs& l, void* ws, int* status, cudaStream_t st);
 // The product with the weights unpacked inside it, on tokens laid out
-// in fp16 (fx, fw: the powers of two of token and weight rows).
+// in fp16 (fx, fw: the powers of two of token and weight rows; sb: scales and biases
+// as fp16 pairs, [group][out_dim], times the weight row's power).
 cudaError_t launch_linear_fused(const LinArgs& l, const __half* x16, const float* fx,
-                                const float* fw, int* status, cudaStream_t st);
+                                const float* fw, const uint32_t* sb, int* status,
+                                cudaStream_t st);
 
 }  // namespace moeq
