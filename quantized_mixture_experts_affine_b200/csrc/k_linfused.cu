@@ -330,11 +330,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_lin_fused(const __grid_constant
     auto scales = [&](int kb, uint32_t (&v)[2]) {
       const int col = kb * kBK + 64 * part;
       v[0] = v[1] = 0u;  // beyond the row: zeros
-      if (kb < kb1 && col < l.in_dim) v[0] = v[1] = sb[(int64_t)(col >> shift) * l.out_dim];
-      if (shift == 5) {
-        v[1] = 0u;
-        if (kb < kb1 && col + 32 < l.in_dim) v[1] = sb[(int64_t)((col + 32) >> 5) * l.out_dim];
-      }
+      if (kb < kb1 && col < l.in_dim) v[0] = sb[(int64_t)(col >> shift) * l.out_dim];
+      // (the second half's own only for groups of 32: a copy would wait here)
+      if (shift == 5 && kb < kb1 && col + 32 < l.in_dim)
+        v[1] = sb[(int64_t)((col + 32) >> 5) * l.out_dim];
     };
     uint32_t sbw[2][2];
     scales(kb0, sbw[0]);
@@ -353,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lin_fused(const __grid_constant
             ok = false;
             break;
           }
-          const uint32_t w = sbw[d][j >> 1];
+          const uint32_t w = j >= 2 && shift == 5 ? sbw[d][1] : sbw[d][0];
           const uint32_t su = __byte_perm(w, 0u, 0x1010u), bu = __byte_perm(w, 0u, 0x3232u);
           if (TWO) {
             const __half2 h = *reinterpret_cast<const __half2*>(&w);
