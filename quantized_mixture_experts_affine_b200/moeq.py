@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "lib", "libmoeq.so")
@@ -118,9 +119,9 @@ _lib.moeq_set_profile_events.restype = C.c_int
 _lib.moeq_launch_count.restype = C.c_uint64
 _lib.moeq_route_groups.argtypes = [C.POINTER(Routing), _P, C.c_int32, C.c_int64, _P, C.c_int32, _P,
                                    _P, _P]
-_lib.moeq_add_rmsnorm.argtypes = [C.POINTER(NormArgs), C.c_int32, C.c_int32, _P]
-_lib.moeq_linear.argtypes = [C.POINTER(QTensor), C.c_int32, C.POINTER(LinearArgs), C.c_int32, _P,
-                             C.c_size_t, _P]
+_lib.moeq_add_rmsnorm.argtypes = [_P, C.c_int32, C.c_int32, _P]  # NormArgs
+_lib.moeq_linear.argtypes = [C.POINTER(QTensor), C.c_int32, _P, C.c_int32, _P, C.c_size_t,
+                             _P]  # the third: LinearArgs
 _lib.moeq_linear_workspace_bytes.argtypes = [C.POINTER(QTensor), C.c_int32, C.c_int32, C.c_int32]
 _lib.moeq_linear_workspace_bytes.restype = C.c_size_t
 _lib.moeq_layer_forward_routed.argtypes = [C.POINTER(Layer), C.POINTER(Routing), _P, _P, C.c_int32,
@@ -157,7 +158,7 @@ def _ptr(t):
 def _stream(s):
     if s is None:
         import torch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch.cuda.current_stream().cuda_stream
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -178,20 +179,31 @@ _DTYPES = {}
 def dtype_code(dtype) -> int:
     """moeq_dtype of a torch dtype."""
     if not _DTYPES:
-        import torch
-        _DTYPES.update({torch.float32: F32, torch.bfloat16: BF16, torch.int8: I8,
-                        torch.float8_e4m3fn: E4M3})
+        _load_torch()
     try:
         return _DTYPES[dtype]
     except KeyError:
         raise MoeqError(f"dtype {dtype}", ERR_UNSUPPORTED) from None
 
 
+def _load_torch() -> None:
+    """torch's types and its current device and stream, looked up once: these
+    calls are made thousands of times a second, a microsecond counts."""
+    global _int32, _float32, _bfloat16, _current_device, _raw_stream
+    import torch
+    _int32, _float32, _bfloat16 = torch.int32, torch.float32, torch.bfloat16
+    _current_device = torch._C._cuda_getDevice if torch.cuda.is_available() else lambda: -2
+    _raw_stream = torch._C._cuda_getCurrentRawStream if torch.cuda.is_available() else None
+    _DTYPES.update({torch.float32: F32, torch.bfloat16: BF16, torch.int8: I8,
+                    torch.float8_e4m3fn: E4M3})
+
+
 def _device(name, t) -> int:
     """Launches go to the current device: its tensors have to be there too."""
-    import torch
+    if not _DTYPES:
+        _load_torch()
     d = t.get_device()
-    if d < 0 or d != torch.cuda.current_device():
+    if d < 0 or d != _current_device():
         raise ValueError(f"{name}: on {t.device}, not on the current CUDA device")
     return d
 
@@ -216,6 +228,13 @@ def _dense(name, t, shape, dtype, device):
         raise ValueError(f"{name}: expected contiguous {dtype} {shape} on device {device}, got "
                          f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
     return t.data_ptr()
+
+
+# The argument structs packed in one step (native alignment; a null pointer
+# is 0): several times faster than filling a ctypes Structure.
+_NORM_ARGS = struct.Struct("@PiqPiqPqPfPqPiqPi0q")
+_LINEAR_ARGS = struct.Struct("@PiqPiPiPqPqPiq0q")
+assert _NORM_ARGS.size == C.sizeof(NormArgs) and _LINEAR_ARGS.size == C.sizeof(LinearArgs)
 
 
 def _x_scales_shape(M, n, group):
@@ -258,16 +277,15 @@ def routing(n_experts: int, top_k: int, score: int = SCORE_SOFTMAX, n_groups: in
 def moeq_route_groups(r: Routing, logits, idx, w, bias=None, stream=None) -> None:
     """Routing `r` of logits [M][E] (fp32 or bf16, rows may be strided) into
     idx int32 [M][K] and w fp32 [M][K]; bias: fp32 [E] or None."""
-    import torch
     dev = _device("logits", logits)
     M, E, K = logits.shape[0], r.n_experts, r.top_k
-    _check("moeq_route_groups",
-           _lib.moeq_route_groups(
-               C.byref(r), logits.data_ptr(), dtype_code(logits.dtype),
-               _rows("logits", logits, M, E),
-               None if bias is None else _dense("bias", bias, (E,), torch.float32, dev), M,
-               _dense("idx", idx, (M, K), torch.int32, dev),
-               _dense("w", w, (M, K), torch.float32, dev), _stream(stream)))
+    rc = _lib.moeq_route_groups(
+        C.byref(r), logits.data_ptr(), dtype_code(logits.dtype), _rows("logits", logits, M, E),
+        None if bias is None else _dense("bias", bias, (E,), _float32, dev), M,
+        _dense("idx", idx, (M, K), _int32, dev), _dense("w", w, (M, K), _float32, dev),
+        _raw_stream(dev) if stream is None else _stream(stream))
+    if rc:
+        _check("moeq_route_groups", rc)
 
 
 def moeq_add_rmsnorm(x, gamma, eps: float, residual=None, r_out=None, y=None, q=None,
@@ -275,27 +293,27 @@ def moeq_add_rmsnorm(x, gamma, eps: float, residual=None, r_out=None, y=None, q=
     """r = x + residual (into r_out), y = bf16 RMS norm of r with weights
     gamma, q = its int8 or float8_e4m3fn codes with q_scales fp32 [M][1]
     (q_group 0) or [M][ceil(H / 128)] (q_group 128)."""
-    import torch
     dev = _device("x", x)
     M, H = x.shape
-    a = NormArgs(x.data_ptr(), dtype_code(x.dtype), _rows("x", x, M, H))
-    a.gamma, a.eps = _dense("gamma", gamma, (H,), torch.bfloat16, dev), eps
+    pr = tr = sr = po = so = py = sy = pq = tq = sq = ps = 0
     if residual is not None:
-        a.residual, a.r_type = residual.data_ptr(), dtype_code(residual.dtype)
-        a.r_stride = _rows("residual", residual, M, H, None, dev)
+        pr, tr = residual.data_ptr(), dtype_code(residual.dtype)
+        sr = _rows("residual", residual, M, H, None, dev)
     if r_out is not None:
-        a.r_out = r_out.data_ptr()
-        a.r_out_stride = _rows("r_out", r_out, M, H,
-                               None if residual is None else residual.dtype, dev)
+        po = r_out.data_ptr()
+        so = _rows("r_out", r_out, M, H, None if residual is None else residual.dtype, dev)
     if y is not None:
-        a.y, a.y_stride = y.data_ptr(), _rows("y", y, M, H, torch.bfloat16, dev)
+        py, sy = y.data_ptr(), _rows("y", y, M, H, _bfloat16, dev)
     if q is not None:
-        a.q, a.q_type, a.q_group = q.data_ptr(), dtype_code(q.dtype), q_group
-        a.q_stride = _rows("q", q, M, H, None, dev)
+        pq, tq, sq = q.data_ptr(), dtype_code(q.dtype), _rows("q", q, M, H, None, dev)
         if q_scales is not None:
-            a.q_scales = _dense("q_scales", q_scales, _x_scales_shape(M, H, q_group),
-                                torch.float32, dev)
-    _check("moeq_add_rmsnorm", _lib.moeq_add_rmsnorm(C.byref(a), M, H, _stream(stream)))
+            ps = _dense("q_scales", q_scales, _x_scales_shape(M, H, q_group), _float32, dev)
+    a = _NORM_ARGS.pack(x.data_ptr(), dtype_code(x.dtype), _rows("x", x, M, H), pr, tr, sr, po, so,
+                        _dense("gamma", gamma, (H,), _bfloat16, dev), eps, py, sy, pq, tq, sq, ps,
+                        q_group)
+    rc = _lib.moeq_add_rmsnorm(a, M, H, _raw_stream(dev) if stream is None else _stream(stream))
+    if rc:
+        _check("moeq_add_rmsnorm", rc)
 
 
 def moeq_linear_workspace_bytes(t: QTensor, M: int, x_dtype, out_dtype) -> int:
@@ -309,30 +327,28 @@ def moeq_linear(t: QTensor, expert: int, x, y, x_scales=None, x_group: int = 0, 
     x: bf16, int8 or float8_e4m3fn (with x_scales as moeq_add_rmsnorm writes
     them) [M][in_dim]; y, mul, residual: fp32 or bf16 [M][out_dim]; ws: uint8
     buffer of moeq_linear_workspace_bytes."""
-    import torch
     dev = _device("x", x)
-    M, n, o = x.shape[0], t.in_dim, t.out_dim
-    a = LinearArgs(x.data_ptr(), dtype_code(x.dtype), _rows("x", x, M, n))
+    M, n, o, yt = x.shape[0], t.in_dim, t.out_dim, y.dtype
+    ps = pb = pm = sm = pr = sr = pw = nw = 0
     if x_scales is not None:
-        a.x_scales = _dense("x_scales", x_scales, _x_scales_shape(M, n, x_group), torch.float32,
-                            dev)
-        a.x_group = x_group
-    a.act, a.y, a.out_type = act, y.data_ptr(), dtype_code(y.dtype)
-    a.y_stride = _rows("y", y, M, o, None, dev)
+        ps = _dense("x_scales", x_scales, _x_scales_shape(M, n, x_group), _float32, dev)
     if bias is not None:
-        a.bias = _dense("bias", bias, (o,), torch.bfloat16, dev)
+        pb = _dense("bias", bias, (o,), _bfloat16, dev)
     if mul is not None:
-        a.mul, a.mul_stride = mul.data_ptr(), _rows("mul", mul, M, o, y.dtype, dev)
+        pm, sm = mul.data_ptr(), _rows("mul", mul, M, o, yt, dev)
     if residual is not None:
-        a.residual = residual.data_ptr()
-        a.residual_stride = _rows("residual", residual, M, o, y.dtype, dev)
-    n_ws = 0
+        pr, sr = residual.data_ptr(), _rows("residual", residual, M, o, yt, dev)
     if ws is not None:
-        n_ws = ws.numel() * ws.element_size()
+        pw, nw = ws.data_ptr(), ws.nbytes
         if ws.get_device() != dev or not ws.is_contiguous():
             raise ValueError(f"ws: expected contiguous on device {dev}, got {ws.device}")
-    _check("moeq_linear", _lib.moeq_linear(C.byref(t), expert, C.byref(a), M, _ptr(ws), n_ws,
-                                           _stream(stream)))
+    a = _LINEAR_ARGS.pack(x.data_ptr(), dtype_code(x.dtype), _rows("x", x, M, n), ps, x_group, pb,
+                          act, pm, sm, pr, sr, y.data_ptr(), dtype_code(yt),
+                          _rows("y", y, M, o, None, dev))
+    rc = _lib.moeq_linear(C.byref(t), expert, a, M, pw, nw,
+                          _raw_stream(dev) if stream is None else _stream(stream))
+    if rc:
+        _check("moeq_linear", rc)
 
 
 def moeq_routed_workspace_bytes(L: Layer, M: int, mode: int = MODE_AUTO) -> int:
