@@ -125,53 +125,95 @@ __device__ __forceinline__ void run8_values(uint2 w, float s, float b, float (&v
   }
 }
 
-// A row of W by one warp, four runs of a lane in flight.
+// 1024 columns of a row of W by one warp, its loads all in flight at once.
+constexpr int kPrepCols = 1024;
 template <int BITS, bool MX, bool TWO>
-__device__ __forceinline__ void prep_weights(const PrepArgs& p, int64_t o) {
+__device__ __forceinline__ void prep_weights(const PrepArgs& p, int64_t o, int col0) {
   const LinArgs& l = p.l;
   const int lane = threadIdx.x & 31, K = l.in_dim;
-  const int groups = K / l.G, shift = l.G == 32 ? 5 : l.G == 64 ? 6 : 7;
-  const uint32_t* row = l.w + o * ((int64_t)K * BITS / 32);
+  const int shift = l.G == 32 ? 5 : l.G == 64 ? 6 : 7, groups = K >> shift;
+  const uint32_t* row = l.w + o * (K / 32 * BITS);
   const uint16_t* sc = l.scales + o * groups;
   const uint8_t* ex = reinterpret_cast<const uint8_t*>(l.scales) + o * groups;
   const uint16_t* bi = MX ? nullptr : l.biases + o * groups;
-  constexpr int U = 4;
+  constexpr int U = kPrepCols / 256;
   uint2 w[U];
-  auto fetch = [&](int c0) {
+  float s[U], b[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (c0 + 256 * u < K) w[u] = load_run8<BITS>(row, c0 + 256 * u);
-  };
-  fetch(lane * 8);
+  for (int u = 0; u < U; ++u) {
+    const int c = min(col0 + lane * 8 + 256 * u, K - 8);
+    w[u] = load_run8<BITS>(row, c);
+    s[u] = MX ? mx_scale(ex[c >> shift]) : bf16_bits_to_float(sc[c >> shift]);
+    b[u] = MX ? 0.0f : bf16_bits_to_float(bi[c >> shift]);
+  }
   float largest = 0.0f;
+#pragma unroll 2
   for (int g = lane; g < groups; g += 32)
     largest = fmaxf(largest, MX ? 6.0f * mx_scale(ex[g])
                                 : fabsf(bf16_bits_to_float(sc[g])) * (float)((1u << BITS) - 1u) +
                                       fabsf(bf16_bits_to_float(bi[g])));
   const int k = lift_of(warp_max(largest));
   const float f = pow2(k);
-  if (lane == 0) p.fw[o] = pow2(-k);
+  if (lane == 0 && col0 == 0) p.fw[o] = pow2(-k);
   __half* out = p.w16 + o * K;
-  for (int c0 = lane * 8; c0 < K; c0 += 256 * U) {
-    float s[U], b[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int g = min(c0 + 256 * u, K - 8) >> shift;
-      s[u] = (MX ? mx_scale(ex[g]) : bf16_bits_to_float(sc[g])) * f;
-      b[u] = MX ? 0.0f : bf16_bits_to_float(bi[g]) * f;
+  for (int u = 0; u < U; ++u) {
+    const int c = col0 + lane * 8 + 256 * u;
+    if (c < K) {
+      float v[8];
+      run8_values<BITS, MX>(w[u], s[u] * f, b[u] * f, v);
+      store_halves(out + c, (int64_t)l.out_dim * K, TWO, v);
     }
-    uint2 x[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) x[u] = w[u];
-    fetch(c0 + 256 * U);
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (c0 + 256 * u < K) {
-        float v[8];
-        run8_values<BITS, MX>(x[u], s[u], b[u], v);
-        store_halves(out + c0 + 256 * u, (int64_t)l.out_dim * K, TWO, v);
-      }
   }
+}
+
+// Token rows of bf16 by one warp each (many rows): the whole row in flight,
+// up to 8 * 32 * RV columns of it in registers, longer ones read again.
+constexpr int RV = 16;
+__device__ __forceinline__ void prep_bf16_rows(const PrepArgs& p, int64_t m) {
+  const LinArgs& l = p.l;
+  const int lane = threadIdx.x & 31, K = l.in_dim;
+  const uint16_t* row = reinterpret_cast<const uint16_t*>(l.a.x) + m * l.a.x_stride + 8 * lane;
+  __half* out = p.x16 + m * K + 8 * lane;
+  uint4 v[RV];
+#pragma unroll
+  for (int i = 0; i < RV; ++i) {
+    v[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (8 * lane + 256 * i < K) v[i] = *reinterpret_cast<const uint4*>(row + 256 * i);
+  }
+  __nv_bfloat162 top = __floats2bfloat162_rn(0.0f, 0.0f);
+  auto take = [&](uint32_t u) {
+    u &= 0x7FFF7FFFu;
+    top = __hmax2(top, *reinterpret_cast<const __nv_bfloat162*>(&u));
+  };
+#pragma unroll
+  for (int i = 0; i < RV; ++i) {
+    take(v[i].x);
+    take(v[i].y);
+    take(v[i].z);
+    take(v[i].w);
+  }
+  for (int c = 256 * RV; c + 8 * lane < K; c += 256) {
+    const uint4 u = *reinterpret_cast<const uint4*>(row + c);
+    take(u.x);
+    take(u.y);
+    take(u.z);
+    take(u.w);
+  }
+  const float2 t = __bfloat1622float2(top);
+  const int k = lift_of(warp_max(fmaxf(t.x, t.y)));
+  const float f = pow2(k);
+  if (lane == 0) p.fx[m] = pow2(-k);
+  auto pair = [&](uint32_t u) -> uint32_t {
+    return half_pair(__uint_as_float(u << 16) * f, __uint_as_float(u & 0xFFFF0000u) * f);
+  };
+  auto put = [&](int c, const uint4& u) {
+    *reinterpret_cast<uint4*>(out + c) = make_uint4(pair(u.x), pair(u.y), pair(u.z), pair(u.w));
+  };
+#pragma unroll
+  for (int i = 0; i < RV; ++i)
+    if (8 * lane + 256 * i < K) put(256 * i, v[i]);
+  for (int c = 256 * RV; c + 8 * lane < K; c += 256) put(c, *reinterpret_cast<const uint4*>(row + c));
 }
 
 // A token row by the whole CTA; up to 8 * NV values of a thread stay in
@@ -258,18 +300,25 @@ __device__ __forceinline__ void prep_tokens(const PrepArgs& p, int64_t m) {
   }
 }
 
-// The first x_blocks CTAs take a token row each, the others a row of W per
-// warp.
+// The first x_blocks CTAs take a token row each (bf16: a row per warp), the
+// others 1024 columns of a row of W per warp.
 template <int BITS, bool MX, bool TWO>
 __global__ void __launch_bounds__(256) k_lin_prep(const __grid_constant__ PrepArgs p) {
   tc::grid_dep_launch();
+  const int warp = threadIdx.x >> 5;
   if ((int)blockIdx.x < p.x_blocks) {
-    prep_tokens(p, blockIdx.x);
+    if (p.l.a.x_type == MOEQ_BF16) {
+      const int64_t m = (int64_t)blockIdx.x * 8 + warp;
+      if (m < p.l.M) prep_bf16_rows(p, m);
+    } else {
+      prep_tokens(p, blockIdx.x);
+    }
     return;
   }
-  const int64_t o =
-      ((int64_t)blockIdx.x - p.x_blocks) * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (o < p.l.out_dim) prep_weights<BITS, MX, TWO>(p, o);
+  const int64_t i = ((int64_t)blockIdx.x - p.x_blocks) * 8 + warp;
+  const int per_row = (p.l.in_dim + kPrepCols - 1) / kPrepCols;
+  const int64_t o = i / per_row;
+  if (o < p.l.out_dim) prep_weights<BITS, MX, TWO>(p, o, (int)(i - o * per_row) * kPrepCols);
 }
 
 // 2^-k of a weight row, by one warp.
@@ -318,7 +367,8 @@ __global__ void __launch_bounds__(256) k_lin_tokens(const __grid_constant__ Prep
 
 template <bool TWO>
 void run_prep(const PrepArgs& p, cudaStream_t st) {
-  const int blocks = p.x_blocks + (p.l.out_dim + 7) / 8;
+  const int64_t warps = (int64_t)p.l.out_dim * ((p.l.in_dim + kPrepCols - 1) / kPrepCols);
+  const int blocks = p.x_blocks + (int)((warps + 7) / 8);
   if (p.l.mx) {
     k_lin_prep<4, true, TWO><<<blocks, 256, 0, st>>>(p);
     return;
@@ -593,6 +643,7 @@ cudaError_t launch_linear_gemm(const LinArgs& l, void* ws, int* status, cudaStre
   g.tiles_o = (l.out_dim + 2 * kTile - 1) / (2 * kTile);
   g.tiles_m = (l.M + bn - 1) / bn;
   g.status = status;
+  if (l.a.x_type == MOEQ_BF16) p.x_blocks = (l.M + 7) / 8;
   if (p.w_parts == 2) run_prep<true>(p, st);
   else run_prep<false>(p, st);
   const cudaError_t e = cudaGetLastError();
