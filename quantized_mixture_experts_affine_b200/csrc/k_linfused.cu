@@ -6,8 +6,8 @@
 // 128-byte swizzle (one fused multiply-add each, a single rounding; for an fp32
 // y a second tile holds what it left), TMA brings the tokens' 64 columns, and
 // one thread issues D (128 rows of W) x (up to 256 tokens) in TMEM.  The tokens
-// are fp16 rows with a power of two each, from k_lin_prep; the weights' power
-// is taken per row and run from its scales and biases.
+// are fp16 rows with a power of two each, from k_lin_tokens, as
+// are the weights' scales, each row's times a power of its own.
 //
 // The columns are split over a cluster of up to eight CTAs, so that few rows
 // of W still fill the GPU; the partial sums meet through distributed shared

@@ -9,7 +9,7 @@
 // y the weights keep a second fp16 (22 bits), and so do tokens whose scales
 // change along the row; the product is then the sum of the parts' products.
 //
-// The second (k_lin_gemm) is a persistent GEMM on CTA pairs (cta_group::2):
+// The third (k_lin_gemm) is a persistent GEMM on CTA pairs (cta_group::2):
 // D (256 rows of W) x (BN tokens) per pair in TMEM, two accumulators, operands
 // by TMA in the 128-byte swizzle.  W's rows are D's rows, so a lane of the
 // epilogue holds one output column o: bias and row power are one register, and
@@ -300,25 +300,28 @@ __device__ __forceinline__ void prep_tokens(const PrepArgs& p, int64_t m) {
   }
 }
 
-// The first x_blocks CTAs take a token row each (bf16: a row per warp), the
-// others 1024 columns of a row of W per warp.
-template <int BITS, bool MX, bool TWO>
-__global__ void __launch_bounds__(256) k_lin_prep(const __grid_constant__ PrepArgs p) {
+// Tokens: bf16 a row per warp, 8 bits a row per CTA.
+__global__ void __launch_bounds__(256) k_lin_rows(const __grid_constant__ PrepArgs p) {
   tc::grid_dep_launch();
-  const int warp = threadIdx.x >> 5;
-  if ((int)blockIdx.x < p.x_blocks) {
-    if (p.l.a.x_type == MOEQ_BF16) {
-      const int64_t m = (int64_t)blockIdx.x * 8 + warp;
-      if (m < p.l.M) prep_bf16_rows(p, m);
-    } else {
-      prep_tokens(p, blockIdx.x);
-    }
-    return;
+  if (p.l.a.x_type == MOEQ_BF16) {
+    const int64_t m = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (m < p.l.M) prep_bf16_rows(p, m);
+  } else {
+    prep_tokens(p, blockIdx.x);
   }
-  const int64_t i = ((int64_t)blockIdx.x - p.x_blocks) * 8 + warp;
+}
+
+// Weights: 1024 columns of a row per warp.  Runs beside the tokens' kernel
+// before it in the stream, and ends after it, so that what waits for this one
+// has waited for both.
+template <int BITS, bool MX, bool TWO>
+__global__ void __launch_bounds__(256) k_lin_weights(const __grid_constant__ PrepArgs p) {
+  tc::grid_dep_launch();
+  const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int per_row = (p.l.in_dim + kPrepCols - 1) / kPrepCols;
   const int64_t o = i / per_row;
   if (o < p.l.out_dim) prep_weights<BITS, MX, TWO>(p, o, (int)(i - o * per_row) * kPrepCols);
+  tc::grid_dep_wait();
 }
 
 // 2^-k of a weight row, by one warp.
@@ -365,21 +368,34 @@ __global__ void __launch_bounds__(256) k_lin_tokens(const __grid_constant__ Prep
   }
 }
 
+template <typename... A>
+cudaError_t launch_after(void (*kernel)(A...), unsigned blocks, unsigned threads, size_t smem,
+                         cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(blocks);
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, args...);
+}
+
 template <bool TWO>
-void run_prep(const PrepArgs& p, cudaStream_t st) {
+cudaError_t run_weights(const PrepArgs& p, cudaStream_t st) {
   const int64_t warps = (int64_t)p.l.out_dim * ((p.l.in_dim + kPrepCols - 1) / kPrepCols);
-  const int blocks = p.x_blocks + (int)((warps + 7) / 8);
-  if (p.l.mx) {
-    k_lin_prep<4, true, TWO><<<blocks, 256, 0, st>>>(p);
-    return;
-  }
+  const unsigned b = (unsigned)((warps + 7) / 8);
+  if (p.l.mx) return launch_after(k_lin_weights<4, true, TWO>, b, 256, 0, st, p);
   switch (p.l.bits) {
-    case 2: k_lin_prep<2, false, TWO><<<blocks, 256, 0, st>>>(p); break;
-    case 3: k_lin_prep<3, false, TWO><<<blocks, 256, 0, st>>>(p); break;
-    case 4: k_lin_prep<4, false, TWO><<<blocks, 256, 0, st>>>(p); break;
-    case 5: k_lin_prep<5, false, TWO><<<blocks, 256, 0, st>>>(p); break;
-    case 6: k_lin_prep<6, false, TWO><<<blocks, 256, 0, st>>>(p); break;
-    default: k_lin_prep<8, false, TWO><<<blocks, 256, 0, st>>>(p); break;
+    case 2: return launch_after(k_lin_weights<2, false, TWO>, b, 256, 0, st, p);
+    case 3: return launch_after(k_lin_weights<3, false, TWO>, b, 256, 0, st, p);
+    case 4: return launch_after(k_lin_weights<4, false, TWO>, b, 256, 0, st, p);
+    case 5: return launch_after(k_lin_weights<5, false, TWO>, b, 256, 0, st, p);
+    case 6: return launch_after(k_lin_weights<6, false, TWO>, b, 256, 0, st, p);
+    default: return launch_after(k_lin_weights<8, false, TWO>, b, 256, 0, st, p);
   }
 }
 
@@ -535,8 +551,16 @@ done:
   }
 }
 
-// Up to here the weights are unpacked inside the product (k_linfused.cu).
-constexpr int kFusedTokens = 512;
+// The weights are unpacked inside the product (k_linfused.cu) while its tiles
+// of 128 rows x 256 tokens take one wave of the GPU, and always for a single
+// tile of tokens, which reads them once.  Beyond, every token tile would unpack
+// them again, and laying them out once wins: 4096 x 4096, 4-bit, bf16 y, 1024
+// tokens (128 tiles) 46.3 against 46.9 us, 1536 tokens (192 tiles) 84.1
+// against 65.6 us; 1024 rows, 2048 tokens (64 tiles) 34.6 against 38.5 us.
+bool unpack_inside(int64_t M, int64_t out_dim) {
+  const int64_t tiles_m = (M + 255) / 256, tiles_o = (out_dim + 127) / 128;
+  return tiles_m == 1 || tiles_m * tiles_o <= 148;
+}
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
@@ -576,17 +600,7 @@ cudaError_t run_gemm(GemmArgs& g, int sms, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int64_t items = (int64_t)g.tiles_o * g.tiles_m;
   const int64_t units = items < sms / 2 ? items : sms / 2;
-  cudaLaunchConfig_t c = {};
-  c.gridDim = dim3((unsigned)(2 * units));
-  c.blockDim = dim3(384);
-  c.dynamicSmemBytes = bytes;
-  c.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  c.attrs = at;
-  c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, k_lin_gemm<BN>, g);
+  return launch_after(k_lin_gemm<BN>, (unsigned)(2 * units), 384, bytes, st, g);
 }
 
 }  // namespace
@@ -597,11 +611,13 @@ size_t linear_gemm_workspace(const moeq_qtensor& t, int M, int x_type, int out_t
   const size_t fused = fused_layout(M, t.in_dim, t.out_dim, t.group_size).total;
   const size_t gemm =
       layout(M, t.in_dim, t.out_dim, xp, out_type == MOEQ_F32 ? 2 : 1).total;
-  if (M > kFusedTokens) return gemm;
+  if (!unpack_inside(M, t.out_dim)) return gemm;
   return xp == 1 || fused > gemm ? fused : gemm;
 }
 
-cudaError_t launch_linear_gemm(const LinArgs& l, void* ws, int* status, cudaStream_t st) {
+cudaError_t launch_linear_gemm(const LinArgs& l, void* ws, int* status, int* launches,
+                               cudaStream_t st) {
+  *launches = 3;
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
   PrepArgs p;
@@ -617,7 +633,7 @@ cudaError_t launch_linear_gemm(const LinArgs& l, void* ws, int* status, cudaStre
   p.x_blocks = l.M;
   p.x_row = l.in_dim;
   p.x_runs = p.x_split = 0;
-  if (l.M <= kFusedTokens && p.x_parts == 1) {
+  if (unpack_inside(l.M, l.out_dim) && p.x_parts == 1) {
     const FusedLayout fl = fused_layout(l.M, l.in_dim, l.out_dim, l.G);
     p.x16 = (__half*)(base + fl.x16);
     p.fx = (float*)(base + fl.fx);
@@ -626,6 +642,7 @@ cudaError_t launch_linear_gemm(const LinArgs& l, void* ws, int* status, cudaStre
     p.x_row = (l.in_dim + 255) / 256 * 256;
     p.x_runs = 1;
     p.x_split = l.bits == 2 || l.bits == 4;
+    *launches = 2;
     k_lin_tokens<<<p.x_blocks + (l.out_dim + 7) / 8, 256, 0, st>>>(p);
     const cudaError_t e = cudaGetLastError();
     return e != cudaSuccess ? e : launch_linear_fused(l, p.x16, p.fx, p.fw, p.sb, status, st);
@@ -643,10 +660,9 @@ cudaError_t launch_linear_gemm(const LinArgs& l, void* ws, int* status, cudaStre
   g.tiles_o = (l.out_dim + 2 * kTile - 1) / (2 * kTile);
   g.tiles_m = (l.M + bn - 1) / bn;
   g.status = status;
-  if (l.a.x_type == MOEQ_BF16) p.x_blocks = (l.M + 7) / 8;
-  if (p.w_parts == 2) run_prep<true>(p, st);
-  else run_prep<false>(p, st);
-  const cudaError_t e = cudaGetLastError();
+  k_lin_rows<<<l.a.x_type == MOEQ_BF16 ? (l.M + 7) / 8 : l.M, 256, 0, st>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) e = p.w_parts == 2 ? run_weights<true>(p, st) : run_weights<false>(p, st);
   if (e != cudaSuccess) return e;
   return bn == 256 ? run_gemm<256>(g, sms, st) : run_gemm<128>(g, sms, st);
 }

@@ -29,9 +29,11 @@ struct LinArgs {
 
 cudaError_t launch_linear_small(const LinArgs& l, cudaStream_t st);
 
-// Many tokens: two launches (operand layout, GEMM) over a workspace.
+// Many tokens: operand layout and product, over a workspace; *launches: how
+// many kernels that took.
 size_t linear_gemm_workspace(const moeq_qtensor& t, int M, int x_type, int out_type);
-cudaError_t launch_linear_gemm(const LinArgs& l, void* ws, int* status, cudaStream_t st);
+cudaError_t launch_linear_gemm(const LinArgs& l, void* ws, int* status, int* launches,
+                               cudaStream_t st);
 // The product with the weights unpacked inside it, on tokens laid out
 // in fp16 (fx, fw: the powers of two of token and weight rows; sb: scales and biases
 // as fp16 pairs, [group][out_dim], times the weight row's power).

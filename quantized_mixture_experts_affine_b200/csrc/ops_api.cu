@@ -165,7 +165,9 @@ MOEQ_API moeq_status moeq_linear(const moeq_qtensor* t, int32_t expert, const mo
   if (M <= kSmallTokens) return launched(launch_linear_small(l, (cudaStream_t)stream));
   int* status = device_status_word();
   if (!status) return MOEQ_ERR_CUDA;
-  return launched(launch_linear_gemm(l, ws, status, (cudaStream_t)stream), 2);
+  int launches = 0;
+  const cudaError_t e = launch_linear_gemm(l, ws, status, &launches, (cudaStream_t)stream);
+  return launched(e, launches);
 }
 
 // ------------------------------------------------------------------ the layer with such a router
