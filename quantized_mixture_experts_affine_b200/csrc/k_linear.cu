@@ -128,6 +128,23 @@ __device__ __forceinline__ void x_pairs(const uint32_t (&raw)[C / 2], int type,
   }
 }
 
+// The scales (or biases) of four spans from entry `at` on: four entries, or two
+// where a group holds two spans (shift 1); MX FP4: four bytes.
+template <bool MX>
+__device__ __forceinline__ void four_scales(const uint16_t* p, int64_t at, int shift,
+                                            uint32_t (&v)[2]) {
+  v[1] = 0u;
+  if (MX) {
+    v[0] = *reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint8_t*>(p) + at);
+  } else if (shift) {
+    v[0] = *reinterpret_cast<const uint32_t*>(p + at);
+  } else {
+    const uint2 u = *reinterpret_cast<const uint2*>(p + at);
+    v[0] = u.x;
+    v[1] = u.y;
+  }
+}
+
 // grid.x: blocks of 16 rows; grid.y: blocks of 8 NT tokens.  The warps split
 // the spans; their sums are added in warp order.  A warp asks for everything
 // of U spans before it uses the first, so that its run of a 4096-column row
@@ -141,11 +158,15 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_linear_small(const __grid_co
   const int o0 = blockIdx.x * 16;
   const int64_t m0 = (int64_t)blockIdx.y * TOKS;
   const int spans = l.in_dim / (4 * C);
-  const int sp0 = spans * warp / kWarps, sp1 = spans * (warp + 1) / kWarps;
+  // (whole fours of spans per warp: see below)
+  const int fours = (spans + 3) >> 2;
+  const int sp0 = 4 * (fours * warp / kWarps), sp1 = min(4 * (fours * (warp + 1) / kWarps), spans);
   const int64_t words_per_row = (int64_t)l.in_dim * BITS / 32;
   // spans per group: 1, or 2 (64-column spans in groups of 128)
   const int shift = l.G == 4 * C ? 0 : 1;
   const int groups = spans >> shift;
+  // a row's scales of four spans in one load where they are aligned to that
+  const bool wide = l.scales_wide;
   const bool bf16 = l.a.x_type == MOEQ_BF16;
   const bool by128 = !bf16 && l.a.x_group == 128;
   const int xsg = (l.in_dim + 127) / 128;
@@ -184,12 +205,33 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_linear_small(const __grid_co
   for (int base = sp0; base < sp1; base += U) {
     uint32_t w[U][2][W], x[U][NT][C / 2];
     uint32_t s[U][2], b[U][2];
+    if (wide) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int64_t at = srow[h] + ((base & ~3) >> shift);  // the four that holds base
+        uint32_t sv[2], bv[2];
+        four_scales<MX>(l.scales, at, shift, sv);
+        if (!MX) four_scales<false>(l.biases, at, shift, bv);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int e0 = (base & 3) + u;  // span within the four
+          const int e = shift ? e0 >> 1 : e0;
+          if (MX) {
+            s[u][h] = (sv[0] >> (8 * e)) & 255u;
+          } else {
+            s[u][h] = __byte_perm(e & 2 ? sv[1] : sv[0], 0u, e & 1 ? 0x4432u : 0x4410u);
+            b[u][h] = __byte_perm(e & 2 ? bv[1] : bv[0], 0u, e & 1 ? 0x4432u : 0x4410u);
+          }
+        }
+      }
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int sp = min(base + u, sp1 - 1), grp = sp >> shift;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         load_run<BITS, C>(wrow[h], sp, t, w[u][h]);
+        if (wide) continue;
         if (MX) {
           s[u][h] = reinterpret_cast<const uint8_t*>(l.scales)[srow[h] + grp];
         } else {
@@ -274,7 +316,13 @@ cudaError_t run_bits(const LinArgs& l, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_linear_small(const LinArgs& l, cudaStream_t st) {
+cudaError_t launch_linear_small(const LinArgs& args, cudaStream_t st) {
+  LinArgs l = args;
+  // four spans: 4 groups of 64 (of 32 with 32-column spans), 2 of 128
+  const int entries = l.G == 128 ? 2 : 4, item = l.mx ? 1 : 2;
+  l.scales_wide = (l.in_dim / l.G) % entries == 0 &&
+                  ((uintptr_t)l.scales % (entries * item)) == 0 &&
+                  (l.mx || ((uintptr_t)l.biases % (entries * item)) == 0);
   if (l.mx) return run<4, true, 8>(l, st);
   switch (l.bits) {
     case 2: return run_bits<2>(l, st);

@@ -29,6 +29,7 @@ struct RouteArgs {
   int bf16;
   int M;
   int lanes_per_group;  // power of two
+  int slot;             // 8-byte words of shared memory per warp
   int group_quads;      // registers path: quads per group, a power of two
 };
 
@@ -364,7 +365,8 @@ __device__ __forceinline__ uint32_t seg_ballot(bool p) {
 }
 
 // Every lane of the warp calls it; m: its segment's token (store: whether to
-// write it).  slots: 32 x 3 words of the warp's shared memory.  Returns false
+// write it).  slots: 96 words of the warp's shared memory, then 4 NQ words for
+// each lane.  Returns false
 // in every lane of a segment whose row is not settled (nothing is written).
 template <int L, int NQ, bool GROUPS, bool BIAS>
 __device__ __forceinline__ bool route_regs(const RouteArgs& a, int m, bool store,
@@ -476,39 +478,25 @@ __device__ __forceinline__ bool route_regs(const RouteArgs& a, int m, bool store
         gk[j] = KT::of(v1 + v2);
       }
     }
-    // lane g: the keys of groups g, g + L, ...
-    constexpr int GP = L == 32 ? 1 : 32 / L;
-    uint32_t mine[GP];
-    int rank[GP];
+    // lane g: the key of group g (n_groups <= L)
+    uint32_t mine = 0;
+    const int at = lane << lg;  // its first quad
 #pragma unroll
-    for (int p = 0; p < GP; ++p) {
-      mine[p] = 0;
-      rank[p] = 0;
-      const int at = (lane + L * p) << lg;  // its first quad
-#pragma unroll
-      for (int j = 0; j < NQ; ++j) {
-        const uint32_t v = __shfl_sync(0xffffffffu, gk[j], at & (L - 1), L);
-        if (lane + L * p < r.n_groups && at / L == j) mine[p] = v;
-      }
+    for (int j = 0; j < NQ; ++j) {
+      const uint32_t v = __shfl_sync(0xffffffffu, gk[j], at & (L - 1), L);
+      if (lane < r.n_groups && at / L == j) mine = v;
     }
-#pragma unroll
-    for (int p = 0; p < GP; ++p)
-      for (int g = 0; g < L && g + L * p < r.n_groups; ++g) {
-        const uint32_t v = __shfl_sync(0xffffffffu, mine[p], g, L);
-#pragma unroll
-        for (int o = 0; o < GP; ++o)
-          rank[o] += (v > mine[o] || (v == mine[o] && g + L * p < lane + L * o)) ? 1 : 0;
-      }
-    uint32_t kept = 0, last = 0, next = 0;
-#pragma unroll
-    for (int p = 0; p < GP; ++p) {
-      const bool in = lane + L * p < r.n_groups;
-      kept |= seg_ballot<L>(in && rank[p] < r.topk_groups) << (L * p & 31);
-      if (in && rank[p] == r.topk_groups - 1) last = mine[p];
-      if (in && rank[p] == r.topk_groups) next = mine[p];
+    int rank = 0;
+#pragma unroll 1
+    for (int g = 0; g < r.n_groups; ++g) {
+      const uint32_t v = __shfl_sync(0xffffffffu, mine, g, L);
+      rank += (v > mine || (v == mine && g < lane)) ? 1 : 0;
     }
+    const bool in = lane < r.n_groups;
+    const uint32_t kept = seg_ballot<L>(in && rank < r.topk_groups);
     if (BIAS || r.group_top == 2) {
-      const uint32_t kl = seg_max<L>(last), kn = seg_max<L>(next);
+      const uint32_t kl = seg_max<L>(in && rank == r.topk_groups - 1 ? mine : 0u);
+      const uint32_t kn = seg_max<L>(in && rank == r.topk_groups ? mine : 0u);
       if (kl > 1 && kn > 1) {
         // two scores and three roundings on each side
         const float vl = KT::value(kl), vn = KT::value(kn);
@@ -523,33 +511,57 @@ __device__ __forceinline__ bool route_regs(const RouteArgs& a, int m, bool store
       }
   }
 
-  uint32_t lk = 0;
-  int li = kNoExpert;
-  auto rescan = [&]() {
-    lk = 0;
-    li = kNoExpert;
-#pragma unroll
-    for (int j = 0; j < NQ; ++j)
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (k[j][c] > lk) {
-          lk = k[j][c];
-          li = 4 * (lane + L * j) + c;
-        }
+  // A lane keeps its quads' largest keys in registers and the keys themselves
+  // in shared memory, where a pick clears one and looks at its quad again.
+  uint32_t qk[NQ] = {}, lk = 0;
+  int qi[NQ] = {}, li = kNoExpert;
+  uint4* own = reinterpret_cast<uint4*>(slots + 96) + NQ * (threadIdx.x & 31);
+  auto top_of = [](const uint4& v, uint32_t& k1, int& i1) {
+    const bool a = v.y > v.x, b = v.w > v.z;
+    const uint32_t ka = a ? v.y : v.x, kb = b ? v.w : v.z;
+    const bool c = kb > ka;
+    k1 = c ? kb : ka;
+    i1 = c ? (b ? 3 : 2) : (a ? 1 : 0);
   };
-  rescan();
+  auto best = [&]() {
+    lk = qk[0];
+    li = qi[0];
+#pragma unroll
+    for (int j = 1; j < NQ; ++j)
+      if (qk[j] > lk) {
+        lk = qk[j];
+        li = qi[j];
+      }
+    if (lk == 0) li = kNoExpert;
+  };
+#pragma unroll
+  for (int j = 0; j < NQ; ++j) {
+    const uint4 v = make_uint4(k[j][0], k[j][1], k[j][2], k[j][3]);
+    own[j] = v;
+    top_of(v, qk[j], qi[j]);
+    qi[j] += 4 * (lane + L * j);
+  }
+  best();
   uint32_t my_k = 0;
   int my_e = 0;
+#pragma unroll 1
   for (int i = 0; i < r.top_k; ++i) {
     const uint32_t top = seg_max<L>(lk);
     const int win = (int)seg_min<L>(lk == top ? (uint32_t)li : 0x7fffffffu);
     if (li == win && win != kNoExpert) {
+      const int j0 = (win >> 2) / L;
+      reinterpret_cast<uint32_t*>(own)[4 * j0 + (win & 3)] = 0u;
+      uint32_t k1;
+      int i1;
+      top_of(own[j0], k1, i1);
+      i1 += win & ~3;
 #pragma unroll
       for (int j = 0; j < NQ; ++j)
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (4 * (lane + L * j) + c == win) k[j][c] = 0;
-      rescan();
+        if (j == j0) {
+          qk[j] = k1;
+          qi[j] = i1;
+        }
+      best();
     }
     if (lane == i) {
       my_k = top;
@@ -587,11 +599,13 @@ __device__ __forceinline__ bool route_regs(const RouteArgs& a, int m, bool store
 #pragma unroll
       for (int j = 0; j < NQ; ++j)
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (k[j][c] > 1 && !(KT::value(k[j][c]) < border)) {
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t left = reinterpret_cast<const uint32_t*>(own)[4 * j + c];
+          if (left > 1 && !(KT::value(left) < border)) {
             near |= 1u << (4 * j + c);
             if (!(l[j][c] == l_last && b[j][c] == b_last)) doubt = true;
           }
+        }
     }
     if (seg_ballot<L>(doubt)) {
       if (L < 32) {
@@ -686,8 +700,8 @@ __device__ __noinline__ void route_row64(const RouteArgs& a, int m, uint64_t* mi
 // A warp's slots: 4 nq keys of 8 bytes, then 4 nq logits.
 __device__ __forceinline__ uint64_t* warp_slots(const RouteArgs& a, float*& raw) {
   extern __shared__ uint64_t slots[];
-  const int nq = max((a.r.n_experts + 3) >> 2, 8);
-  uint64_t* mine = slots + (size_t)(threadIdx.x >> 5) * (6 * nq);
+  const int nq = (a.r.n_experts + 3) >> 2;
+  uint64_t* mine = slots + (size_t)(threadIdx.x >> 5) * a.slot;
   raw = reinterpret_cast<float*>(mine + 4 * nq);
   return mine;
 }
@@ -768,13 +782,14 @@ cudaError_t launch_route_groups(const moeq_routing& r, const void* logits, int l
   // lane holds four quads; the picks sit one per lane.
   int lanes = 32;
   if (regs && M > sms * 16) {
-    if (nq <= 32 && r.top_k <= 8 && !(groups && gq > 8)) lanes = 8;
-    else if (nq <= 64 && r.top_k <= 16 && !(groups && gq > 16)) lanes = 16;
+    if (nq <= 32 && r.top_k <= 8 && !(groups && (gq > 8 || r.n_groups > 8))) lanes = 8;
+    else if (nq <= 64 && r.top_k <= 16 && !(groups && (gq > 16 || r.n_groups > 16))) lanes = 16;
   }
   const int rows = (M + 32 / lanes - 1) / (32 / lanes);  // warps
-  // 48 bytes per quad of experts and warp (48 KB hold one row of 4096),
-  // 384 at least for a row's candidates
-  const size_t slot = (size_t)(nq < 8 ? 8 : nq) * 48;
+  // 48 bytes per quad of experts and warp (48 KB hold one row of 4096); in
+  // registers 384 for a row's candidates and 64 per lane for its keys
+  const size_t slot = regs && nq < 51 ? 384 + 32 * 64 : (size_t)nq * 48;
+  a.slot = (int)(slot / 8);
   int warps = (rows + sms - 1) / sms;  // few rows: spread over the SMs first
   if (warps > 8) warps = 8;
   while (warps > 1 && warps * slot > 48 * 1024) --warps;

@@ -25,6 +25,7 @@ struct LinArgs {
   int out_dim, in_dim, bits, G, mx;
   moeq_linear_args a;
   int M;
+  int scales_wide;  // (k_linear.cu) a row's scales can be loaded four spans at a time
 };
 
 cudaError_t launch_linear_small(const LinArgs& l, cudaStream_t st);

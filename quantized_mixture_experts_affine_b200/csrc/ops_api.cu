@@ -78,8 +78,16 @@ LinArgs lin_args(const moeq_qtensor& t, int expert, const moeq_linear_args& a, i
   return l;
 }
 
-// Up to here the tokens go through the code products (measured in k_linear.cu).
-constexpr int kSmallTokens = 8;
+// The code products (k_linear.cu) take up to 16 tokens, and more while their
+// CTAs (16 rows x 16 tokens each) are resident at once: one per SM, or two
+// where y is fp32, which doubles the other path's products.  4096 columns:
+// 512 rows, 64 tokens, fp32 (128 CTAs) 7.9 against 11.7 us; 128 tokens (256
+// CTAs) 10.7 against 13.7; 1024 rows, 64 tokens, bf16 (256 CTAs) 12.8 against
+// 10.4; 4096 rows, 16 tokens, bf16 11.0 against 11.3.
+bool small_case(int64_t M, int64_t out_dim, int out_type) {
+  return M <= 16 ||
+         (M + 15) / 16 * ((out_dim + 15) / 16) <= (out_type == MOEQ_F32 ? 2 * 148 : 148);
+}
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
@@ -131,7 +139,8 @@ MOEQ_API moeq_status moeq_add_rmsnorm(const moeq_norm_args* n, int32_t M, int32_
 MOEQ_API size_t moeq_linear_workspace_bytes(const moeq_qtensor* t, int32_t M, int32_t x_type,
                                             int32_t out_type) {
   const bool x8 = x_type == MOEQ_I8 || x_type == MOEQ_E4M3;
-  if (check_matrix(t, 0) != MOEQ_OK || M <= kSmallTokens || !(x8 || x_type == MOEQ_BF16) ||
+  if (check_matrix(t, 0) != MOEQ_OK || M <= 0 || small_case(M, t->out_dim, out_type) ||
+      !(x8 || x_type == MOEQ_BF16) ||
       !float_type(out_type))
     return 0;
   return linear_gemm_workspace(*t, M, x_type, out_type);
@@ -162,7 +171,8 @@ MOEQ_API moeq_status moeq_linear(const moeq_qtensor* t, int32_t expert, const mo
   }
   if (sm_count() <= 0) return MOEQ_ERR_CUDA;  // no current device to size launches for
   const LinArgs l = lin_args(*t, expert, *a, M);
-  if (M <= kSmallTokens) return launched(launch_linear_small(l, (cudaStream_t)stream));
+  if (small_case(M, t->out_dim, a->out_type))
+    return launched(launch_linear_small(l, (cudaStream_t)stream));
   int* status = device_status_word();
   if (!status) return MOEQ_ERR_CUDA;
   int launches = 0;
