@@ -163,11 +163,13 @@ __device__ __forceinline__ uint2 codes8(bool i8, const float (&t)[8], float f) {
   } else {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(t[4 * h] * f, t[4 * h + 1] * f),
-                                                  __NV_SATFINITE, __NV_E4M3);
-      const uint32_t b = __nv_cvt_float2_to_fp8x2(
-          make_float2(t[4 * h + 2] * f, t[4 * h + 3] * f), __NV_SATFINITE, __NV_E4M3);
-      out[h] = a | b << 16;
+      asm("{\n\t.reg .b16 a, b;\n\t"
+          "cvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\t"
+          "cvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\t"
+          "mov.b32 %0, {a, b};\n\t}"
+          : "=r"(out[h])
+          : "f"(t[4 * h] * f), "f"(t[4 * h + 1] * f), "f"(t[4 * h + 2] * f),
+            "f"(t[4 * h + 3] * f));
     }
   }
   return make_uint2(out[0], out[1]);
@@ -211,7 +213,8 @@ __device__ __forceinline__ float lanes_max(float k) {
 // MAXT: threads of the largest block.
 constexpr int kAny = -1, kNone = -2;
 
-template <int NV, int XT, int RT, int MAXT>
+// FULL: every thread has NV whole vectors.
+template <int NV, int XT, int RT, bool FULL, int MAXT>
 __global__ void __launch_bounds__(MAXT) k_add_rmsnorm(const __grid_constant__ NormArgs a) {
   constexpr bool ANY = XT == kAny;
   __shared__ float red[32], red_max[32];
@@ -226,7 +229,7 @@ __global__ void __launch_bounds__(MAXT) k_add_rmsnorm(const __grid_constant__ No
   const bool whole = n.q && n.q_group == 0, i8 = n.q_type == MOEQ_I8;
   auto count = [&](int i) -> int {
     const int v = tid + i * T;
-    return v >= a.vecs ? 0 : ANY ? min(8, a.H - 8 * v) : 8;
+    return FULL ? 8 : v >= a.vecs ? 0 : ANY ? min(8, a.H - 8 * v) : 8;
   };
   float r[NV][8];
   uint4 gp[NV];
@@ -260,16 +263,19 @@ __global__ void __launch_bounds__(MAXT) k_add_rmsnorm(const __grid_constant__ No
     for (int i = 0; i < NV; ++i) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) r[i][j] += s[i][j];
+      const int cnt = count(i);
       // the norm is of the stream as it is stored
       if (rt == MOEQ_BF16) {
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          const uint32_t p = bf16_pair(r[i][j], r[i][j + 1]);
-          r[i][j] = __uint_as_float(p << 16);
-          r[i][j + 1] = __uint_as_float(p & 0xFFFF0000u);
+        const uint4 p = make_uint4(bf16_pair(r[i][0], r[i][1]), bf16_pair(r[i][2], r[i][3]),
+                                   bf16_pair(r[i][4], r[i][5]), bf16_pair(r[i][6], r[i][7]));
+        unpack8(p, r[i]);
+        if (!ANY) {
+          if (n.r_out && cnt > 0)
+            *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(n.r_out) + m * n.r_out_stride +
+                                      8 * (tid + i * T)) = p;
+          continue;
         }
       }
-      const int cnt = count(i);
       if (n.r_out && cnt > 0)
         store8(n.r_out, rt, m * n.r_out_stride + 8 * (tid + i * T), cnt, !ANY || a.vro, r[i]);
     }
@@ -316,7 +322,7 @@ __global__ void __launch_bounds__(MAXT) k_add_rmsnorm(const __grid_constant__ No
   }
   if (whole && !exact) row_max = __uint_as_float((uint32_t)(row_key >> 32));
   const float inv = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss, (float)a.H) + n.eps));
-  const float top = i8 ? 127.0f : 448.0f;
+  const float top = i8 ? 127.0f : 448.0f, to_scale = inv * (i8 ? 1.0f / 127.0f : 1.0f / 448.0f);
 
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -339,9 +345,9 @@ __global__ void __launch_bounds__(MAXT) k_add_rmsnorm(const __grid_constant__ No
       for (int j = 0; j < 8; ++j) am = max_nan(am, fabsf(t[j]));
       am = lanes_max<8>(am);
     }
-    // t f is off by 4 roundings at most (2^-22 relative); where moving it by
-    // 2^-20 either way changes a code, fp64 decides
-    const float f = __fdiv_rn(top, am);
+    // t f is off by three roundings and the division's 2 ulp (2^-21 relative);
+    // where moving it by 2^-20 either way changes a code, fp64 decides
+    const float f = __fdividef(top, am);
     uint2 code = codes8(i8, t, f * (1.0f + 9.5367431640625e-7f));
     const uint2 other = codes8(i8, t, f * (1.0f - 9.5367431640625e-7f));
     const bool finite = am < INFINITY, tiny = am < kTinyMax;
@@ -355,7 +361,7 @@ __global__ void __launch_bounds__(MAXT) k_add_rmsnorm(const __grid_constant__ No
     if (cnt > 0) {
       if (whole ? v == 0 : (v & 15) == 0)
         n.q_scales[m * a.n_scales + (whole ? 0 : v >> 4)] =
-            finite ? __fdiv_rn(am * inv, top) : __uint_as_float(0x7FC00000u);
+            finite ? am * to_scale : __uint_as_float(0x7FC00000u);
       uint8_t* q = reinterpret_cast<uint8_t*>(n.q) + m * n.q_stride + 8 * v;
       if (!ANY || (a.vq && cnt == 8)) {
         *reinterpret_cast<uint2*>(q) = code;
@@ -368,15 +374,22 @@ __global__ void __launch_bounds__(MAXT) k_add_rmsnorm(const __grid_constant__ No
   }
 }
 
+template <int NV, int XT, int RT, int MAXT>
+void run_sized(const NormArgs& a, int M, int warps, cudaStream_t st) {
+  if (XT != kAny && a.vecs == warps * 32 * NV)
+    k_add_rmsnorm<NV, XT, RT, XT != kAny, MAXT><<<M, warps * 32, 0, st>>>(a);
+  else
+    k_add_rmsnorm<NV, XT, RT, false, MAXT><<<M, warps * 32, 0, st>>>(a);
+}
+
 template <int XT, int RT>
 void run(const NormArgs& a, int M, int sms, cudaStream_t st) {
   const int warps = (a.vecs + 31) / 32;
   // Many rows: two vectors a thread, so that the reductions and addresses are
   // paid less often; few rows: as many threads as vectors, for the latency.
-  if (warps <= 16 && M < 4 * sms)
-    k_add_rmsnorm<1, XT, RT, 512><<<M, warps * 32, 0, st>>>(a);
-  else if (warps <= 32) k_add_rmsnorm<2, XT, RT, 512><<<M, (warps + 1) / 2 * 32, 0, st>>>(a);
-  else k_add_rmsnorm<4, XT, RT, 1024><<<M, (warps + 3) / 4 * 32, 0, st>>>(a);
+  if (warps <= 16 && M < 4 * sms) run_sized<1, XT, RT, 512>(a, M, warps, st);
+  else if (warps <= 32) run_sized<2, XT, RT, 512>(a, M, (warps + 1) / 2, st);
+  else run_sized<4, XT, RT, 1024>(a, M, (warps + 3) / 4, st);
 }
 
 bool wide(const void* p, int64_t stride, int item, int bytes) {
