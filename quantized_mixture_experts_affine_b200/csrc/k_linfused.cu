@@ -313,9 +313,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_lin_fused(const __grid_constant
         for (int p = 0; p < (TWO ? 2 : 1); ++p)
 #pragma unroll
           for (int kk = 0; kk < kBK / 16; ++kk) {
-            mma_if<false>(on, tmem, dw + p * (A1 >> 4) + 2 * kk, dx + 2 * kk, idesc, more);
-            more = 1;
+            mma_if<false>(on, tmem + p * (uint32_t)N, dw + p * (A1 >> 4) + 2 * kk, dx + 2 * kk, idesc,
+                          more | (kk != 0));
           }
+        more = 1;
         at += BLOCK;
       }
       if (on) tc::mma_commit(&empty[s]);
@@ -413,6 +414,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_lin_fused(const __grid_constant
         int dst = 0, tl = c0;
         while (tl >= nt) tl -= nt, ++dst;
         tc::tmem_wait_ld();
+        if (TWO) {
+          uint32_t u[16];
+          tmem_ld16(acc + N + c0, u);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(u[j]));
+        }
         const uint32_t to = sums + (uint32_t)(((int)rank * nt * kRows + q * 32 + lane) * 4);
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
@@ -444,6 +453,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_lin_fused(const __grid_constant
       } else {
         tmem_ld8(acc + c0, v);
         tc::tmem_wait_ld();
+        if (TWO) {
+          uint32_t u[8];
+          tmem_ld8(acc + N + c0, u);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(u[j]));
+        }
       }
       const float fx = lane < nm ? a.fx[n0 + c0 + lane] : 0.0f;
       const float f = lsplit ? 1.0f : fw;
@@ -501,10 +518,25 @@ cudaError_t run_format(const FusedLinArgs& a, int split, int to, int tm, uint32_
 
 }  // namespace
 
+// As many CTAs as SMs, a run of columns each at least.  The tensor cores cut
+// their sums off, about n 2^-27 for n products of 16 columns: for an fp32 y a
+// CTA takes at most six runs (96 products; the rounding rests of the weights
+// have an accumulator of their own).
+int linear_fused_split(int64_t M, int64_t in_dim, int64_t out_dim, int out_type) {
+  const int64_t tiles = (M + 255) / 256 * ((out_dim + kRows - 1) / kRows);
+  const int64_t runs = (in_dim + 255) / 256;
+  int split = 1;
+  while (split < 8 && 2 * split * tiles <= 148 && runs >= 2 * split) split *= 2;
+  if (out_type == MOEQ_F32) {
+    while (split < 8 && runs > 6 * split) split *= 2;
+    if (runs > 6 * split) return 0;
+  }
+  return split;
+}
+
 cudaError_t launch_linear_fused(const LinArgs& l, const __half* x16, const float* fx,
                                 const float* fw, const uint32_t* sb, int* status,
                                 cudaStream_t st) {
-  const int sms = sm_count();
   FusedLinArgs a;
   a.l = l;
   a.fx = fx;
@@ -515,14 +547,12 @@ cudaError_t launch_linear_fused(const LinArgs& l, const __half* x16, const float
   a.n = ((l.M + tiles_m - 1) / tiles_m + 15) / 16 * 16;
   a.k_runs = (l.in_dim + 255) / 256;
   const int tiles_o = (l.out_dim + kRows - 1) / kRows;
-  // as many CTAs as SMs, a run of columns each at least
-  int split = 1;
-  while (split < 8 && 2 * split * tiles_o * tiles_m <= sms && a.k_runs >= 2 * split) split *= 2;
+  const int split = linear_fused_split(l.M, l.in_dim, l.out_dim, l.a.out_type);
   a.log2_split = split == 8 ? 3 : split == 4 ? 2 : split == 2 ? 1 : 0;
   a.log2_group = l.G == 32 ? 5 : l.G == 64 ? 6 : 7;
   a.tmem_cols = 32;
-  while (a.tmem_cols < a.n) a.tmem_cols *= 2;
   const bool two = l.a.out_type == MOEQ_F32;
+  while (a.tmem_cols < a.n * (two ? 2 : 1)) a.tmem_cols *= 2;
   const uint32_t block = (two ? 2 : 1) * kRows * 128 + (uint32_t)a.n * 128;
   const uint32_t sums = split > 1 ? (uint32_t)a.n * kRows * 4 : 0u;
   // Two stages at least; as many blocks in each (up to four) as fit, so that

@@ -428,7 +428,15 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* tmap,
 }
 
 // Warps 0: TMA, 1: MMA (rank 0), 2: TMEM; 4..11: epilogue.
-template <int BN>
+//
+// The tensor cores cut their sums off (towards zero): a chain of n products of
+// 16 columns comes out about n 2^-27 too small.  A bf16 y does not show it;
+// for an fp32 y (SUMS) the accumulator is read after every kChunk blocks and
+// the parts are added in registers, rounded to nearest: the two accumulators
+// then take turns within a tile too.
+constexpr int kChunk = 8;
+
+template <int BN, bool SUMS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     k_lin_gemm(const __grid_constant__ GemmArgs a) {
   using S = GemmSmem<BN>;
@@ -462,84 +470,120 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
 
   const int unit0 = blockIdx.x >> 1, units = gridDim.x >> 1;
   const int items = a.tiles_o * a.tiles_m, KB = a.k_blocks;
+  const int chunk = SUMS ? kChunk : KB;
 
   if (warp == 0) {
     uint32_t it = 0;
     for (int item = unit0; item < items; item += units) {
       const int o0 = item % a.tiles_o * (2 * kTile) + (int)rank * kTile;
       const int m0 = item / a.tiles_o * BN + (int)rank * (BN / 2);
-      for (int prod = 0; prod < a.products; ++prod)
-        for (int kb = 0; kb < KB; ++kb, ++it) {
-          const uint32_t s = it % ST, ph = (it / ST) & 1u;
-          if (!wait_bar(&empty[s], ph ^ 1u, a.status)) goto done;
-          if (lane == 0) {
-            const uint32_t bar = tc::mapa_shared(tc::smem_u32(&full[s]), 0);
-            const uint32_t at = base + s * (S::A + S::B);
-            if (rank == 0) tc::mbar_arrive_expect_tx(&full[s], 2 * (S::A + S::B));
-            tma_load_3d_pair(at, &a.tm_w, kb * kBK, o0, prod == 1 ? 1 : 0, bar);
-            tma_load_3d_pair(at + S::A, &a.tm_x, kb * kBK, m0, prod == 2 ? 1 : 0, bar);
+      for (int k0 = 0; k0 < KB; k0 += chunk)
+        for (int prod = 0; prod < a.products; ++prod)
+          for (int kb = k0; kb < min(k0 + chunk, KB); ++kb, ++it) {
+            const uint32_t s = it % ST, ph = (it / ST) & 1u;
+            if (!wait_bar(&empty[s], ph ^ 1u, a.status)) goto done;
+            if (lane == 0) {
+              const uint32_t bar = tc::mapa_shared(tc::smem_u32(&full[s]), 0);
+              const uint32_t at = base + s * (S::A + S::B);
+              if (rank == 0) tc::mbar_arrive_expect_tx(&full[s], 2 * (S::A + S::B));
+              tma_load_3d_pair(at, &a.tm_w, kb * kBK, o0, prod == 1 ? 1 : 0, bar);
+              tma_load_3d_pair(at + S::A, &a.tm_x, kb * kBK, m0, prod == 2 ? 1 : 0, bar);
+            }
+            __syncwarp();
           }
-          __syncwarp();
-        }
     }
     // every release of this CTA's stages has landed before it may exit
     for (int j = 0; j < ST; ++j, ++it)
       if (!wait_bar(&empty[it % ST], ((it / ST) & 1u) ^ 1u, a.status)) goto done;
   } else if (warp == 1 && rank == 0) {
     constexpr uint32_t IDESC = tc::idesc_f16_f32(2 * kTile, BN);
-    const int n = KB * a.products;
     const uint32_t on = elect_one();
     uint32_t it = 0, tile = 0;
-    for (int item = unit0; item < items; item += units, ++tile) {
-      const uint32_t acc = tile & 1u;
-      if (!wait_bar(&tmem_empty[acc], ((tile >> 1) & 1u) ^ 1u, a.status)) goto done;
-      tc::tc_fence_after();
-      const uint32_t d = tmem + acc * BN;
-      for (int kb = 0; kb < n; ++kb, ++it) {
-        const uint32_t s = it % ST;
-        if (!wait_bar(&full[s], (it / ST) & 1u, a.status)) goto done;
+    for (int item = unit0; item < items; item += units)
+      for (int k0 = 0; k0 < KB; k0 += chunk, ++tile) {
+        const uint32_t acc = tile & 1u;
+        if (!wait_bar(&tmem_empty[acc], ((tile >> 1) & 1u) ^ 1u, a.status)) goto done;
         tc::tc_fence_after();
-        const uint64_t da = tc::sw128_kmajor_desc(base + s * (S::A + S::B));
-        const uint64_t db = tc::sw128_kmajor_desc(base + s * (S::A + S::B) + S::A);
+        const uint32_t d = tmem + acc * BN;
+        const int n = min(chunk, KB - k0) * a.products;
+        for (int kb = 0; kb < n; ++kb, ++it) {
+          const uint32_t s = it % ST;
+          if (!wait_bar(&full[s], (it / ST) & 1u, a.status)) goto done;
+          tc::tc_fence_after();
+          const uint64_t da = tc::sw128_kmajor_desc(base + s * (S::A + S::B));
+          const uint64_t db = tc::sw128_kmajor_desc(base + s * (S::A + S::B) + S::A);
 #pragma unroll
-        for (int kk = 0; kk < kBK / 16; ++kk)
-          mma_if<true>(on, d, da + 2 * kk, db + 2 * kk, IDESC, (kb | kk) != 0);
-        if (on) tc::mma_commit_pair(&empty[s], 3);
+          for (int kk = 0; kk < kBK / 16; ++kk)
+            mma_if<true>(on, d, da + 2 * kk, db + 2 * kk, IDESC, (kb | kk) != 0);
+          if (on) tc::mma_commit_pair(&empty[s], 3);
+          __syncwarp();
+        }
+        if (on) tc::mma_commit_pair(&tmem_full[acc], 3);
         __syncwarp();
       }
-      if (on) tc::mma_commit_pair(&tmem_full[acc], 3);
-      __syncwarp();
-    }
   } else if (warp >= 4) {
     const int q = warp & 3, half = (warp - 4) >> 2;
     uint32_t tile = 0;
-    for (int item = unit0; item < items; item += units, ++tile) {
-      const uint32_t acc = tile & 1u;
+    for (int item = unit0; item < items; item += units) {
       const int o = item % a.tiles_o * (2 * kTile) + (int)rank * kTile + q * 32 + lane;
       const int m0 = item / a.tiles_o * BN;
       const bool live = o < a.l.out_dim;
-      const float fw = live ? a.fw[o] : 0.0f;
-      const float bias =
-          live && a.l.a.bias ? bf16_bits_to_float(a.l.a.bias[o]) : 0.0f;
-      if (!wait_bar(&tmem_full[acc], (tile >> 1) & 1u, a.status)) goto done;
-      tc::tc_fence_after();
+      const int oc = min(o, a.l.out_dim - 1);
+      const float fw = a.fw[oc];
+      const float bias = a.l.a.bias ? bf16_bits_to_float(a.l.a.bias[oc]) : 0.0f;
+      const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + half * (BN / 2);
+      if (SUMS) {
+        constexpr int C = BN / 2;  // columns of this warp
+        uint32_t sum[C];
+#pragma unroll
+        for (int j = 0; j < C; ++j) sum[j] = 0u;
+        for (int k0 = 0; k0 < KB; k0 += chunk, ++tile) {
+          const uint32_t acc = tile & 1u;
+          if (!wait_bar(&tmem_full[acc], (tile >> 1) & 1u, a.status)) goto done;
+          tc::tc_fence_after();
+#pragma unroll
+          for (int c0 = 0; c0 < C; c0 += 32) {
+            uint32_t v[32];
+            tc::tmem_ld32(lanes + acc * BN + c0, v);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              sum[c0 + j] = __float_as_uint(__uint_as_float(sum[c0 + j]) + __uint_as_float(v[j]));
+          }
+          tc::tc_fence_before();
+          __syncwarp();
+          if (lane == 0)
+            tc::mbar_arrive_cluster(tc::mapa_shared(tc::smem_u32(&tmem_empty[acc]), 0));
+        }
+#pragma unroll
+        for (int c0 = 0; c0 < C; c0 += 16) {
+          const int m = m0 + half * C + c0, nm = min(16, a.l.M - m);
+          if (nm <= 0) break;
+          uint32_t v[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = sum[c0 + j];
+          const float fx = lane < nm ? a.fx[m + lane] : 0.0f;
+          finish<float, 16>(a.l.a, m, nm, oc, live, fw, bias, fx, v);
+        }
+      } else {
+        const uint32_t acc = tile & 1u;
+        if (!wait_bar(&tmem_full[acc], (tile >> 1) & 1u, a.status)) goto done;
+        tc::tc_fence_after();
+        ++tile;
 #pragma unroll 1
-      for (int c0 = half * (BN / 2); c0 < (half + 1) * (BN / 2); c0 += 32) {
-        const int nm = min(32, a.l.M - (m0 + c0));
-        if (nm <= 0) break;
-        uint32_t v[32];
-        tc::tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + acc * BN + c0, v);
-        const float fx = lane < nm ? a.fx[m0 + c0 + lane] : 0.0f;
-        tc::tmem_wait_ld();
-        const int oc = min(o, a.l.out_dim - 1);
-        if (a.l.a.out_type == MOEQ_F32)
-          finish<float, 32>(a.l.a, m0 + c0, nm, oc, live, fw, bias, fx, v);
-        else
-          finish<uint16_t, 32>(a.l.a, m0 + c0, nm, oc, live, fw, bias, fx, v);
+        for (int c0 = 0; c0 < BN / 2; c0 += 32) {
+          const int m = m0 + half * (BN / 2) + c0, nm = min(32, a.l.M - m);
+          if (nm <= 0) break;
+          uint32_t v[32];
+          tc::tmem_ld32(lanes + acc * BN + c0, v);
+          const float fx = lane < nm ? a.fx[m + lane] : 0.0f;
+          tc::tmem_wait_ld();
+          finish<uint16_t, 32>(a.l.a, m, nm, oc, live, fw, bias, fx, v);
+        }
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive_cluster(tc::mapa_shared(tc::smem_u32(&tmem_empty[acc]), 0));
       }
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive_cluster(tc::mapa_shared(tc::smem_u32(&tmem_empty[acc]), 0));
     }
   }
 done:
@@ -557,9 +601,9 @@ done:
 // them again, and laying them out once wins: 4096 x 4096, 4-bit, bf16 y, 1024
 // tokens (128 tiles) 46.3 against 46.9 us, 1536 tokens (192 tiles) 84.1
 // against 65.6 us; 1024 rows, 2048 tokens (64 tiles) 34.6 against 38.5 us.
-bool unpack_inside(int64_t M, int64_t out_dim) {
+bool unpack_inside(int64_t M, int64_t in_dim, int64_t out_dim, int out_type) {
   const int64_t tiles_m = (M + 255) / 256, tiles_o = (out_dim + 127) / 128;
-  return tiles_m == 1 || tiles_m * tiles_o <= 148;
+  return (tiles_m == 1 || tiles_m * tiles_o <= 148) && linear_fused_split(M, in_dim, out_dim, out_type);
 }
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -592,15 +636,15 @@ int x_parts_of(int x_type, int x_group, int out_type) {
   return out_type == MOEQ_F32 && x_type != MOEQ_BF16 && x_group == 128 ? 2 : 1;
 }
 
-template <int BN>
+template <int BN, bool SUMS>
 cudaError_t run_gemm(GemmArgs& g, int sms, cudaStream_t st) {
   constexpr uint32_t bytes = GemmSmem<BN>::BYTES;
-  cudaError_t e = cudaFuncSetAttribute(k_lin_gemm<BN>,
+  cudaError_t e = cudaFuncSetAttribute(k_lin_gemm<BN, SUMS>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   if (e != cudaSuccess) return e;
   const int64_t items = (int64_t)g.tiles_o * g.tiles_m;
   const int64_t units = items < sms / 2 ? items : sms / 2;
-  return launch_after(k_lin_gemm<BN>, (unsigned)(2 * units), 384, bytes, st, g);
+  return launch_after(k_lin_gemm<BN, SUMS>, (unsigned)(2 * units), 384, bytes, st, g);
 }
 
 }  // namespace
@@ -611,7 +655,7 @@ size_t linear_gemm_workspace(const moeq_qtensor& t, int M, int x_type, int out_t
   const size_t fused = fused_layout(M, t.in_dim, t.out_dim, t.group_size).total;
   const size_t gemm =
       layout(M, t.in_dim, t.out_dim, xp, out_type == MOEQ_F32 ? 2 : 1).total;
-  if (!unpack_inside(M, t.out_dim)) return gemm;
+  if (!unpack_inside(M, t.in_dim, t.out_dim, out_type)) return gemm;
   return xp == 1 || fused > gemm ? fused : gemm;
 }
 
@@ -633,7 +677,7 @@ cudaError_t launch_linear_gemm(const LinArgs& l, void* ws, int* status, int* lau
   p.x_blocks = l.M;
   p.x_row = l.in_dim;
   p.x_runs = p.x_split = 0;
-  if (unpack_inside(l.M, l.out_dim) && p.x_parts == 1) {
+  if (unpack_inside(l.M, l.in_dim, l.out_dim, l.a.out_type) && p.x_parts == 1) {
     const FusedLayout fl = fused_layout(l.M, l.in_dim, l.out_dim, l.G);
     p.x16 = (__half*)(base + fl.x16);
     p.fx = (float*)(base + fl.fx);
@@ -648,7 +692,8 @@ cudaError_t launch_linear_gemm(const LinArgs& l, void* ws, int* status, int* lau
     return e != cudaSuccess ? e : launch_linear_fused(l, p.x16, p.fx, p.fw, p.sb, status, st);
   }
   GemmArgs g;
-  const int bn = l.M > 128 ? 256 : 128;
+  const bool sums = l.a.out_type == MOEQ_F32;
+  const int bn = sums ? 128 : 256;
   if (!half_map(&g.tm_w, p.w16, l.in_dim, l.out_dim, p.w_parts, kTile) ||
       !half_map(&g.tm_x, p.x16, l.in_dim, l.M, p.x_parts, bn / 2))
     return cudaErrorNotSupported;
@@ -664,7 +709,7 @@ cudaError_t launch_linear_gemm(const LinArgs& l, void* ws, int* status, int* lau
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) e = p.w_parts == 2 ? run_weights<true>(p, st) : run_weights<false>(p, st);
   if (e != cudaSuccess) return e;
-  return bn == 256 ? run_gemm<256>(g, sms, st) : run_gemm<128>(g, sms, st);
+  return sums ? run_gemm<128, true>(g, sms, st) : run_gemm<256, false>(g, sms, st);
 }
 
 }  // namespace moeq
