@@ -414,7 +414,7 @@ struct GemmArgs {
 template <int BN>
 struct GemmSmem {
   static constexpr uint32_t A = kTile * 128, B = BN / 2 * 128;
-  static constexpr int STAGES = BN == 256 ? 6 : 8;
+  static constexpr int STAGES = 6;
   static constexpr uint32_t BYTES = STAGES * (A + B) + 1024;
 };
 
@@ -427,7 +427,7 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* tmap,
       : "memory");
 }
 
-// Warps 0: TMA, 1: MMA (rank 0), 2: TMEM; 4..11: epilogue.
+// Warps 0: TMA, 1: MMA (rank 0), 2: TMEM; 4..11 (SUMS: 4..19): epilogue.
 //
 // The tensor cores cut their sums off (towards zero): a chain of n products of
 // 16 columns comes out about n 2^-27 too small.  A bf16 y does not show it;
@@ -435,9 +435,10 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* tmap,
 // the parts are added in registers, rounded to nearest: the two accumulators
 // then take turns within a tile too.
 constexpr int kChunk = 8;
+constexpr int gemm_threads(bool sums) { return sums ? 640 : 384; }
 
 template <int BN, bool SUMS>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(SUMS), 1)
     k_lin_gemm(const __grid_constant__ GemmArgs a) {
   using S = GemmSmem<BN>;
   constexpr int ST = S::STAGES;
@@ -454,7 +455,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&tmem_full[i], 1);
-      tc::mbar_init(&tmem_empty[i], 16);  // eight warps of both CTAs
+      tc::mbar_init(&tmem_empty[i], SUMS ? 32 : 16);  // the epilogue warps of both CTAs
     }
     tc::fence_mbar_init();
   }
@@ -531,9 +532,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
       const int oc = min(o, a.l.out_dim - 1);
       const float fw = a.fw[oc];
       const float bias = a.l.a.bias ? bf16_bits_to_float(a.l.a.bias[oc]) : 0.0f;
-      const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + half * (BN / 2);
+      constexpr int C = SUMS ? BN / 4 : BN / 2;  // columns of this warp
+      const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + half * C;
       if (SUMS) {
-        constexpr int C = BN / 2;  // columns of this warp
         uint32_t sum[C];
 #pragma unroll
         for (int j = 0; j < C; ++j) sum[j] = 0u;
@@ -542,12 +543,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
           if (!wait_bar(&tmem_full[acc], (tile >> 1) & 1u, a.status)) goto done;
           tc::tc_fence_after();
 #pragma unroll
-          for (int c0 = 0; c0 < C; c0 += 32) {
-            uint32_t v[32];
-            tc::tmem_ld32(lanes + acc * BN + c0, v);
+          for (int c0 = 0; c0 < C; c0 += 16) {
+            uint32_t v[16];
+            tmem_ld16(lanes + acc * BN + c0, v);
             tc::tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
+            for (int j = 0; j < 16; ++j)
               sum[c0 + j] = __float_as_uint(__uint_as_float(sum[c0 + j]) + __uint_as_float(v[j]));
           }
           tc::tc_fence_before();
@@ -556,14 +557,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
             tc::mbar_arrive_cluster(tc::mapa_shared(tc::smem_u32(&tmem_empty[acc]), 0));
         }
 #pragma unroll
-        for (int c0 = 0; c0 < C; c0 += 16) {
-          const int m = m0 + half * C + c0, nm = min(16, a.l.M - m);
+        for (int c0 = 0; c0 < C; c0 += 8) {
+          const int m = m0 + half * C + c0, nm = min(8, a.l.M - m);
           if (nm <= 0) break;
-          uint32_t v[16];
+          uint32_t v[8];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] = sum[c0 + j];
+          for (int j = 0; j < 8; ++j) v[j] = sum[c0 + j];
           const float fx = lane < nm ? a.fx[m + lane] : 0.0f;
-          finish<float, 16>(a.l.a, m, nm, oc, live, fw, bias, fx, v);
+          finish<float, 8>(a.l.a, m, nm, oc, live, fw, bias, fx, v);
         }
       } else {
         const uint32_t acc = tile & 1u;
@@ -571,8 +572,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
         tc::tc_fence_after();
         ++tile;
 #pragma unroll 1
-        for (int c0 = 0; c0 < BN / 2; c0 += 32) {
-          const int m = m0 + half * (BN / 2) + c0, nm = min(32, a.l.M - m);
+        for (int c0 = 0; c0 < C; c0 += 32) {
+          const int m = m0 + half * C + c0, nm = min(32, a.l.M - m);
           if (nm <= 0) break;
           uint32_t v[32];
           tc::tmem_ld32(lanes + acc * BN + c0, v);
@@ -644,7 +645,8 @@ cudaError_t run_gemm(GemmArgs& g, int sms, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int64_t items = (int64_t)g.tiles_o * g.tiles_m;
   const int64_t units = items < sms / 2 ? items : sms / 2;
-  return launch_after(k_lin_gemm<BN, SUMS>, (unsigned)(2 * units), 384, bytes, st, g);
+  return launch_after(k_lin_gemm<BN, SUMS>, (unsigned)(2 * units), gemm_threads(SUMS), bytes, st,
+                      g);
 }
 
 }  // namespace
@@ -692,8 +694,7 @@ cudaError_t launch_linear_gemm(const LinArgs& l, void* ws, int* status, int* lau
     return e != cudaSuccess ? e : launch_linear_fused(l, p.x16, p.fx, p.fw, p.sb, status, st);
   }
   GemmArgs g;
-  const bool sums = l.a.out_type == MOEQ_F32;
-  const int bn = sums ? 128 : 256;
+  constexpr int bn = 256;
   if (!half_map(&g.tm_w, p.w16, l.in_dim, l.out_dim, p.w_parts, kTile) ||
       !half_map(&g.tm_x, p.x16, l.in_dim, l.M, p.x_parts, bn / 2))
     return cudaErrorNotSupported;
@@ -709,7 +710,8 @@ cudaError_t launch_linear_gemm(const LinArgs& l, void* ws, int* status, int* lau
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) e = p.w_parts == 2 ? run_weights<true>(p, st) : run_weights<false>(p, st);
   if (e != cudaSuccess) return e;
-  return sums ? run_gemm<128, true>(g, sms, st) : run_gemm<256, false>(g, sms, st);
+  return l.a.out_type == MOEQ_F32 ? run_gemm<bn, true>(g, sms, st)
+                                  : run_gemm<bn, false>(g, sms, st);
 }
 
 }  // namespace moeq
