@@ -353,7 +353,8 @@ __global__ void __launch_bounds__(256) k_lin_tokens(const __grid_constant__ Prep
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, groups = l.in_dim / l.G;
   const int o0 = ((int)blockIdx.x - p.x_blocks) * 8;
   const int64_t o = min(o0 + warp, l.out_dim - 1);
-  const float f = row_lift(l, o), up = __fdividef(1.0f, f);
+  const float f = row_lift(l, o);                                         // 2^-k
+  const float up = __uint_as_float((254u << 23) - __float_as_uint(f));  // 2^k
   if (lane == 0) p.fw[o] = f;
   const int g8 = threadIdx.x >> 3, r8 = threadIdx.x & 7;
   for (int g0 = 0; g0 < groups; g0 += 32) {

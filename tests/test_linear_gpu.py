@@ -80,6 +80,9 @@ def check(M, n, o, bits, G, xt="bf16", group=0, mx=False, act="none", bias=False
     return y
 
 
+# Sizes that take each of the three ways: products of the codes, weights
+# unpacked inside the product, weights laid out before it.
+WAYS = {"codes": (9, 130), "inside": (100, 700), "before": (2600, 1930)}
 FORMATS = [(2, 64, False), (2, 32, False), (2, 128, False), (3, 64, False), (3, 32, False),
            (4, 32, False), (4, 64, False), (4, 128, False), (5, 32, False), (5, 128, False),
            (6, 32, False), (6, 64, False), (8, 32, False), (8, 64, False), (8, 128, False),
@@ -92,6 +95,58 @@ ROWS = [1, 8, 9, 16, 17, 33, 64, 65, 130, 300]
 def test_formats(bits, G, mx, M):
     check(M, 384, 130, bits, G, mx=mx, out="f32")
     check(M, 1024, 67, bits, G, mx=mx, out="bf16", bias=True)
+
+
+@pytest.mark.parametrize("way", list(WAYS))
+@pytest.mark.parametrize("bits,G,mx", FORMATS)
+def test_formats_every_way(bits, G, mx, way):
+    M, o = WAYS[way]
+    check(M, 384, o, bits, G, mx=mx, out="f32")
+    check(M, 640, o, bits, G, mx=mx, out="bf16", bias=True)
+
+
+@pytest.mark.parametrize("way", list(WAYS))
+@pytest.mark.parametrize("n,bits,G", [(32, 4, 32), (32, 8, 32), (64, 2, 64), (64, 6, 32), (96, 4, 32),
+                                      (160, 8, 32), (288, 4, 32), (320, 8, 64), (448, 2, 32),
+                                      (1056, 4, 32), (2080, 8, 32), (128, 5, 32), (640, 3, 128)])
+def test_odd_columns_every_way(n, bits, G, way):
+    M, o = WAYS[way]
+    check(M, n, o, bits, G, out="f32", res=True)
+    check(M, n, o, bits, G, out="bf16")
+    if G == 32 and bits == 4:
+        check(M, n, o, 4, 32, mx=True, out="bf16")
+
+
+@pytest.mark.parametrize("way", list(WAYS))
+@pytest.mark.parametrize("xt,group", [("int8", 0), ("int8", 128), ("e4m3", 0), ("e4m3", 128)])
+def test_eight_bit_tokens_every_way(xt, group, way):
+    M, o = WAYS[way]
+    for n, bits, G in ((640, 4, 64), (416, 8, 32)):
+        check(M, n, o, bits, G, xt, group, out="f32", res=True)
+        check(M, n, o, bits, G, xt, group, out="bf16", act="silu", mul=True)
+
+
+@pytest.mark.parametrize("way", list(WAYS))
+@pytest.mark.parametrize("act", ["none", "silu", "gelu", "gelu_tanh", "relu", "sigmoid"])
+def test_epilogue_every_way(act, way):
+    M, o = WAYS[way]
+    for out in ("f32", "bf16"):
+        check(M, 256, o, 4, 64, act=act, bias=True, mul=True, res=True, out=out)
+
+
+@pytest.mark.parametrize("M,o,n", [(40, 2000, 8192), (20, 700, 12288), (20, 700, 12544), (300, 300, 16384),
+                                   (2600, 1930, 4096), (17, 8200, 1024), (513, 260, 1024)])
+def test_long_sums_in_fp32(M, o, n):
+    """fp32 outputs over thousands of columns stay near the 64-bit sum: the
+    tensor cores cut off at most 96 additions in a row at about 2^-27 each
+    (7.2e-7), then parts are added with rounding (at most 32 of them, 2^-24
+    each in the worst case, far less in norm): under 1.5e-6 in norm."""
+    g = gen(n + M)
+    w = ref.matrix(o, n, 4, 64, g)
+    x, _ = tokens(M, n, "bf16", 0, g)
+    y = linear(qt(w, o, n, 4, 64), x, T["f32"])
+    want = x.double() @ w["dense"].t()
+    assert float((y.double() - want).norm() / want.norm()) < 1.5e-6
 
 
 @pytest.mark.parametrize("M", [1, 5, 24, 100, 257])
@@ -131,12 +186,12 @@ def test_larger(M, n, o, bits, G, out):
     check(M, n, o, bits, G, out=out, act="silu", res=True)
 
 
-@pytest.mark.parametrize("M", [3, 150])
+@pytest.mark.parametrize("M,o", [(3, 45), (150, 45), (150, 701), (2600, 1931)])
 @pytest.mark.parametrize("out", ["f32", "bf16"])
-def test_strides_in_place_and_untouched_memory(out, M):
+def test_strides_in_place_and_untouched_memory(out, M, o):
     """Rows inside wider ones, y in the residual's memory, rows behind the last
     left as they were; the same values as the plain call."""
-    n, o = 256, 45
+    n = 256
     g = gen(M)
     w = ref.matrix(o, n, 4, 64, g)
     t = qt(w, o, n, 4, 64)
@@ -158,9 +213,9 @@ def test_strides_in_place_and_untouched_memory(out, M):
     linear(t, x[:0], T[out])
 
 
-@pytest.mark.parametrize("M", [2, 9, 200])
-def test_expert_of_a_bank(M):
-    n, o, E = 256, 64, 3
+@pytest.mark.parametrize("M,o", [(2, 64), (9, 64), (200, 704), (2600, 1930)])
+def test_expert_of_a_bank(M, o):
+    n, E = 256, 3
     g = gen(3)
     ws = [ref.matrix(o, n, 4, 64, g) for _ in range(E)]
     bank = [torch.stack([w[k] for w in ws]).contiguous() for k in ("w", "s", "b")]
@@ -171,12 +226,12 @@ def test_expert_of_a_bank(M):
         assert torch.equal(linear(t, x, expert=e), one)
 
 
-@pytest.mark.parametrize("M", [4, 40, 300])
+@pytest.mark.parametrize("M,o", [(4, 80), (40, 80), (300, 700), (2600, 1930)])
 @pytest.mark.parametrize("out", ["f32", "bf16"])
-def test_a_bad_token_stays_alone(out, M):
+def test_a_bad_token_stays_alone(out, M, o):
     """A row of NaN and infinities changes no other row; huge and tiny rows
     keep their own precision."""
-    n, o = 512, 80
+    n = 512
     g = gen(9)
     w = ref.matrix(o, n, 4, 64, g)
     t = qt(w, o, n, 4, 64)
@@ -198,11 +253,11 @@ def test_a_bad_token_stays_alone(out, M):
     assert torch.equal(got[3].float(), want[3].float() * 2.0 ** -90)
 
 
-@pytest.mark.parametrize("M", [1, 31, 400])
-def test_two_calls_at_once_and_in_a_graph(M):
+@pytest.mark.parametrize("M,o", [(1, 320), (31, 320), (400, 320), (60, 2000), (2600, 1930)])
+def test_two_calls_at_once_and_in_a_graph(M, o):
     """Two streams with a workspace each, and a captured call replayed on new
     tokens, give the plain call's values."""
-    n, o = 1024, 320
+    n = 1024
     g = gen(12)
     w = ref.matrix(o, n, 4, 64, g)
     t = qt(w, o, n, 4, 64)

@@ -51,6 +51,37 @@ def test_route_groups(M, E, K, groups, keep, top, with_bias, score):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("E,K,groups,keep,top", [
+    (128, 8, 8, 3, 1), (128, 8, 8, 4, 2), (100, 3, 1, 1, 1), (64, 8, 4, 2, 2), (16, 2, 2, 1, 1),
+    (256, 8, 8, 4, 2), (200, 16, 1, 1, 1), (256, 9, 16, 5, 1), (128, 9, 8, 4, 2),
+    (128, 8, 16, 4, 2), (512, 8, 8, 4, 2)])
+def test_many_rows(E, K, groups, keep, top, with_bias, score):
+    """More than 16 rows per SM: several rows share a warp."""
+    M = 2371 if E < 512 else 2369
+    l, b = draw(M, E, E + K)
+    l[5, ::3] = float("-inf")
+    l[7] = float("nan")
+    l[8] = float("-inf")
+    l[8, 1] = 0.5
+    check(l, K, b if with_bias else None, score, groups, keep, top, renorm=K % 2 == 0)
+
+
+def test_near_ties_in_many_rows():
+    """Rows that need the second look, beside rows that do not, in one warp."""
+    E, M = 64, 2500
+    l, b = draw(M, E, 77)
+    tie = torch.linspace(-1e-6, 1e-6, E, device="cuda")
+    for m in range(0, M, 3):
+        l[m] = tie.roll(m)
+    flat = 0.5 - torch.sigmoid(l[0].double()).float()
+    check(l, 8, flat, "sigmoid")
+    check(l, 8, flat, "sigmoid", 8, 4, 2)
+    check(l, 6, flat, "softmax", 4, 2, 1)
+    check(l.to(torch.bfloat16), 6, (b * 20).round() / 20, "sigmoid", 8, 3, 2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_bf16_logits_tie_by_index(score):
     """bf16 logits tie often; so do equal biases."""
     l, b = draw(200, 256, 5, torch.bfloat16)
