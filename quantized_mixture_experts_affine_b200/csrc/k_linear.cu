@@ -13,8 +13,6 @@
 namespace moeq {
 namespace {
 
-constexpr int kWarps = 8;
-
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
@@ -149,18 +147,18 @@ __device__ __forceinline__ void four_scales(const uint16_t* p, int64_t at, int s
 // the spans; their sums are added in warp order.  A warp asks for everything
 // of U spans before it uses the first, so that its run of a 4096-column row
 // costs one trip to memory.
-template <int BITS, bool MX, int C, int NT, int U>
-__global__ void __launch_bounds__(kWarps * 32, 2) k_linear_small(const __grid_constant__ LinArgs l) {
+template <int BITS, bool MX, int C, int NT, int U, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) k_linear_small(const __grid_constant__ LinArgs l) {
   constexpr int W = Run<BITS, C>::WORDS;
   constexpr int TOKS = 8 * NT;
-  __shared__ float red[kWarps][16][TOKS + 1];
+  __shared__ float red[WARPS][16][TOKS + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int o0 = blockIdx.x * 16;
   const int64_t m0 = (int64_t)blockIdx.y * TOKS;
   const int spans = l.in_dim / (4 * C);
   // (whole fours of spans per warp: see below)
   const int fours = (spans + 3) >> 2;
-  const int sp0 = 4 * (fours * warp / kWarps), sp1 = min(4 * (fours * (warp + 1) / kWarps), spans);
+  const int sp0 = 4 * (fours * warp / WARPS), sp1 = min(4 * (fours * (warp + 1) / WARPS), spans);
   const int64_t words_per_row = (int64_t)l.in_dim * BITS / 32;
   // spans per group: 1, or 2 (64-column spans in groups of 128)
   const int shift = l.G == 4 * C ? 0 : 1;
@@ -244,14 +242,14 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_linear_small(const __grid_co
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (base + u >= sp1) break;
+      const bool in = base + u < sp1;  // (otherwise the last span again, times 0)
       uint32_t a[2][C / 2];
       float sf[2], bf[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         to_pairs<BITS, MX, C>(w[u][h], a[h]);
-        sf[h] = MX ? mx_scale(s[u][h]) : __uint_as_float(s[u][h] << 16);
-        bf[h] = MX ? 0.0f : __uint_as_float(b[u][h] << 16);
+        sf[h] = !in ? 0.0f : MX ? mx_scale(s[u][h]) : __uint_as_float(s[u][h] << 16);
+        bf[h] = !in || MX ? 0.0f : __uint_as_float(b[u][h] << 16);
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -269,7 +267,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_linear_small(const __grid_co
         }
         float f[2] = {1.0f, 1.0f};
         if (by128) {
-          const int64_t c = (int64_t)(base + u) * (4 * C) >> 7;
+          const int64_t c = (int64_t)min(base + u, sp1 - 1) * (4 * C) >> 7;
 #pragma unroll
           for (int i = 0; i < 2; ++i)
             f[i] = l.a.x_scales[min(m0 + 8 * n + 2 * t + i, (int64_t)l.M - 1) * xsg + c];
@@ -291,20 +289,29 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_linear_small(const __grid_co
   if (mine) {
     float v = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k) v += red[k][erow][etok];
+    for (int k = 0; k < WARPS; ++k) v += red[k][erow][etok];
     if (!bf16 && !by128) v *= ep.x_scale;
     ep.finish(l.a, em, o0 + erow, v);
   }
 }
 
+template <int BITS, bool MX, int C, int WARPS>
+void run_warps(const LinArgs& l, int blocks, cudaStream_t st) {
+  if (l.M <= 8)
+    k_linear_small<BITS, MX, C, 1, 4, WARPS><<<blocks, WARPS * 32, 0, st>>>(l);
+  else
+    k_linear_small<BITS, MX, C, 2, 2, WARPS>
+        <<<dim3(blocks, (l.M + 15) / 16), WARPS * 32, 0, st>>>(l);
+}
+
+// Sixteen warps a CTA (fewer spans for each) while one CTA per SM is all there
+// are, eight when two have to share an SM.
 template <int BITS, bool MX, int C>
 cudaError_t run(const LinArgs& l, cudaStream_t st) {
   const int blocks = (l.out_dim + 15) / 16;
-  if (l.M <= 8)
-    k_linear_small<BITS, MX, C, 1, 4><<<blocks, kWarps * 32, 0, st>>>(l);
-  else
-    k_linear_small<BITS, MX, C, 2, 2>
-        <<<dim3(blocks, (l.M + 15) / 16), kWarps * 32, 0, st>>>(l);
+  const int64_t ctas = (int64_t)blocks * (l.M <= 8 ? 1 : (l.M + 15) / 16);
+  if (ctas <= sm_count() && l.in_dim / (4 * C) > 32) run_warps<BITS, MX, C, 16>(l, blocks, st);
+  else run_warps<BITS, MX, C, 8>(l, blocks, st);
   return cudaGetLastError();
 }
 
