@@ -22,7 +22,7 @@ SYNTH = os.path.join(PKG, "synth")
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
-COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",
+COMMON = ["--threads", "0", "-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",
           "--expt-relaxed-constexpr", "-shared", "-cudart", "static"]
 
 
@@ -48,7 +48,8 @@ def _nvcc(target: str, srcs: list[str], deps: list[str], extra: list[str], force
 
 def build_moeq(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
-    deps = sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [os.path.join(INCLUDE, "moeq.h")]
+    deps = (sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) +
+            sorted(glob.glob(os.path.join(CSRC, "*.h"))) + [os.path.join(INCLUDE, "moeq.h")])
     extra = ["-I", INCLUDE, "-I", CSRC]
     if ptxas_verbose:
         extra += ["-Xptxas", "-v"]

@@ -14,6 +14,8 @@
 // memory, each CTA adding up, in rank order, and finishing its share of the
 // tokens.  The weights of the run are pulled into L2 first, while the tokens'
 // layout kernel still runs.
+#include <type_traits>
+
 #include "lingemm.cuh"
 
 namespace moeq {
@@ -381,6 +383,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_lin_fused(const __grid_constant
   tc::tc_fence_after();
   // where a token's sums are added up
   const uint32_t sums = base + (a.own_sums ? (uint32_t)ST * STAGE : 0u);
+  // Eight tokens at a time; what a chunk reads from memory is asked for one
+  // chunk ahead, the first before the sums are exchanged.
+  using T = typename std::conditional<TWO, float, uint16_t>::type;
+  T res[8] = {};
+  float fx = 0.0f;
+  auto ahead = [&](int c0) {
+    const int nm = min(min(8, nt - c0), l.M - (n0 + c0));
+    if (warp < 4 || nm <= 0) return;
+    if (l.a.residual) column(l.a.residual, l.a.residual_stride, n0 + c0, nm, oc, res);
+    fx = lane < nm ? a.fx[n0 + c0 + lane] : 0.0f;
+  };
+  ahead(share * 8);
   if (lsplit) {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     // each partial sum goes to the rank that finishes its token:
@@ -443,12 +457,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_lin_fused(const __grid_constant
             v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(u[j]));
         }
       }
-      const float fx = lane < nm ? a.fx[n0 + c0 + lane] : 0.0f;
-      const float f = lsplit ? 1.0f : fw;
-      if (l.a.out_type == MOEQ_F32)
-        finish<float, 8>(l.a, n0 + c0, nm, oc, live, f, bias, fx, v);
-      else
-        finish<uint16_t, 8>(l.a, n0 + c0, nm, oc, live, f, bias, fx, v);
+      T now[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) now[j] = res[j];
+      const float fx_now = fx;
+      ahead(c0 + 32);
+      finish_with<T, 8>(l.a, n0 + c0, nm, oc, live, lsplit ? 1.0f : fw, bias, fx_now, v, now);
     }
   }
   tc::tc_fence_before();

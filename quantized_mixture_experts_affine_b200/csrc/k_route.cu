@@ -339,17 +339,23 @@ __device__ __forceinline__ float fast_numerator(const moeq_routing& r, float l, 
 
 template <int L>
 __device__ __forceinline__ uint32_t seg_max(uint32_t v) {
-  if (L == 32) return __reduce_max_sync(0xffffffffu, v);
+  if constexpr (L == 32) {
+    return __reduce_max_sync(0xffffffffu, v);
+  } else {
 #pragma unroll
-  for (int o = L >> 1; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+    for (int o = L >> 1; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+  }
 }
 template <int L>
 __device__ __forceinline__ uint32_t seg_min(uint32_t v) {
-  if (L == 32) return __reduce_min_sync(0xffffffffu, v);
+  if constexpr (L == 32) {
+    return __reduce_min_sync(0xffffffffu, v);
+  } else {
 #pragma unroll
-  for (int o = L >> 1; o > 0; o >>= 1) v = min(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+    for (int o = L >> 1; o > 0; o >>= 1) v = min(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+  }
 }
 template <int L>
 __device__ __forceinline__ float seg_sum(float v) {

@@ -109,13 +109,12 @@ __device__ __forceinline__ void as_out(float v, uint16_t* p) {
   *reinterpret_cast<__nv_bfloat16*>(p) = __float2bfloat16_rn(v);
 }
 
-// T: the type of y, mul and the residual (uint16_t: bf16 bits).
+// T: the type of y, mul and the residual (uint16_t: bf16 bits).  r: the
+// residual's values, read ahead (unused without one).
 template <typename T, int N>
-__device__ __forceinline__ void finish(const moeq_linear_args& a, int64_t m0, int nm, int o,
-                                       bool live, float fw, float bias, float fx,
-                                       const uint32_t (&acc)[N]) {
-  T r[N];
-  if (a.residual) column(a.residual, a.residual_stride, m0, nm, o, r);
+__device__ __forceinline__ void finish_with(const moeq_linear_args& a, int64_t m0, int nm, int o,
+                                            bool live, float fw, float bias, float fx,
+                                            const uint32_t (&acc)[N], const T (&r)[N]) {
   float y[N];
 #pragma unroll
   for (int j = 0; j < N; ++j)
@@ -137,6 +136,14 @@ __device__ __forceinline__ void finish(const moeq_linear_args& a, int64_t m0, in
     for (int j = 0; j < N; ++j)
       if (j < nm) as_out(y[j], c + j * a.y_stride);
   }
+}
+template <typename T, int N>
+__device__ __forceinline__ void finish(const moeq_linear_args& a, int64_t m0, int nm, int o,
+                                       bool live, float fw, float bias, float fx,
+                                       const uint32_t (&acc)[N]) {
+  T r[N];
+  if (a.residual) column(a.residual, a.residual_stride, m0, nm, o, r);
+  finish_with<T, N>(a, m0, nm, o, live, fw, bias, fx, acc, r);
 }
 
 // [parts][rows][cols] fp16, boxes of 64 columns x `box` rows, 128-byte swizzle;

@@ -211,14 +211,17 @@ def _device(name, t) -> int:
 def _rows(name, t, M, n, dtype=None, device=None):
     """Row stride of a [M][n] tensor whose rows are contiguous, of the given
     type and on the given device; raises ValueError otherwise."""
-    if t.shape != (M, n) or (n > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name}: expected [{M}][{n}] with contiguous rows, got "
-                         f"{tuple(t.shape)} with strides {t.stride()}")
+    stride = n
+    if t.shape != (M, n) or not t.is_contiguous():
+        if t.shape != (M, n) or (n > 1 and t.stride(1) != 1):
+            raise ValueError(f"{name}: expected [{M}][{n}] with contiguous rows, got "
+                             f"{tuple(t.shape)} with strides {t.stride()}")
+        stride = t.stride(0) if M > 1 else n
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
     if device is not None and t.get_device() != device:
         raise ValueError(f"{name}: on {t.device}, not on CUDA device {device}")
-    return t.stride(0) if M > 1 else n
+    return stride
 
 
 def _dense(name, t, shape, dtype, device):
