@@ -331,10 +331,17 @@ __device__ bool route_row(const RouteArgs& a, int m, typename Keys<T>::K* keys, 
 // the picks themselves is settled on the spot: the few experts concerned are
 // scored in fp64, one per lane, and ranked again.
 
-// 1 / (1 + e^-z) and e^d; expf is within 2 ulp, the fast division too.
+// 1 / (1 + e^-z) and e^d; the fast exponential and division are within 2 ulp,
+// but for the exponent's rounding.
 __device__ __forceinline__ float fast_numerator(const moeq_routing& r, float l, float mx) {
-  if (r.score == MOEQ_SCORE_SIGMOID) return __fdividef(1.0f, 1.0f + expf(-r.router_scale * l));
-  return l == mx ? 1.0f : expf(r.router_scale * (l - mx));
+  if (r.score == MOEQ_SCORE_SIGMOID) return __fdividef(1.0f, 1.0f + __expf(-r.router_scale * l));
+  return l == mx ? 1.0f : __expf(r.router_scale * (l - mx));
+}
+
+// Keys<float>::of for what is not NaN (v + 0 makes one zero of both).
+__device__ __forceinline__ uint32_t key_of(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 
 template <int L>
@@ -444,7 +451,7 @@ __device__ __forceinline__ bool route_regs(const RouteArgs& a, int m, bool store
     sum = seg_sum<L>(z);
   }
   const float inv = __fdividef(1.0f, sum);
-  // Error of a score relative to the largest: expf 2^-22, division 2^-22, the
+  // Error of a score relative to the largest: exponential 2^-22, division 2^-22, the
   // exponent's and the last roundings under 2^-22 (e^-d d < 0.37), and the
   // normaliser's additions
   const float s_max = is_out(mx) ? 0.0f : fast_numerator(r, mx, mx) * inv;
@@ -457,7 +464,7 @@ __device__ __forceinline__ bool route_regs(const RouteArgs& a, int m, bool store
     for (int c = 0; c < 4; ++c) {
       const int e = 4 * (lane + L * j) + c;
       const float v = BIAS ? fast_numerator(r, l[j][c], mx) * inv + b[j][c] : l[j][c];
-      k[j][c] = e >= E ? 0u : is_out(l[j][c]) ? 1u : KT::of(v);
+      k[j][c] = e >= E ? 0u : is_out(l[j][c]) ? 1u : BIAS ? KT::of(v) : key_of(v);
     }
 
   bool sure = true;
