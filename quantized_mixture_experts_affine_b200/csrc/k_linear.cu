@@ -1,13 +1,19 @@
 // Linear with few tokens: y = x W^T on the packed codes, exact products.
 //
-// A warp owns 16 rows of W and a run of columns; mma.m16n8k16 (bf16,
-// fp32 sums) multiplies the codes, which bf16 holds exactly (integers to
-// 255, or E2M1 values), with eight tokens at a time.  The codes go from
-// global memory straight into the fragments: the order of the columns
-// within a product is free as long as both operands share it, so lane t of
-// a quad takes C neighbouring columns of a span of 4 C, which lies in one
-// scale group.  Per span the sums of q x enter the total as
-// s sum(q x) + b sum(x); sum(x) is one more product, with ones.
+// A CTA owns 16 rows of W and all columns, a warp a run of them; mma.m16n8k16
+// (bf16, fp32 sums) multiplies the codes, which bf16 holds exactly (integers to
+// 255, or E2M1 values), with eight tokens at a time.  The codes go from global
+// memory straight into the fragments: the order of the columns within a product
+// is free as long as both operands share it, so lane t of a quad takes C
+// neighbouring columns of a span of 4 C, which lies in one scale group.  Per
+// span the sums of q x enter the total as s sum(q x) + b sum(x); sum(x) is one
+// more product, with ones.
+//
+// mma.sync, not tcgen05: up to 16 tokens the products are a small part of the
+// time, and fragments from registers need no shared-memory tiles, no token
+// layout and no TMEM.  Bound by latency: two rounds of loads and products per
+// warp.  One token 4096 x 4096, 4-bit: 7.0 us (1.3 TB/s; a launch is about 2 of
+// it); 8 tokens in int8, 1024 rows: 5.7 us; 64 tokens, 512 rows of 8 bits: 7.1.
 #include "lincommon.cuh"
 
 namespace moeq {

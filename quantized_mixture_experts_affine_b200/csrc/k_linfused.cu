@@ -2,18 +2,27 @@
 //
 // For some tens to hundreds of tokens a separate pass that writes W in fp16
 // would cost more than the product.  Here a CTA owns 128 rows of W and a run of
-// columns: eight warps unpack the codes of 64 columns at a time to fp16 in the
-// 128-byte swizzle (one fused multiply-add each, a single rounding; for an fp32
-// y a second tile holds what it left), TMA brings the tokens' 64 columns, and
-// one thread issues D (128 rows of W) x (up to 256 tokens) in TMEM.  The tokens
-// are fp16 rows with a power of two each, from k_lin_tokens, as
-// are the weights' scales, each row's times a power of its own.
+// columns: sixteen warps unpack the codes to fp16 in the 128-byte swizzle (one
+// fused multiply-add each, a single rounding; for an fp32 y a second tile holds
+// what it left), TMA brings the tokens, and one thread issues D (128 rows of W)
+// x (up to 256 tokens) in TMEM.  The tokens are fp16 rows with a power of two
+// each, from k_lin_tokens, as are the weights' scales, times a power of their
+// row.
 //
 // The columns are split over a cluster of up to eight CTAs, so that few rows
-// of W still fill the GPU; the partial sums meet through distributed shared
-// memory, each CTA adding up, in rank order, and finishing its share of the
-// tokens.  The weights of the run are pulled into L2 first, while the tokens'
-// layout kernel still runs.
+// of W still fill the GPU; each partial sum is pushed through distributed
+// shared memory to the CTA that finishes its token, which adds the parts in
+// rank order.  The weights of the run are pulled into L2 first, while the
+// tokens' layout kernel still runs.
+//
+// What bounds it: under about 128 tokens the time around the loop (16 tokens,
+// 4096 x 4096, 4-bit, 11.3 us: layout 2.5, prologue 2, unpacking 4, exchange
+// and epilogue 2), above that the products (1024 tokens 44.6 us, 0.77 PFLOP/s:
+// the tile's operands and the unpacked weights together need 1.5 times an SM's
+// shared-memory bandwidth).  A thread takes 64 neighbouring codes, so its loads
+// are wide and one or two scales serve them: with 16 codes and a scale from
+// memory per block the loop was bound by the cache lines its loads touched
+// (13.3 us).
 #include <type_traits>
 
 #include "lingemm.cuh"

@@ -1,17 +1,20 @@
 // Grouped top-k routing: softmax or sigmoid scores, a balance bias that only
 // the selection sees, group-limited choice, renormalised weights.
 //
-// One warp per token.  The selection is exact: it gives what real arithmetic
-// would.  Without a bias the experts are ordered by their logits.  With one
-// (and for the sums of two that rank groups) the scores are taken in fp32
-// first, with a bound on their error; only a row in which two candidates
-// that decide something lie closer than that bound is done again in fp64.
-// Near ties are rare (under 1 % of rows of 512 normal logits), so the row
-// costs what the fp32 pass costs.
+// The selection is exact: it gives what real arithmetic would.  Without a bias
+// the experts are ordered by their logits.  With one (and for the sums of two
+// that rank groups) the scores are taken in fp32 first, with a bound on their
+// error; where two candidates that decide something lie closer than that, fp64
+// decides: for picks among the few experts concerned, one per lane, for groups
+// the whole row again.  Such rows are under 1 % of 512 normal logits.
 //
-// Keys live in shared memory, four experts of a lane side by side, so that
-// one code path serves 1 to 4096 experts and a pick rescans the winning
-// lane's experts only.
+// A row of up to 512 experts is held in registers by a warp, or with many rows
+// by 8 or 16 lanes; any other shape (k_route_any) lives in shared memory.  Few
+// rows are bound by the chain of load, exponential and K picks (4 us for one
+// row, 6 us for 2048 rows of 256 experts in 8 groups), many by instruction
+// issue (16,068 rows of 128 in 8 groups, top-8: 11.4 us; 15.4 us with picks
+// that scanned 16 registers instead of a quad in shared memory, 24.3 us with a
+// warp per row).
 #include "common.cuh"
 #include "ops.h"
 #include "route.cuh"
