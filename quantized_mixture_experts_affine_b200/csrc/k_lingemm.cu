@@ -420,12 +420,14 @@ struct GemmArgs {
   int k_blocks;   // 64-column blocks of one product
   int products;   // 1: w x; 2: + (rest of w) x; 3: + w (rest of x)
   int tiles_o, tiles_m;
+  int tokens;     // of a tile, a multiple of 16
   int* status;
 };
 
-template <int BN>
+constexpr int kMaxTokens = 256;  // of a tile
+
 struct GemmSmem {
-  static constexpr uint32_t A = kTile * 128, B = BN / 2 * 128;
+  static constexpr uint32_t A = kTile * 128, B = kMaxTokens / 2 * 128;
   static constexpr int STAGES = 6;
   static constexpr uint32_t BYTES = STAGES * (A + B) + 1024;
 };
@@ -449,10 +451,11 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* tmap,
 constexpr int kChunk = 8;
 constexpr int gemm_threads(bool sums) { return sums ? 640 : 384; }
 
-template <int BN, bool SUMS>
+template <bool SUMS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(SUMS), 1)
     k_lin_gemm(const __grid_constant__ GemmArgs a) {
-  using S = GemmSmem<BN>;
+  using S = GemmSmem;
+  const int BN = a.tokens;
   constexpr int ST = S::STAGES;
   extern __shared__ uint8_t dyn[];
   __shared__ uint64_t full[ST], empty[ST], tmem_full[2], tmem_empty[2];
@@ -472,7 +475,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(SUMS), 
     tc::fence_mbar_init();
   }
   if (warp == 2) {
-    tc::tmem_alloc_pair(&tmem_holder, 2 * BN < 32 ? 32 : 2 * BN);
+    tc::tmem_alloc_pair(&tmem_holder, 2 * kMaxTokens);
     tc::tmem_relinquish_pair();
   }
   tc::tc_fence_before();
@@ -498,7 +501,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(SUMS), 
             if (lane == 0) {
               const uint32_t bar = tc::mapa_shared(tc::smem_u32(&full[s]), 0);
               const uint32_t at = base + s * (S::A + S::B);
-              if (rank == 0) tc::mbar_arrive_expect_tx(&full[s], 2 * (S::A + S::B));
+              if (rank == 0) tc::mbar_arrive_expect_tx(&full[s], 2 * S::A + (uint32_t)BN * 128);
               tma_load_3d_pair(at, &a.tm_w, kb * kBK, o0, prod == 1 ? 1 : 0, bar);
               tma_load_3d_pair(at + S::A, &a.tm_x, kb * kBK, m0, prod == 2 ? 1 : 0, bar);
             }
@@ -509,7 +512,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(SUMS), 
     for (int j = 0; j < ST; ++j, ++it)
       if (!wait_bar(&empty[it % ST], ((it / ST) & 1u) ^ 1u, a.status)) goto done;
   } else if (warp == 1 && rank == 0) {
-    constexpr uint32_t IDESC = tc::idesc_f16_f32(2 * kTile, BN);
+    const uint32_t idesc = tc::idesc_f16_f32(2 * kTile, BN);
     const uint32_t on = elect_one();
     uint32_t it = 0, tile = 0;
     for (int item = unit0; item < items; item += units)
@@ -517,7 +520,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(SUMS), 
         const uint32_t acc = tile & 1u;
         if (!wait_bar(&tmem_empty[acc], ((tile >> 1) & 1u) ^ 1u, a.status)) goto done;
         tc::tc_fence_after();
-        const uint32_t d = tmem + acc * BN;
+        const uint32_t d = tmem + acc * kMaxTokens;
         const int n = min(chunk, KB - k0) * a.products;
         for (int kb = 0; kb < n; ++kb, ++it) {
           const uint32_t s = it % ST;
@@ -527,7 +530,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(SUMS), 
           const uint64_t db = tc::sw128_kmajor_desc(base + s * (S::A + S::B) + S::A);
 #pragma unroll
           for (int kk = 0; kk < kBK / 16; ++kk)
-            mma_if<true>(on, d, da + 2 * kk, db + 2 * kk, IDESC, (kb | kk) != 0);
+            mma_if<true>(on, d, da + 2 * kk, db + 2 * kk, idesc, (kb | kk) != 0);
           if (on) tc::mma_commit_pair(&empty[s], 3);
           __syncwarp();
         }
@@ -544,20 +547,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(SUMS), 
       const int oc = min(o, a.l.out_dim - 1);
       const float fw = a.fw[oc];
       const float bias = a.l.a.bias ? bf16_bits_to_float(a.l.a.bias[oc]) : 0.0f;
-      constexpr int C = SUMS ? BN / 4 : BN / 2;  // columns of this warp
+      const int C = SUMS ? kMaxTokens / 4 : BN / 2;  // columns of this warp
       const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + half * C;
       if (SUMS) {
-        uint32_t sum[C];
+        constexpr int CS = kMaxTokens / 4;
+        uint32_t sum[CS];
 #pragma unroll
-        for (int j = 0; j < C; ++j) sum[j] = 0u;
+        for (int j = 0; j < CS; ++j) sum[j] = 0u;
         for (int k0 = 0; k0 < KB; k0 += chunk, ++tile) {
           const uint32_t acc = tile & 1u;
           if (!wait_bar(&tmem_full[acc], (tile >> 1) & 1u, a.status)) goto done;
           tc::tc_fence_after();
 #pragma unroll
-          for (int c0 = 0; c0 < C; c0 += 16) {
+          for (int c0 = 0; c0 < CS; c0 += 16) {
             uint32_t v[16];
-            tmem_ld16(lanes + acc * BN + c0, v);
+            tmem_ld16(lanes + acc * kMaxTokens + c0, v);
             tc::tmem_wait_ld();
 #pragma unroll
             for (int j = 0; j < 16; ++j)
@@ -569,8 +573,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(SUMS), 
             tc::mbar_arrive_cluster(tc::mapa_shared(tc::smem_u32(&tmem_empty[acc]), 0));
         }
 #pragma unroll
-        for (int c0 = 0; c0 < C; c0 += 8) {
-          const int m = m0 + half * C + c0, nm = min(8, a.l.M - m);
+        for (int c0 = 0; c0 < CS; c0 += 8) {
+          const int m = m0 + half * C + c0, nm = min(min(8, BN - half * C - c0), a.l.M - m);
           if (nm <= 0) break;
           uint32_t v[8];
 #pragma unroll
@@ -585,10 +589,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(SUMS), 
         ++tile;
 #pragma unroll 1
         for (int c0 = 0; c0 < C; c0 += 32) {
-          const int m = m0 + half * C + c0, nm = min(32, a.l.M - m);
+          const int m = m0 + half * C + c0, nm = min(min(32, C - c0), a.l.M - m);
           if (nm <= 0) break;
           uint32_t v[32];
-          tc::tmem_ld32(lanes + acc * BN + c0, v);
+          tc::tmem_ld32(lanes + acc * kMaxTokens + c0, v);
           const float fx = lane < nm ? a.fx[m + lane] : 0.0f;
           tc::tmem_wait_ld();
           finish<uint16_t, 32>(a.l.a, m, nm, oc, live, fw, bias, fx, v);
@@ -604,7 +608,7 @@ done:
   tc::cluster_sync();
   if (warp == 2) {
     tc::tc_fence_after();
-    tc::tmem_dealloc_pair(tmem, 2 * BN < 32 ? 32 : 2 * BN);
+    tc::tmem_dealloc_pair(tmem, 2 * kMaxTokens);
   }
 }
 
@@ -649,15 +653,34 @@ int x_parts_of(int x_type, int x_group, int out_type) {
   return out_type == MOEQ_F32 && x_type != MOEQ_BF16 && x_group == 128 ? 2 : 1;
 }
 
-template <int BN, bool SUMS>
+// Tokens of a tile: those whose waves take least.  A block of 64 columns costs
+// a pair the bytes it brings, 128 rows of W and half the tokens per CTA, in
+// proportion 256 + tokens; larger tiles bring fewer, smaller ones may fill the
+// last wave better.
+int tile_tokens(int64_t M, int64_t out_dim, int pairs) {
+  const int64_t tiles_o = (out_dim + 2 * kTile - 1) / (2 * kTile);
+  int best = kMaxTokens;
+  int64_t least = INT64_MAX;
+  for (int n = kMaxTokens; n >= 96; n -= 16) {
+    const int64_t tiles = tiles_o * ((M + n - 1) / n);
+    const int64_t cost = (tiles + pairs - 1) / pairs * (256 + n);
+    if (cost < least) {
+      least = cost;
+      best = n;
+    }
+  }
+  return best;
+}
+
+template <bool SUMS>
 cudaError_t run_gemm(GemmArgs& g, int sms, cudaStream_t st) {
-  constexpr uint32_t bytes = GemmSmem<BN>::BYTES;
-  cudaError_t e = cudaFuncSetAttribute(k_lin_gemm<BN, SUMS>,
+  constexpr uint32_t bytes = GemmSmem::BYTES;
+  cudaError_t e = cudaFuncSetAttribute(k_lin_gemm<SUMS>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   if (e != cudaSuccess) return e;
   const int64_t items = (int64_t)g.tiles_o * g.tiles_m;
   const int64_t units = items < sms / 2 ? items : sms / 2;
-  return launch_after(k_lin_gemm<BN, SUMS>, (unsigned)(2 * units), gemm_threads(SUMS), bytes, st,
+  return launch_after(k_lin_gemm<SUMS>, (unsigned)(2 * units), gemm_threads(SUMS), bytes, st,
                       g);
 }
 
@@ -706,7 +729,8 @@ cudaError_t launch_linear_gemm(const LinArgs& l, void* ws, int* status, int* lau
     return e != cudaSuccess ? e : launch_linear_fused(l, p.x16, p.fx, p.fw, p.sb, status, st);
   }
   GemmArgs g;
-  constexpr int bn = 256;
+  const int bn = tile_tokens(l.M, l.out_dim, sms / 2);
+  g.tokens = bn;
   if (!half_map(&g.tm_w, p.w16, l.in_dim, l.out_dim, p.w_parts, kTile) ||
       !half_map(&g.tm_x, p.x16, l.in_dim, l.M, p.x_parts, bn / 2))
     return cudaErrorNotSupported;
@@ -722,8 +746,7 @@ cudaError_t launch_linear_gemm(const LinArgs& l, void* ws, int* status, int* lau
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) e = p.w_parts == 2 ? run_weights<true>(p, st) : run_weights<false>(p, st);
   if (e != cudaSuccess) return e;
-  return l.a.out_type == MOEQ_F32 ? run_gemm<bn, true>(g, sms, st)
-                                  : run_gemm<bn, false>(g, sms, st);
+  return l.a.out_type == MOEQ_F32 ? run_gemm<true>(g, sms, st) : run_gemm<false>(g, sms, st);
 }
 
 }  // namespace moeq
