@@ -15,11 +15,13 @@
 // rank order.  The weights of the run are pulled into L2 first, while the
 // tokens' layout kernel still runs.
 //
-// What bounds it: under about 128 tokens the time around the loop (16 tokens,
-// 4096 x 4096, 4-bit, 11.3 us: layout 2.5, prologue 2, unpacking 4, exchange
-// and epilogue 2), above that the products (1024 tokens 44.6 us, 0.77 PFLOP/s:
-// the tile's operands and the unpacked weights together need 1.5 times an SM's
-// shared-memory bandwidth).  A thread takes 64 neighbouring codes, so its loads
+// What bounds it: under about 128 tokens the time around the loop (64 tokens,
+// 4096 x 4096, 4-bit, bf16 y, 12.4 us, of which the layout's launch 2.5, the
+// prologue 2, unpacking 4), above that the products (256 tokens 20.8 us, 480
+// tokens 28.5 us, 0.57 PFLOP/s: the tile's operands and the unpacked weights
+// together need 1.5 times an SM's shared-memory bandwidth, and one wave has no
+// other tile to hide its ends behind).  fp32 y: 64 tokens 17.0 us, 256 tokens
+// 26.7 us.  A thread takes 64 neighbouring codes, so its loads
 // are wide and one or two scales serve them: with 16 codes and a scale from
 // memory per block the loop was bound by the cache lines its loads touched
 // (13.3 us).
@@ -240,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lin_fused(const __grid_constant
     }
     // the rest of the run, and what the epilogue reads, into L2
     const char* p = reinterpret_cast<const char*>(row + (kb0 >> 2) * (8 * BITS));
-    const char* e = p + min((kb1 - kb0) * 8 * BITS, (l.in_dim - kb0 * kBK) / 8 * BITS);
+    const char* e = p + min((kb1 - kb0) * 8, (l.in_dim - kb0 * kBK) / 8 - 8 * part) * BITS;
 #pragma unroll 1
     for (const char* c = p + 64 * BITS; c < e; c += 32 * BITS)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(c));
@@ -520,22 +522,52 @@ cudaError_t run_format(const FusedLinArgs& a, int split, int to, int tm, uint32_
   }
 }
 
+constexpr uint32_t kRoom = 224 * 1024;  // shared memory for stages and sums
+uint32_t block_bytes(int n, bool two) { return (two ? 2 : 1) * kRows * 128 + (uint32_t)n * 128; }
+// Whether the sums of n tokens have a place beside four blocks.
+bool own_sums(int n, bool two) { return kRoom >= (uint32_t)n * kRows * 4 + 4 * block_bytes(n, two); }
+
 }  // namespace
 
-// As many CTAs as SMs, a run of columns each at least.  The tensor cores cut
-// their sums off, about n 2^-27 for n products of 16 columns: for an fp32 y a
-// CTA takes at most six runs (96 products; the rounding rests of the weights
-// have an accumulator of their own).
-int linear_fused_split(int64_t M, int64_t in_dim, int64_t out_dim, int out_type) {
-  const int64_t tiles = (M + 255) / 256 * ((out_dim + kRows - 1) / kRows);
-  const int64_t runs = (in_dim + 255) / 256;
-  int split = 1;
-  while (split < 8 && 2 * split * tiles <= 148 && runs >= 2 * split) split *= 2;
-  if (out_type == MOEQ_F32) {
-    while (split < 8 && runs > 6 * split) split *= 2;
-    if (runs > 6 * split) return 0;
+// Tiles and clusters of a call, and its clocks.
+//
+// As many CTAs as SMs, a run of columns each at least.  A cluster lies within
+// one GPC: of four CTAs (one per SM) 33 fit at a time, of eight 15 (fewer where
+// a GPU has other SMs switched off, so 32 and 14 here); one more and they take
+// two waves (64 x 4096 x 2048: 16 tiles in clusters of eight 16.6 us, of four
+// 11.7).  The tensor cores cut their sums off, about n 2^-27 for n products of
+// 16 columns: for an fp32 y a CTA takes at most six runs (96 products; the
+// rounding rests of the weights have an accumulator of their own).
+//
+// The clocks are fits to measured calls: a block of 64 columns takes 190 and 3.5
+// a token, 470 at least for its unpacking (fp32 y: 750 and 4.2), the exchange of
+// sums 2500 and 22 a token, 4000 more where it has to wait for the stages' place,
+// an epilogue without it 12 a token, the rest 8500.  So 256 tokens are two tiles
+// of 128 where the GPU has room (4096 x 2048: 20.2 -> 14.7 us; 2048 x 1024:
+// 15.2 -> 9.5).
+LinPlan linear_fused_plan(int64_t M, int64_t in_dim, int64_t out_dim, int out_type) {
+  const int64_t tiles_o = (out_dim + kRows - 1) / kRows, runs = (in_dim + 255) / 256;
+  const bool two = out_type == MOEQ_F32;
+  const int fit[4] = {148, 74, 32, 14};
+  LinPlan best = {0, 0, 0, 0.0};
+  const int64_t first = (M + 255) / 256;
+  for (int64_t tiles_m = first; tiles_m <= first + 3; ++tiles_m) {
+    const int64_t n = ((M + tiles_m - 1) / tiles_m + 15) / 16 * 16;
+    const int64_t tiles = (M + n - 1) / n * tiles_o;
+    int l = 0;
+    while (l < 3 && tiles <= fit[l + 1] && runs >= 2 << l) ++l;
+    if (two)
+      while (l < 3 && runs > 6 << l) ++l;
+    if ((two && runs > 6 << l) || tiles_m > 65535) break;  // (tiles_m: the grid's limit)
+    const double block = two ? 750 + 4.2 * n : n > 80 ? 190 + 3.5 * n : 470;
+    const double waves = (double)((tiles + fit[l] - 1) / fit[l]);
+    const double end = l ? 2500 + 22.0 * n + (own_sums((int)n, two) ? 0 : 4000) : 12.0 * n;
+    const double clocks =
+        8500 + waves * (4.0 * ((runs + (1 << l) - 1) >> l) * block + end);
+    if (best.tokens == 0 || clocks < best.clocks) best = {(int)n, l, (int)((M + n - 1) / n), clocks};
+    if (n <= 64) break;
   }
-  return split;
+  return best;
 }
 
 cudaError_t launch_linear_fused(const LinArgs& l, const __half* x16, const float* fx,
@@ -547,24 +579,23 @@ cudaError_t launch_linear_fused(const LinArgs& l, const __half* x16, const float
   a.fw = fw;
   a.sb = sb;
   a.status = status;
-  const int tiles_m = (l.M + 255) / 256;
-  a.n = ((l.M + tiles_m - 1) / tiles_m + 15) / 16 * 16;
+  const LinPlan plan = linear_fused_plan(l.M, l.in_dim, l.out_dim, l.a.out_type);
+  a.n = plan.tokens;
   a.k_runs = (l.in_dim + 255) / 256;
+  a.log2_split = plan.log2_split;
+  const int split = 1 << plan.log2_split, tiles_m = plan.tiles_m;
   const int tiles_o = (l.out_dim + kRows - 1) / kRows;
-  const int split = linear_fused_split(l.M, l.in_dim, l.out_dim, l.a.out_type);
-  a.log2_split = split == 8 ? 3 : split == 4 ? 2 : split == 2 ? 1 : 0;
   a.log2_group = l.G == 32 ? 5 : l.G == 64 ? 6 : 7;
   a.tmem_cols = 32;
   const bool two = l.a.out_type == MOEQ_F32;
   while (a.tmem_cols < a.n * (two ? 2 : 1)) a.tmem_cols *= 2;
-  const uint32_t block = (two ? 2 : 1) * kRows * 128 + (uint32_t)a.n * 128;
+  const uint32_t block = block_bytes(a.n, two);
   const uint32_t sums = split > 1 ? (uint32_t)a.n * kRows * 4 : 0u;
   // Two stages at least; as many blocks in each (up to four) as fit, so that
   // the waits and fences around a stage are paid seldom.
-  const uint32_t room = 224 * 1024;
-  a.own_sums = room >= sums + 4 * block;
-  const uint32_t left = room - (a.own_sums ? sums : 0u);
-  a.per = left >= 8 * block ? 4 : left >= 4 * block ? 2 : 1;
+  a.own_sums = own_sums(a.n, two);
+  const uint32_t left = kRoom - (a.own_sums ? sums : 0u);
+  a.per = left >= 8 * block ? 4 : left >= 4 * block && a.n <= 192 ? 2 : 1;
   a.stages = (int)(left / (block * a.per));
   if (a.stages > 4) a.stages = 4;
   uint32_t bytes = (uint32_t)a.stages * a.per * block;

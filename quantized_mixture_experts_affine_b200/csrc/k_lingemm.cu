@@ -11,10 +11,11 @@
 // sum of the parts' products.
 //
 // The third (k_lin_gemm) is a persistent GEMM on CTA pairs (cta_group::2):
-// D (256 rows of W) x (256 tokens) per pair in TMEM, two accumulators,
-// operands by TMA in the 128-byte swizzle.  A tile of that size needs 64
-// bytes a clock and SM from L2, about what an SM gets; one of 128 tokens needs
-// 96 and ran at two thirds of the rate.  W's rows are D's rows, so a lane of
+// D (256 rows of W) x (up to 256 tokens) per pair in TMEM, two accumulators,
+// operands by TMA in the 128-byte swizzle.  A tile of 256 tokens needs 64
+// bytes a clock and SM from L2, about what an SM gets; one of 128 needs 96 and
+// ran at two thirds of the rate, so smaller tiles are taken only where they
+// fill the waves better (tile_tokens below).  W's rows are D's rows, so a lane of
 // the epilogue holds one output column o: bias and row power are one register,
 // and a warp's accesses to y, mul and the residual are 32 neighbours at any
 // alignment and stride.  The residual is read before the stores that might
@@ -24,8 +25,8 @@
 // Measured, 16,068 tokens, 4096 x 4096, 8-bit, bf16 y, residual: layout 36 us
 // beside 16 us (16,068 x 4096 tokens are 263 MB), GEMM 342 to 366 us (1.5
 // PFLOP/s), the call 416 us; under the power cap of a long loop 484 us.
-// 2048 tokens, 2048 x 4096, MX FP4: 40 us, of which the GEMM 27 (128 tiles are
-// two waves of 74 pairs).
+// 2048 tokens, 2048 x 4096, MX FP4: 39 us, of which the GEMM 26 (144 tiles
+// of 240 tokens: two waves of 74 pairs, nearly full).
 #include "lingemm.cuh"
 
 namespace moeq {
@@ -612,15 +613,46 @@ done:
   }
 }
 
-// The weights are unpacked inside the product (k_linfused.cu) while its tiles
-// of 128 rows x 256 tokens take one wave of the GPU, and always for a single
-// tile of tokens, which reads them once.  Beyond, every token tile would unpack
-// them again, and laying them out once wins: 4096 x 4096, 4-bit, bf16 y, 1024
-// tokens (128 tiles) 46.3 against 46.9 us, 1536 tokens (192 tiles) 84.1
-// against 65.6 us; 1024 rows, 2048 tokens (64 tiles) 34.6 against 38.5 us.
+// Tokens of a tile: those whose waves take least.  A block of 64 columns costs
+// a pair the bytes it brings, 128 rows of W and half the tokens per CTA, in
+// proportion 256 + tokens; larger tiles bring fewer, smaller ones may fill the
+// last wave better.
+int tile_tokens(int64_t M, int64_t out_dim, int pairs) {
+  const int64_t tiles_o = (out_dim + 2 * kTile - 1) / (2 * kTile);
+  int best = kMaxTokens;
+  int64_t least = INT64_MAX;
+  for (int n = kMaxTokens; n >= 96; n -= 16) {
+    const int64_t tiles = tiles_o * ((M + n - 1) / n);
+    const int64_t cost = (tiles + pairs - 1) / pairs * (256 + n);
+    if (cost < least) {
+      least = cost;
+      best = n;
+    }
+  }
+  return best;
+}
+
+// Whether the weights are unpacked inside the product (k_linfused.cu): for up to
+// 256 tokens always (there it needs a small workspace only), beyond while its
+// clocks are fewer than this way's.  These are a fit too: 8000 around it, 900 per
+// million weights and token values laid out (twice the weights for an fp32 y;
+// 1900 beyond 20 million, which L2 does not keep), and the waves' blocks.
+// Inside against laid out first, 4096 x 4096, 4-bit: bf16 y, 256 tokens 20.8 and
+// 26.5 us, 320 tokens 22.1 and 27.2, 480 tokens 28.5 and 28.6, 768 tokens 43.1
+// and 35.6; fp32 y, 256 tokens 26.7 and 50.3, 400 tokens 45.5 and 52.0, 640
+// tokens 69.7 and 55.9.
 bool unpack_inside(int64_t M, int64_t in_dim, int64_t out_dim, int out_type) {
-  const int64_t tiles_m = (M + 255) / 256, tiles_o = (out_dim + 127) / 128;
-  return (tiles_m == 1 || tiles_m * tiles_o <= 148) && linear_fused_split(M, in_dim, out_dim, out_type);
+  const LinPlan plan = linear_fused_plan(M, in_dim, out_dim, out_type);
+  if (plan.tokens == 0) return false;
+  if (M <= 256) return true;
+  const int64_t pairs = 74, n = tile_tokens(M, out_dim, (int)pairs);
+  const int64_t tiles = (M + n - 1) / n * ((out_dim + 2 * kTile - 1) / (2 * kTile));
+  const int parts = out_type == MOEQ_F32 ? 2 : 1;
+  const double laid = 1e-6 * (double)(in_dim * (out_dim * parts + M));  // millions
+  const double clocks =
+      8000 + 900 * laid + (laid > 20 ? 1000 * (laid - 20) : 0) +
+      (double)((tiles + pairs - 1) / pairs * ((in_dim + kBK - 1) / kBK) * (256 + n) * parts);
+  return plan.clocks <= clocks;
 }
 
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -653,25 +685,6 @@ int x_parts_of(int x_type, int x_group, int out_type) {
   return out_type == MOEQ_F32 && x_type != MOEQ_BF16 && x_group == 128 ? 2 : 1;
 }
 
-// Tokens of a tile: those whose waves take least.  A block of 64 columns costs
-// a pair the bytes it brings, 128 rows of W and half the tokens per CTA, in
-// proportion 256 + tokens; larger tiles bring fewer, smaller ones may fill the
-// last wave better.
-int tile_tokens(int64_t M, int64_t out_dim, int pairs) {
-  const int64_t tiles_o = (out_dim + 2 * kTile - 1) / (2 * kTile);
-  int best = kMaxTokens;
-  int64_t least = INT64_MAX;
-  for (int n = kMaxTokens; n >= 96; n -= 16) {
-    const int64_t tiles = tiles_o * ((M + n - 1) / n);
-    const int64_t cost = (tiles + pairs - 1) / pairs * (256 + n);
-    if (cost < least) {
-      least = cost;
-      best = n;
-    }
-  }
-  return best;
-}
-
 template <bool SUMS>
 cudaError_t run_gemm(GemmArgs& g, int sms, cudaStream_t st) {
   constexpr uint32_t bytes = GemmSmem::BYTES;
@@ -692,8 +705,10 @@ size_t linear_gemm_workspace(const moeq_qtensor& t, int M, int x_type, int out_t
   const size_t fused = fused_layout(M, t.in_dim, t.out_dim, t.group_size).total;
   const size_t gemm =
       layout(M, t.in_dim, t.out_dim, xp, out_type == MOEQ_F32 ? 2 : 1).total;
-  if (!unpack_inside(M, t.in_dim, t.out_dim, out_type)) return gemm;
-  return xp == 1 || fused > gemm ? fused : gemm;
+  // beyond 256 tokens the choice may turn with M: room for both, so that a
+  // workspace for many tokens serves fewer
+  if (M <= 256 && xp == 1 && unpack_inside(M, t.in_dim, t.out_dim, out_type)) return fused;
+  return fused > gemm ? fused : gemm;
 }
 
 cudaError_t launch_linear_gemm(const LinArgs& l, void* ws, int* status, int* launches,
@@ -729,7 +744,7 @@ cudaError_t launch_linear_gemm(const LinArgs& l, void* ws, int* status, int* lau
     return e != cudaSuccess ? e : launch_linear_fused(l, p.x16, p.fx, p.fw, p.sb, status, st);
   }
   GemmArgs g;
-  const int bn = tile_tokens(l.M, l.out_dim, sms / 2);
+  const int bn = tile_tokens(l.M, l.out_dim, 74);
   g.tokens = bn;
   if (!half_map(&g.tm_w, p.w16, l.in_dim, l.out_dim, p.w_parts, kTile) ||
       !half_map(&g.tm_x, p.x16, l.in_dim, l.M, p.x_parts, bn / 2))

@@ -35,8 +35,15 @@ cudaError_t launch_linear_small(const LinArgs& l, cudaStream_t st);
 size_t linear_gemm_workspace(const moeq_qtensor& t, int M, int x_type, int out_type);
 cudaError_t launch_linear_gemm(const LinArgs& l, void* ws, int* status, int* launches,
                                cudaStream_t st);
-// CTAs that share a row's columns there; 0: its sums would be too long.
-int linear_fused_split(int64_t M, int64_t in_dim, int64_t out_dim, int out_type);
+// Tiling of the product that unpacks the weights itself (tokens 0: its sums
+// would be too long for the type of y) and the clocks that a call takes.
+struct LinPlan {
+  int tokens;      // of a tile
+  int log2_split;  // CTAs that share a row's columns
+  int tiles_m;
+  double clocks;
+};
+LinPlan linear_fused_plan(int64_t M, int64_t in_dim, int64_t out_dim, int out_type);
 // The product with the weights unpacked inside it, on tokens laid out
 // in fp16 (fx, fw: the powers of two of token and weight rows; sb: scales and biases
 // as fp16 pairs, [group][out_dim], times the weight row's power).

@@ -101,8 +101,11 @@ def test_formats(bits, G, mx, M):
 @pytest.mark.parametrize("bits,G,mx", FORMATS)
 def test_formats_every_way(bits, G, mx, way):
     M, o = WAYS[way]
+    before = moeq.moeq_launch_count()
     check(M, 384, o, bits, G, mx=mx, out="f32")
     check(M, 640, o, bits, G, mx=mx, out="bf16", bias=True)
+    # one kernel, two (tokens laid out first), three (weights too)
+    assert moeq.moeq_launch_count() - before == 2 * (1 + list(WAYS).index(way))
 
 
 @pytest.mark.parametrize("way", list(WAYS))
@@ -147,6 +150,16 @@ def test_long_sums_in_fp32(M, o, n):
     y = linear(qt(w, o, n, 4, 64), x, T["f32"])
     want = x.double() @ w["dense"].t()
     assert float((y.double() - want).norm() / want.norm()) < 1.5e-6
+
+
+def test_a_workspace_for_many_tokens_serves_fewer():
+    g = gen(5)
+    for n, o in ((1024, 1024), (4096, 2048), (288, 5000)):
+        t = qt(ref.matrix(o, n, 4, 64 if n > 288 else 32, g), o, n, 4, 64 if n > 288 else 32)
+        for xt in (torch.bfloat16, torch.int8):
+            for out in (torch.bfloat16, torch.float32):
+                need = [moeq.moeq_linear_workspace_bytes(t, M, xt, out) for M in range(1, 1200, 7)]
+                assert need == sorted(need) and need[0] == 0
 
 
 @pytest.mark.parametrize("M", [1, 5, 24, 100, 257])
