@@ -733,27 +733,29 @@ template <int L, int NQ, bool GROUPS, bool BIAS>
 __global__ void __launch_bounds__(256) k_route_regs(const __grid_constant__ RouteArgs a) {
   constexpr int ROWS = 32 / L;
   const int lane = threadIdx.x & 31;
-  const int m0 = (blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * ROWS;
+  const int64_t m0 = ((int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * ROWS;
   if (m0 >= a.M) return;
   float* raw;
   uint64_t* mine = warp_slots(a, raw);
-  const int m = m0 + lane / L;
-  const bool settled = route_regs<L, NQ, GROUPS, BIAS>(a, min(m, a.M - 1), m < a.M,
-                                                       reinterpret_cast<uint32_t*>(mine));
-  uint32_t left = __ballot_sync(0xffffffffu, !settled && m < a.M && lane % L == 0);
+  const bool in = m0 + lane / L < a.M;
+  const int m = in ? (int)m0 + lane / L : a.M - 1;
+  const bool settled =
+      route_regs<L, NQ, GROUPS, BIAS>(a, m, in, reinterpret_cast<uint32_t*>(mine));
+  uint32_t left = __ballot_sync(0xffffffffu, !settled && in && lane % L == 0);
   if (L == 32) {
-    if (left) route_row64(a, m0, mine, raw);
+    if (left) route_row64(a, (int)m0, mine, raw);
     return;
   }
   constexpr int NQ32 = NQ * L / 32 > 0 ? NQ * L / 32 : 1;
   for (; left; left &= left - 1)
-    route_again<NQ32, GROUPS, BIAS>(a, m0 + (__ffs(left) - 1) / L, mine, raw);
+    route_again<NQ32, GROUPS, BIAS>(a, (int)m0 + (__ffs(left) - 1) / L, mine, raw);
 }
 
 // Any number of experts and groups of any size.
 __global__ void __launch_bounds__(256) k_route_any(const __grid_constant__ RouteArgs a) {
-  const int m = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (m >= a.M) return;
+  const int64_t row = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (row >= a.M) return;
+  const int m = (int)row;
   float* raw;
   uint64_t* mine = warp_slots(a, raw);
   if (!route_row<float>(a, m, reinterpret_cast<uint32_t*>(mine), raw)) route_row64(a, m, mine, raw);
@@ -801,15 +803,15 @@ cudaError_t launch_route_groups(const moeq_routing& r, const void* logits, int l
     if (nq <= 32 && r.top_k <= 8 && !(groups && (gq > 8 || r.n_groups > 8))) lanes = 8;
     else if (nq <= 64 && r.top_k <= 16 && !(groups && (gq > 16 || r.n_groups > 16))) lanes = 16;
   }
-  const int rows = (M + 32 / lanes - 1) / (32 / lanes);  // warps
+  const int64_t rows = ((int64_t)M + 32 / lanes - 1) / (32 / lanes);  // warps
   // 48 bytes per quad of experts and warp (48 KB hold one row of 4096); in
   // registers 384 for a row's candidates and 64 per lane for its keys
   const size_t slot = regs && nq < 51 ? 384 + 32 * 64 : (size_t)nq * 48;
   a.slot = (int)(slot / 8);
-  int warps = (rows + sms - 1) / sms;  // few rows: spread over the SMs first
-  if (warps > 8) warps = 8;
+  // few rows: spread over the SMs first
+  int warps = (int)(rows > 8 * (int64_t)sms ? 8 : (rows + sms - 1) / sms);
   while (warps > 1 && warps * slot > 48 * 1024) --warps;
-  const int blocks = (rows + warps - 1) / warps, threads = warps * 32;
+  const int blocks = (int)((rows + warps - 1) / warps), threads = warps * 32;
   const size_t smem = warps * slot;
   if (!regs) k_route_any<<<blocks, threads, smem, st>>>(a);
   else if (lanes == 8) run_regs<8, 4>(a, groups, blocks, threads, smem, st);

@@ -175,3 +175,13 @@ def test_deterministic_in_a_graph_on_another_stream():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(idx, i0) and torch.equal(w, w0)
+
+
+def test_as_many_rows_as_an_int_counts():
+    M = 2 ** 31 - 1
+    idx = torch.full((M, 1), -1, dtype=torch.int32, device="cuda")
+    w = torch.zeros(M, 1, device="cuda")
+    l = torch.ones(M, 1, dtype=torch.bfloat16, device="cuda")
+    moeq.moeq_route_groups(moeq.routing(1, 1), l, idx, w)
+    assert int(idx.max()) == 0 and int(idx.min()) == 0
+    assert float(w.max()) == 1 and float(w.min()) == 1
