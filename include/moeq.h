@@ -450,9 +450,10 @@ typedef struct {
  * the gate's), router logits of a whole prompt.  An I8 or E4M3 x with its
  * scales is moeq_add_rmsnorm's output.
  * Sums are fp32 throughout.  Few tokens multiply the codes themselves
- * (exact products).  Many tokens with a bf16 y take weights rounded to fp16
- * (relative 2^-11, an eighth of y's own rounding); with an fp32 y the
- * weights keep 22 bits.  Neither has a range limit: rows are scaled by powers of two.
+ * (exact products; |x| up to 2^110, the sums are of codes times x).  Many
+ * tokens with a bf16 y take weights rounded to fp16 (relative 2^-11, an eighth
+ * of y's own rounding); with an fp32 y the weights keep 22 bits.  Neither has
+ * a range limit: rows are scaled by powers of two.
  * An x row that holds an infinity or NaN gives a row of unspecified values
  * and leaves the others untouched.
  *   y may be mul's or residual's memory (same stride); it may not overlap x.

@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lin_fused(const __grid_constant
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           st_cluster(tc::mapa_shared(to, (uint32_t)dst) + (uint32_t)(tl * (kRows * 4)),
-                     __float_as_uint(__uint_as_float(v[j]) * fw));
+                     v[j]);
           if (++tl == nt) tl = 0, ++dst;
         }
       }
@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_lin_fused(const __grid_constant
       for (int j = 0; j < 8; ++j) now[j] = res[j];
       const float fx_now = fx;
       ahead(c0 + 32);
-      finish_with<T, 8>(l.a, n0 + c0, nm, oc, live, lsplit ? 1.0f : fw, bias, fx_now, v, now);
+      finish_with<T, 8>(l.a, n0 + c0, nm, oc, live, fw, bias, fx_now, v, now);
     }
   }
   tc::tc_fence_before();

@@ -25,7 +25,7 @@
 // Measured, 16,068 tokens, 4096 x 4096, 8-bit, bf16 y, residual: layout 36 us
 // beside 16 us (16,068 x 4096 tokens are 263 MB), GEMM 342 to 366 us (1.5
 // PFLOP/s), the call 416 us; under the power cap of a long loop 484 us.
-// 2048 tokens, 2048 x 4096, MX FP4: 39 us, of which the GEMM 26 (144 tiles
+// 2048 tokens, 2048 x 4096, MX FP4: 38 us, of which the GEMM 25 (144 tiles
 // of 240 tokens: two waves of 74 pairs, nearly full).
 #include "lingemm.cuh"
 
@@ -585,6 +585,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(SUMS), 
         }
       } else {
         const uint32_t acc = tile & 1u;
+        auto power = [&](int c0) {  // of the chunk's tokens, asked for one chunk ahead
+          const int i = half * C + c0 + lane;
+          return c0 + lane < C && m0 + i < a.l.M ? a.fx[m0 + i] : 0.0f;
+        };
+        float next = power(0);
         if (!wait_bar(&tmem_full[acc], (tile >> 1) & 1u, a.status)) goto done;
         tc::tc_fence_after();
         ++tile;
@@ -594,7 +599,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(SUMS), 
           if (nm <= 0) break;
           uint32_t v[32];
           tc::tmem_ld32(lanes + acc * kMaxTokens + c0, v);
-          const float fx = lane < nm ? a.fx[m + lane] : 0.0f;
+          const float fx = next;
+          next = power(c0 + 32);
           tc::tmem_wait_ld();
           finish<uint16_t, 32>(a.l.a, m, nm, oc, live, fw, bias, fx, v);
         }

@@ -110,7 +110,8 @@ __device__ __forceinline__ void as_out(float v, uint16_t* p) {
 }
 
 // T: the type of y, mul and the residual (uint16_t: bf16 bits).  r: the
-// residual's values, read ahead (unused without one).
+// residual's values, read ahead (unused without one).  (The two powers first:
+// huge weights and tiny tokens make up for one another.)
 template <typename T, int N>
 __device__ __forceinline__ void finish_with(const moeq_linear_args& a, int64_t m0, int nm, int o,
                                             bool live, float fw, float bias, float fx,
@@ -118,7 +119,7 @@ __device__ __forceinline__ void finish_with(const moeq_linear_args& a, int64_t m
   float y[N];
 #pragma unroll
   for (int j = 0; j < N; ++j)
-    y[j] = __uint_as_float(acc[j]) * fw * __shfl_sync(0xffffffffu, fx, j) + bias;
+    y[j] = __uint_as_float(acc[j]) * (fw * __shfl_sync(0xffffffffu, fx, j)) + bias;
   act_all(y, a.act);
   if (a.mul) {
     T f[N];

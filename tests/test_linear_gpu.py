@@ -266,6 +266,22 @@ def test_a_bad_token_stays_alone(out, M, o):
     assert torch.equal(got[3].float(), want[3].float() * 2.0 ** -90)
 
 
+@pytest.mark.parametrize("way", list(WAYS))
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_huge_weights_and_tiny_tokens(out, way):
+    """Powers of two that cancel change no bit."""
+    M, o = WAYS[way]
+    n = 512
+    g = gen(31)
+    w = ref.matrix(o, n, 4, 64, g)
+    x, _ = tokens(M, n, "bf16", 0, g)
+    x = torch.where(x.abs() < 2.0 ** -8, torch.full_like(x, 2.0 ** -8), x)
+    y = linear(qt(w, o, n, 4, 64), x, T[out])
+    h = dict(w, s=w["s"] * 2.0 ** 118, b=w["b"] * 2.0 ** 118)
+    got = linear(qt(h, o, n, 4, 64), x * 2.0 ** -114, T[out])
+    assert torch.equal(got.float(), y.float() * 16)
+
+
 @pytest.mark.parametrize("M,o", [(1, 320), (31, 320), (400, 320), (60, 2000), (2600, 1930)])
 def test_two_calls_at_once_and_in_a_graph(M, o):
     """Two streams with a workspace each, and a captured call replayed on new

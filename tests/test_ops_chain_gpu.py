@@ -1,6 +1,10 @@
 """The routing, norm and linear operators together, as a model runs them:
 norm with 8-bit output -> dense block (gate, up, down) -> norm -> layer under
 a grouped sigmoid router."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -121,3 +125,42 @@ def test_the_chain_in_a_graph():
         torch.cuda.synchronize()
         for a, b in zip(out, want[k]):
             assert torch.equal(a, b)
+
+
+FIRST = """
+import sys
+sys.path[:0] = {path!r}
+import torch
+import ops_reference as ref
+from quantized_mixture_experts_affine_b200 import moeq
+from quantized_mixture_experts_affine_b200.layer import add_rmsnorm, linear, route_groups
+g = torch.Generator(device="cuda").manual_seed(1)
+w = ref.matrix(1930, 256, 4, 64, g)
+t = moeq.qtensor(w["w"], w["s"], w["b"], 1930, 256, 4, 64)
+gamma = torch.ones(256, device="cuda", dtype=torch.bfloat16)
+xs = [torch.randn(M, 256, device="cuda", generator=g) for M in (3, 100, 2600)]
+R = moeq.routing(1930, 8, moeq.SCORE_SIGMOID, 10, 4, 2)
+def step():
+    outs = []
+    for x in xs:
+        _, y, q, s = add_rmsnorm(x, gamma, 1e-6, q_dtype=torch.int8)
+        l = linear(t, y, torch.float32)
+        outs += [l, linear(t, q, torch.bfloat16, x_scales=s), *route_groups(R, l)]
+    return outs
+graph = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(graph):
+    outs = step()
+graph.replay()
+torch.cuda.synchronize()
+assert moeq.moeq_device_status() == 0
+for a, b in zip(outs, step()):
+    assert torch.equal(a, b)
+"""
+
+
+def test_first_calls_inside_a_capture():
+    """A process that has made no call before captures its first ones."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = FIRST.format(path=[os.path.dirname(here), here])
+    subprocess.run([sys.executable, "-c", code], check=True, timeout=300)
