@@ -12,9 +12,10 @@
 // mma.sync, not tcgen05: up to 16 tokens the products are a small part of the
 // time, and fragments from registers need no shared-memory tiles, no token
 // layout and no TMEM.  Bound by latency: two rounds of loads and products per
-// warp.  One token 4096 x 4096, 4-bit: 7.0 us (1.3 TB/s; a launch is about 2 of
-// it); 8 tokens in int8, 1024 rows: 5.7 us; 64 tokens, 512 rows of 8 bits: 7.1.
+// warp.  One token 4096 x 4096, 4-bit: 6.5 us (1.5 TB/s; a launch is about 1.5
+// of it); 8 tokens in int8, 1024 rows: 5.1 us; 64 tokens, 512 rows of 8 bits: 6.2.
 #include "lincommon.cuh"
+#include "tc.cuh"
 
 namespace moeq {
 namespace {
@@ -190,14 +191,17 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) k_linear_small(const _
     xrow[n] = reinterpret_cast<const char*>(l.a.x) + m * l.a.x_stride * (bf16 ? 2 : 1);
   }
 
-  // The run's codes and scales into L2 while the first loads are on their way,
-  // and what the epilogue needs: nothing later waits for DRAM.
-  if (sp1 > sp0 + U) {
+  // The run's codes go to L2 while the preceding kernel ends; what the epilogue
+  // needs is asked for first: nothing later waits for DRAM.
+  if (sp1 > sp0) {
     const char* p = reinterpret_cast<const char*>(wrow[t >> 1] + (int64_t)sp0 * (C * BITS / 8));
     const char* e = p + (int64_t)(sp1 - sp0) * (C * BITS / 2);
     for (const char* c = p + 128 * (t & 1); c < e; c += 256)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(c));
   }
+  tc::grid_dep_wait();
+  // (few CTAs: the next kernel's fit beside them; 5.3 -> 5.1 us for eight tokens)
+  tc::grid_dep_launch();
   const int erow = threadIdx.x & 15, etok = threadIdx.x >> 4;
   const int64_t em = m0 + etok;
   const bool mine = threadIdx.x < 16 * TOKS && em < l.M && o0 + erow < l.out_dim;
@@ -302,12 +306,12 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) k_linear_small(const _
 }
 
 template <int BITS, bool MX, int C, int WARPS>
-void run_warps(const LinArgs& l, int blocks, cudaStream_t st) {
+cudaError_t run_warps(const LinArgs& l, int blocks, cudaStream_t st) {
   if (l.M <= 8)
-    k_linear_small<BITS, MX, C, 1, 4, WARPS><<<blocks, WARPS * 32, 0, st>>>(l);
-  else
-    k_linear_small<BITS, MX, C, 2, 2, WARPS>
-        <<<dim3(blocks, (l.M + 15) / 16), WARPS * 32, 0, st>>>(l);
+    return launch_after(k_linear_small<BITS, MX, C, 1, 4, WARPS>, dim3(blocks), WARPS * 32, 0, st,
+                        l);
+  return launch_after(k_linear_small<BITS, MX, C, 2, 2, WARPS>, dim3(blocks, (l.M + 15) / 16),
+                      WARPS * 32, 0, st, l);
 }
 
 // Sixteen warps a CTA (fewer spans for each) while one CTA per SM is all there
@@ -316,9 +320,8 @@ template <int BITS, bool MX, int C>
 cudaError_t run(const LinArgs& l, cudaStream_t st) {
   const int blocks = (l.out_dim + 15) / 16;
   const int64_t ctas = (int64_t)blocks * (l.M <= 8 ? 1 : (l.M + 15) / 16);
-  if (ctas <= sm_count() && l.in_dim / (4 * C) > 32) run_warps<BITS, MX, C, 16>(l, blocks, st);
-  else run_warps<BITS, MX, C, 8>(l, blocks, st);
-  return cudaGetLastError();
+  return ctas <= sm_count() && l.in_dim / (4 * C) > 32 ? run_warps<BITS, MX, C, 16>(l, blocks, st)
+                                                       : run_warps<BITS, MX, C, 8>(l, blocks, st);
 }
 
 // Spans of 64 columns lie in one group of 64 or 128, of 32 in one of 32.

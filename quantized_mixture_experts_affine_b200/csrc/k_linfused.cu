@@ -16,11 +16,11 @@
 // tokens' layout kernel still runs.
 //
 // What bounds it: under about 128 tokens the time around the loop (64 tokens,
-// 4096 x 4096, 4-bit, bf16 y, 12.4 us, of which the layout's launch 2.5, the
+// 4096 x 4096, 4-bit, bf16 y, 12.0 us, of which the layout's launch 2.5, the
 // prologue 2, unpacking 4), above that the products (256 tokens 20.8 us, 480
 // tokens 28.5 us, 0.57 PFLOP/s: the tile's operands and the unpacked weights
 // together need 1.5 times an SM's shared-memory bandwidth, and one wave has no
-// other tile to hide its ends behind).  fp32 y: 64 tokens 17.0 us, 256 tokens
+// other tile to hide its ends behind).  fp32 y: 64 tokens 16.6 us, 256 tokens
 // 26.7 us.  A thread takes 64 neighbouring codes, so its loads
 // are wide and one or two scales serve them: with 16 codes and a scale from
 // memory per block the loop was bound by the cache lines its loads touched

@@ -314,6 +314,8 @@ __device__ __forceinline__ void prep_tokens(const PrepArgs& p, int64_t m) {
 
 // Tokens: bf16 a row per warp, 8 bits a row per CTA.
 __global__ void __launch_bounds__(256) k_lin_rows(const __grid_constant__ PrepArgs p) {
+  // (in this order: the weights' kernel writes what the last call's product reads)
+  tc::grid_dep_wait();
   tc::grid_dep_launch();
   if (p.l.a.x_type == MOEQ_BF16) {
     const int64_t m = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -355,6 +357,8 @@ __device__ __forceinline__ float row_lift(const LinArgs& l, int64_t o) {
 // Tokens as above, but of the weights the powers and scales only: eight rows
 // per CTA, transposed through shared memory.
 __global__ void __launch_bounds__(256) k_lin_tokens(const __grid_constant__ PrepArgs p) {
+  // (in this order: the product reads weights before it waits)
+  tc::grid_dep_wait();
   tc::grid_dep_launch();
   if ((int)blockIdx.x < p.x_blocks) {
     prep_tokens(p, blockIdx.x);
@@ -379,22 +383,6 @@ __global__ void __launch_bounds__(256) k_lin_tokens(const __grid_constant__ Prep
       p.sb[(int64_t)(g0 + g8) * l.out_dim + o0 + r8] = tile[g8][r8];
     __syncthreads();
   }
-}
-
-template <typename... A>
-cudaError_t launch_after(void (*kernel)(A...), unsigned blocks, unsigned threads, size_t smem,
-                         cudaStream_t st, const A&... args) {
-  cudaLaunchConfig_t c = {};
-  c.gridDim = dim3(blocks);
-  c.blockDim = dim3(threads);
-  c.dynamicSmemBytes = smem;
-  c.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  c.attrs = at;
-  c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, kernel, args...);
 }
 
 template <bool TWO>
@@ -745,8 +733,8 @@ cudaError_t launch_linear_gemm(const LinArgs& l, void* ws, int* status, int* lau
     p.x_runs = 1;
     p.x_split = l.bits == 2 || l.bits == 4;
     *launches = 2;
-    k_lin_tokens<<<p.x_blocks + (l.out_dim + 7) / 8, 256, 0, st>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_after(
+        k_lin_tokens, (unsigned)(p.x_blocks + (l.out_dim + 7) / 8), 256, 0, st, p);
     return e != cudaSuccess ? e : launch_linear_fused(l, p.x16, p.fx, p.fw, p.sb, status, st);
   }
   GemmArgs g;
@@ -763,8 +751,8 @@ cudaError_t launch_linear_gemm(const LinArgs& l, void* ws, int* status, int* lau
   g.tiles_o = (l.out_dim + 2 * kTile - 1) / (2 * kTile);
   g.tiles_m = (l.M + bn - 1) / bn;
   g.status = status;
-  k_lin_rows<<<l.a.x_type == MOEQ_BF16 ? (l.M + 7) / 8 : l.M, 256, 0, st>>>(p);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_after(
+      k_lin_rows, (unsigned)(l.a.x_type == MOEQ_BF16 ? (l.M + 7) / 8 : l.M), 256, 0, st, p);
   if (e == cudaSuccess) e = p.w_parts == 2 ? run_weights<true>(p, st) : run_weights<false>(p, st);
   if (e != cudaSuccess) return e;
   return l.a.out_type == MOEQ_F32 ? run_gemm<true>(g, sms, st) : run_gemm<false>(g, sms, st);

@@ -3,9 +3,9 @@
 //
 // A CTA holds a row in registers (8-element vectors, 16-byte accesses), so
 // x and the residual are read once and each output is written once.  Few rows
-// are bound by the trip to memory and the block reduction (1 x 4096: 3.5 us),
+// are bound by the trip to memory and the block reduction (1 x 4096: 3.3 us),
 // many by HBM (16,068 x 4096, fp32 streams, e4m3 by 128: 129 us, the copy
-// rate) or, on bf16 streams, nearly so (97 us, 4.8 TB/s, 73 % of it; the rest
+// rate) or, on bf16 streams, nearly so (96 us, 4.8 TB/s, 74 % of it; the rest
 // is instruction issue: the codes are taken twice).
 //
 // The codes do not depend on the norm's factor: with t = r gamma and
@@ -17,6 +17,7 @@
 
 #include "common.cuh"
 #include "ops.h"
+#include "tc.cuh"
 
 namespace moeq {
 namespace {
@@ -218,6 +219,7 @@ constexpr int kAny = -1, kNone = -2;
 // FULL: every thread has NV whole vectors.
 template <int NV, int XT, int RT, bool FULL, int MAXT>
 __global__ void __launch_bounds__(MAXT) k_add_rmsnorm(const __grid_constant__ NormArgs a) {
+  tc::grid_dep_wait();
   constexpr bool ANY = XT == kAny;
   __shared__ float red[32], red_max[32];
   __shared__ unsigned long long red_key[32];
@@ -377,21 +379,20 @@ __global__ void __launch_bounds__(MAXT) k_add_rmsnorm(const __grid_constant__ No
 }
 
 template <int NV, int XT, int RT, int MAXT>
-void run_sized(const NormArgs& a, int M, int warps, cudaStream_t st) {
+cudaError_t run_sized(const NormArgs& a, int M, int warps, cudaStream_t st) {
   if (XT != kAny && a.vecs == warps * 32 * NV)
-    k_add_rmsnorm<NV, XT, RT, XT != kAny, MAXT><<<M, warps * 32, 0, st>>>(a);
-  else
-    k_add_rmsnorm<NV, XT, RT, false, MAXT><<<M, warps * 32, 0, st>>>(a);
+    return launch_after(k_add_rmsnorm<NV, XT, RT, XT != kAny, MAXT>, dim3(M), warps * 32, 0, st, a);
+  return launch_after(k_add_rmsnorm<NV, XT, RT, false, MAXT>, dim3(M), warps * 32, 0, st, a);
 }
 
 template <int XT, int RT>
-void run(const NormArgs& a, int M, int sms, cudaStream_t st) {
+cudaError_t run(const NormArgs& a, int M, int sms, cudaStream_t st) {
   const int warps = (a.vecs + 31) / 32;
   // Many rows: two vectors a thread, so that the reductions and addresses are
   // paid less often; few rows: as many threads as vectors, for the latency.
-  if (warps <= 16 && M < 4 * sms) run_sized<1, XT, RT, 512>(a, M, warps, st);
-  else if (warps <= 32) run_sized<2, XT, RT, 512>(a, M, (warps + 1) / 2, st);
-  else run_sized<4, XT, RT, 1024>(a, M, (warps + 3) / 4, st);
+  if (warps <= 16 && M < 4 * sms) return run_sized<1, XT, RT, 512>(a, M, warps, st);
+  if (warps <= 32) return run_sized<2, XT, RT, 512>(a, M, (warps + 1) / 2, st);
+  return run_sized<4, XT, RT, 1024>(a, M, (warps + 3) / 4, st);
 }
 
 bool wide(const void* p, int64_t stride, int item, int bytes) {
@@ -417,14 +418,13 @@ cudaError_t launch_add_rmsnorm(const moeq_norm_args& n, int M, int H, cudaStream
   const bool vec = H % 8 == 0 && a.vx && a.vg && (!n.residual || a.vr) && (!n.r_out || a.vro) &&
                    (!n.y || a.vy) && (!n.q || a.vq);
   const bool xb = n.x_type == MOEQ_BF16, rb = n.r_type == MOEQ_BF16;
-  if (!vec) run<kAny, kAny>(a, M, sms, st);
-  else if (!n.residual && xb) run<MOEQ_BF16, kNone>(a, M, sms, st);
-  else if (!n.residual) run<MOEQ_F32, kNone>(a, M, sms, st);
-  else if (xb && rb) run<MOEQ_BF16, MOEQ_BF16>(a, M, sms, st);
-  else if (xb) run<MOEQ_BF16, MOEQ_F32>(a, M, sms, st);
-  else if (rb) run<MOEQ_F32, MOEQ_BF16>(a, M, sms, st);
-  else run<MOEQ_F32, MOEQ_F32>(a, M, sms, st);
-  return cudaGetLastError();
+  if (!vec) return run<kAny, kAny>(a, M, sms, st);
+  if (!n.residual && xb) return run<MOEQ_BF16, kNone>(a, M, sms, st);
+  if (!n.residual) return run<MOEQ_F32, kNone>(a, M, sms, st);
+  if (xb && rb) return run<MOEQ_BF16, MOEQ_BF16>(a, M, sms, st);
+  if (xb) return run<MOEQ_BF16, MOEQ_F32>(a, M, sms, st);
+  if (rb) return run<MOEQ_F32, MOEQ_BF16>(a, M, sms, st);
+  return run<MOEQ_F32, MOEQ_F32>(a, M, sms, st);
 }
 
 }  // namespace moeq

@@ -10,14 +10,15 @@
 //
 // A row of up to 512 experts is held in registers by a warp, or with many rows
 // by 8 or 16 lanes; any other shape (k_route_any) lives in shared memory.  Few
-// rows are bound by the chain of load, exponential and K picks (4 us for one
-// row, 6 us for 2048 rows of 256 experts in 8 groups), many by instruction
-// issue (16,068 rows of 128 in 8 groups, top-8: 11.4 us; 15.4 us with picks
+// rows are bound by the chain of load, exponential and K picks (3.8 us for one
+// row, 5.8 us for 2048 rows of 256 experts in 8 groups), many by instruction
+// issue (16,068 rows of 128 in 8 groups, top-8: 11.2 us; 15.4 us with picks
 // that scanned 16 registers instead of a quad in shared memory, 24.3 us with a
 // warp per row).
 #include "common.cuh"
 #include "ops.h"
 #include "route.cuh"
+#include "tc.cuh"
 
 namespace moeq {
 namespace {
@@ -731,6 +732,9 @@ __device__ __noinline__ void route_again(const RouteArgs& a, int m, uint64_t* mi
 
 template <int L, int NQ, bool GROUPS, bool BIAS>
 __global__ void __launch_bounds__(256) k_route_regs(const __grid_constant__ RouteArgs a) {
+  // (the next kernel's CTAs are not let in early: routing 16,068 rows again they
+  // filled the SMs unevenly, 11.2 -> 13.1 us)
+  tc::grid_dep_wait();
   constexpr int ROWS = 32 / L;
   const int lane = threadIdx.x & 31;
   const int64_t m0 = ((int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * ROWS;
@@ -753,6 +757,7 @@ __global__ void __launch_bounds__(256) k_route_regs(const __grid_constant__ Rout
 
 // Any number of experts and groups of any size.
 __global__ void __launch_bounds__(256) k_route_any(const __grid_constant__ RouteArgs a) {
+  tc::grid_dep_wait();
   const int64_t row = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (row >= a.M) return;
   const int m = (int)row;
@@ -762,14 +767,14 @@ __global__ void __launch_bounds__(256) k_route_any(const __grid_constant__ Route
 }
 
 template <int L, int NQ>
-void run_regs(const RouteArgs& a, bool groups, int blocks, int threads, size_t smem,
+cudaError_t run_regs(const RouteArgs& a, bool groups, int blocks, int threads, size_t smem,
               cudaStream_t st) {
   if (groups) {
-    if (a.bias) k_route_regs<L, NQ, true, true><<<blocks, threads, smem, st>>>(a);
-    else k_route_regs<L, NQ, true, false><<<blocks, threads, smem, st>>>(a);
+    if (a.bias) return launch_after(k_route_regs<L, NQ, true, true>, dim3(blocks), threads, smem, st, a);
+    return launch_after(k_route_regs<L, NQ, true, false>, dim3(blocks), threads, smem, st, a);
   } else {
-    if (a.bias) k_route_regs<L, NQ, false, true><<<blocks, threads, smem, st>>>(a);
-    else k_route_regs<L, NQ, false, false><<<blocks, threads, smem, st>>>(a);
+    if (a.bias) return launch_after(k_route_regs<L, NQ, false, true>, dim3(blocks), threads, smem, st, a);
+    return launch_after(k_route_regs<L, NQ, false, false>, dim3(blocks), threads, smem, st, a);
   }
 }
 
@@ -813,13 +818,12 @@ cudaError_t launch_route_groups(const moeq_routing& r, const void* logits, int l
   while (warps > 1 && warps * slot > 48 * 1024) --warps;
   const int blocks = (int)((rows + warps - 1) / warps), threads = warps * 32;
   const size_t smem = warps * slot;
-  if (!regs) k_route_any<<<blocks, threads, smem, st>>>(a);
-  else if (lanes == 8) run_regs<8, 4>(a, groups, blocks, threads, smem, st);
-  else if (lanes == 16) run_regs<16, 4>(a, groups, blocks, threads, smem, st);
-  else if (nq <= 32) run_regs<32, 1>(a, groups, blocks, threads, smem, st);
-  else if (nq <= 64) run_regs<32, 2>(a, groups, blocks, threads, smem, st);
-  else run_regs<32, 4>(a, groups, blocks, threads, smem, st);
-  return cudaGetLastError();
+  if (!regs) return launch_after(k_route_any, dim3(blocks), threads, smem, st, a);
+  if (lanes == 8) return run_regs<8, 4>(a, groups, blocks, threads, smem, st);
+  if (lanes == 16) return run_regs<16, 4>(a, groups, blocks, threads, smem, st);
+  if (nq <= 32) return run_regs<32, 1>(a, groups, blocks, threads, smem, st);
+  if (nq <= 64) return run_regs<32, 2>(a, groups, blocks, threads, smem, st);
+  return run_regs<32, 4>(a, groups, blocks, threads, smem, st);
 }
 
 }  // namespace moeq

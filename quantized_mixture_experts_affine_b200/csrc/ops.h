@@ -10,6 +10,28 @@
 
 namespace moeq {
 
+// Launches a kernel as the successor of whatever precedes it in the stream: its
+// CTAs may be set up as soon as that one's have ended or let it (tc::grid_dep_launch),
+// so every one of them waits (tc::grid_dep_wait) before it touches what the
+// other may still write or read.  One call after the other, without a graph:
+// 1 x 4096 x 4096 linear 8.6 -> 6.6 us, 64 x 4096 x 4096 14.3 -> 12.2, 16,068 x
+// 128 routing 13.0 -> 11.2, 333 x 1000 norm 3.45 -> 3.0 (in a graph).
+template <typename... A>
+cudaError_t launch_after(void (*kernel)(A...), dim3 blocks, unsigned threads, size_t smem,
+                         cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = blocks;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, args...);
+}
+
 cudaError_t launch_route_groups(const moeq_routing& r, const void* logits, int logit_type,
                                 int64_t stride, const float* bias, int M, int32_t* idx, float* w,
                                 cudaStream_t st);

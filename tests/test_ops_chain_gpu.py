@@ -127,6 +127,56 @@ def test_the_chain_in_a_graph():
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("M", [1, 40, 700, 2600])
+def test_calls_one_after_the_other(M):
+    """Calls that feed one another, through one workspace and in place, give
+    what they give with the device idle in between."""
+    H, E, O = 1024, 64, 1920
+    g = torch.Generator(device="cuda").manual_seed(M)
+    packed = []
+
+    def qt(o, n):
+        packed.append(ref.matrix(o, n, 4, 64, g))
+        w = packed[-1]
+        return moeq.qtensor(w["w"], w["s"], w["b"], o, n, 4, 64)
+    tu, td, tg = qt(O, H), qt(H, O), qt(E, H)
+    gamma = torch.ones(H, device="cuda", dtype=torch.bfloat16)
+    bias = 0.05 * torch.randn(E, device="cuda", generator=g)
+    R = moeq.routing(E, 6, moeq.SCORE_SIGMOID, 8, 4, 2)
+    x0 = torch.randn(M, H, device="cuda", generator=g)
+    need = max(moeq.moeq_linear_workspace_bytes(t, M, torch.int8, torch.float32)
+               for t in (tu, td, tg))
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+
+    def steps(wait):
+        kept = []
+        stream, x = x0.clone(), 0.25 * x0
+        y = torch.empty(M, H, device="cuda", dtype=torch.bfloat16)
+        q = torch.empty(M, H, device="cuda", dtype=torch.int8)
+        s = torch.empty(M, 1, device="cuda")
+        h = torch.empty(M, O, device="cuda", dtype=torch.bfloat16)
+        l = torch.empty(M, E, device="cuda")
+        idx = torch.empty(M, 6, device="cuda", dtype=torch.int32)
+        w = torch.empty(M, 6, device="cuda")
+        for i in range(12):
+            for call in (
+                    lambda: moeq.moeq_add_rmsnorm(x, gamma, 1e-6, stream, stream, y, q, s),
+                    lambda: moeq.moeq_linear(tu, 0, q, h, x_scales=s, act=moeq.ACT_SILU, ws=ws),
+                    lambda: moeq.moeq_linear(td, 0, h, x, ws=ws),
+                    lambda: moeq.moeq_linear(tg, 0, y, l, ws=ws),
+                    lambda: moeq.moeq_route_groups(R, l, idx, w, bias)):
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+            if i % 4 == 3:
+                kept += [idx.clone(), w.clone()]
+        return kept + [stream, x, h, l]
+    want = steps(True)
+    for _ in range(3):
+        for a, b in zip(steps(False), want):
+            assert torch.equal(a, b)
+
+
 FIRST = """
 import sys
 sys.path[:0] = {path!r}
