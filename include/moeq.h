@@ -457,6 +457,7 @@ typedef struct {
  * An x row that holds an infinity or NaN gives a row of unspecified values
  * and leaves the others untouched.
  *   y may be mul's or residual's memory (same stride); it may not overlap x.
+ *   Their strides are at most 2^28 (else UNSUPPORTED).
  *   ws: device workspace of moeq_linear_workspace_bytes(t, M, x_type,
  *   out_type) bytes, 256-byte aligned, contents ignored on entry; NULL where
  *   that is 0 (few tokens).  Calls that may overlap in time need their own.

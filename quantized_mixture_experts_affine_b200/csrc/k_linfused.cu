@@ -544,12 +544,15 @@ bool own_sums(int n, bool two) { return kRoom >= (uint32_t)n * kRows * 4 + 4 * b
 // sums 2500 and 22 a token, 4000 more where it has to wait for the stages' place,
 // an epilogue without it 12 a token, the rest 8500.  So 256 tokens are two tiles
 // of 128 where the GPU has room (4096 x 2048: 20.2 -> 14.7 us; 2048 x 1024:
-// 15.2 -> 9.5).
+// 15.2 -> 9.5).  That fit is of up to 1024 tokens; the plan's clocks, which
+// unpack_inside compares, are one of 320 to 8000 tokens, 128 to 4096 columns and
+// 64 to 6000 rows (5 % off in the mean).
 LinPlan linear_fused_plan(int64_t M, int64_t in_dim, int64_t out_dim, int out_type) {
   const int64_t tiles_o = (out_dim + kRows - 1) / kRows, runs = (in_dim + 255) / 256;
   const bool two = out_type == MOEQ_F32;
   const int fit[4] = {148, 74, 32, 14};
   LinPlan best = {0, 0, 0, 0.0};
+  double least = 0.0;
   const int64_t first = (M + 255) / 256;
   for (int64_t tiles_m = first; tiles_m <= first + 3; ++tiles_m) {
     const int64_t n = ((M + tiles_m - 1) / tiles_m + 15) / 16 * 16;
@@ -564,7 +567,17 @@ LinPlan linear_fused_plan(int64_t M, int64_t in_dim, int64_t out_dim, int out_ty
     const double end = l ? 2500 + 22.0 * n + (own_sums((int)n, two) ? 0 : 4000) : 12.0 * n;
     const double clocks =
         8500 + waves * (4.0 * ((runs + (1 << l) - 1) >> l) * block + end);
-    if (best.tokens == 0 || clocks < best.clocks) best = {(int)n, l, (int)((M + n - 1) / n), clocks};
+    if (best.tokens == 0 || clocks < least) {
+      least = clocks;
+      const double blocks = waves * (4 * ((runs + (1 << l) - 1) >> l));
+      const double nw = n * waves, nb = blocks * (n > 80 ? n : 80), laid = 1e-6 * (double)(M * in_dim);
+      double c;
+      if (two) c = 5200 + 1000 * laid + 1125 * blocks + nb + (l ? 76 * nw + 2300 * waves : 87 * nw);
+      else if (l) c = 6000 + 1077 * laid + 570 * blocks + 0.83 * nb + 52 * nw + 2250 * waves;
+      else c = 6000 + 1077 * laid + 570 * blocks + 0.83 * nb + 77 * nw;
+      if (!two && l && !own_sums((int)n, two)) c += 2500 * waves;
+      best = {(int)n, l, (int)((M + n - 1) / n), c};
+    }
     if (n <= 64) break;
   }
   return best;

@@ -25,7 +25,7 @@
 // Measured, 16,068 tokens, 4096 x 4096, 8-bit, bf16 y, residual: layout 36 us
 // beside 16 us (16,068 x 4096 tokens are 263 MB), GEMM 342 to 366 us (1.5
 // PFLOP/s), the call 416 us; under the power cap of a long loop 484 us.
-// 2048 tokens, 2048 x 4096, MX FP4: 38 us, of which the GEMM 25 (144 tiles
+// 2048 tokens, 2048 x 4096, MX FP4: 37 us, of which the GEMM 24 (144 tiles
 // of 240 tokens: two waves of 74 pairs, nearly full).
 #include "lingemm.cuh"
 
@@ -211,6 +211,7 @@ __device__ __forceinline__ void prep_bf16_row(const PrepArgs& p, int64_t m) {
   };
 #pragma unroll
   for (int i = 0; i < RV; ++i) {
+    if (256 * i >= K) break;
     take(v[i].x);
     take(v[i].y);
     take(v[i].z);
@@ -235,8 +236,10 @@ __device__ __forceinline__ void prep_bf16_row(const PrepArgs& p, int64_t m) {
     *reinterpret_cast<uint4*>(out + c) = p.x_split ? split_order(h) : h;
   };
 #pragma unroll
-  for (int i = 0; i < RV; ++i)
+  for (int i = 0; i < RV; ++i) {
+    if (256 * i >= p.x_row) break;
     if (8 * lane + 256 * i < p.x_row) put(256 * i, v[i]);
+  }
   for (int c = 256 * RV; c + 8 * lane < p.x_row; c += 256)
     put(c, c + 8 * lane < K ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0u, 0u, 0u, 0u));
 }
@@ -289,8 +292,10 @@ __device__ __forceinline__ void prep_8bit_row(const PrepArgs& p, int64_t m) {
       largest = fmaxf(largest, top * fabsf(scale(c)));
     };
 #pragma unroll
-    for (int i = 0; i < RV; ++i)
-      if (256 * i < K) take(256 * i, v[i]);
+    for (int i = 0; i < RV; ++i) {
+      if (256 * i >= K) break;
+      take(256 * i, v[i]);
+    }
     for (int c = 256 * RV; c < K; c += 256) take(c, read(c));
     const int k = lift_of(warp_max(largest));
     f = pow2(k);
@@ -314,8 +319,10 @@ __device__ __forceinline__ void prep_8bit_row(const PrepArgs& p, int64_t m) {
     }
   };
 #pragma unroll
-  for (int i = 0; i < RV; ++i)
+  for (int i = 0; i < RV; ++i) {
+    if (256 * i >= p.x_row) break;
     if (8 * lane + 256 * i < p.x_row) put(256 * i, v[i]);
+  }
   for (int c = 256 * RV; c + 8 * lane < p.x_row; c += 256) put(c, read(c));
 }
 
@@ -531,7 +538,7 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* tmap,
 // the parts are added in registers, rounded to nearest: the two accumulators
 // then take turns within a tile too.
 constexpr int kChunk = 8;
-constexpr int gemm_threads(bool sums) { return sums ? 640 : 384; }
+constexpr int gemm_threads(bool sums) { return 640; }
 
 template <bool SUMS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(SUMS), 1)
@@ -552,7 +559,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(SUMS), 
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&tmem_full[i], 1);
-      tc::mbar_init(&tmem_empty[i], SUMS ? 32 : 16);  // the epilogue warps of both CTAs
+      tc::mbar_init(&tmem_empty[i], 32);  // the epilogue warps of both CTAs
     }
     tc::fence_mbar_init();
   }
@@ -629,8 +636,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(SUMS), 
       const int oc = min(o, a.l.out_dim - 1);
       const float fw = a.fw[oc];
       const float bias = a.l.a.bias ? bf16_bits_to_float(a.l.a.bias[oc]) : 0.0f;
-      const int C = SUMS ? kMaxTokens / 4 : BN / 2;  // columns of this warp
-      const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + half * C;
+      // this warp's tokens: sixteen of every 64, from 16 `half` on
+      const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16) + half * 16;
+      // what the tile reads of mul goes to L2 under its products (2048 x 256 x 4096,
+      // MX FP4, both: 37.5 -> 34.6 us; the residual is read a chunk ahead)
+      if (a.l.a.mul) {
+        constexpr int SIZE = SUMS ? 4 : 2;  // bytes; 32 columns are as many sectors
+        const int col0 = item % a.tiles_o * (2 * kTile) + (int)rank * kTile + q * 32;
+        for (int i = lane; i < kMaxTokens / 4; i += 32) {
+          const int c = 16 * half + (i >> 4) * 64 + (i & 15);
+          if (c >= BN || m0 + c >= a.l.M) break;
+#pragma unroll
+          for (int j = 0; j < SIZE; ++j)
+            if (col0 + j * (32 / SIZE) < a.l.out_dim)
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                  reinterpret_cast<const char*>(a.l.a.mul) +
+                  ((int64_t)(m0 + c) * a.l.a.mul_stride + col0 + j * (32 / SIZE)) * SIZE));
+        }
+      }
       if (SUMS) {
         constexpr int CS = kMaxTokens / 4;
         uint32_t sum[CS];
@@ -643,7 +666,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(SUMS), 
 #pragma unroll
           for (int c0 = 0; c0 < CS; c0 += 16) {
             uint32_t v[16];
-            tmem_ld16(lanes + acc * kMaxTokens + c0, v);
+            tmem_ld16(lanes + acc * kMaxTokens + 4 * c0, v);
             tc::tmem_wait_ld();
 #pragma unroll
             for (int j = 0; j < 16; ++j)
@@ -656,7 +679,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(SUMS), 
         }
 #pragma unroll
         for (int c0 = 0; c0 < CS; c0 += 8) {
-          const int m = m0 + half * C + c0, nm = min(min(8, BN - half * C - c0), a.l.M - m);
+          const int c = 16 * half + (c0 >> 4) * 64 + (c0 & 8), m = m0 + c;
+          const int nm = min(min(8, BN - c), a.l.M - m);
           if (nm <= 0) break;
           uint32_t v[8];
 #pragma unroll
@@ -666,24 +690,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(SUMS), 
         }
       } else {
         const uint32_t acc = tile & 1u;
-        auto power = [&](int c0) {  // of the chunk's tokens, asked for one chunk ahead
-          const int i = half * C + c0 + lane;
-          return c0 + lane < C && m0 + i < a.l.M ? a.fx[m0 + i] : 0.0f;
+        // What a chunk of sixteen reads from memory is asked for one chunk ahead,
+        // the first before the sums are there.
+        uint16_t res[16] = {};
+        float fx = 0.0f;
+        auto ahead = [&](int c) {
+          const int m = m0 + c, nm = min(min(16, BN - c), a.l.M - m);
+          if (nm <= 0) return;
+          if (a.l.a.residual) {
+            if (nm == 16) column<true>(a.l.a.residual, a.l.a.residual_stride, m, nm, oc, res);
+            else column(a.l.a.residual, a.l.a.residual_stride, m, nm, oc, res);
+          }
+          fx = lane < nm ? a.fx[m + lane] : 0.0f;
         };
-        float next = power(0);
+        ahead(16 * half);
         if (!wait_bar(&tmem_full[acc], (tile >> 1) & 1u, a.status)) goto done;
         tc::tc_fence_after();
         ++tile;
 #pragma unroll 1
-        for (int c0 = 0; c0 < C; c0 += 32) {
-          const int m = m0 + half * C + c0, nm = min(min(32, C - c0), a.l.M - m);
+        for (int c = 16 * half; c < BN; c += 64) {
+          const int m = m0 + c, nm = min(16, a.l.M - m);
           if (nm <= 0) break;
-          uint32_t v[32];
-          tc::tmem_ld32(lanes + acc * kMaxTokens + c0, v);
-          const float fx = next;
-          next = power(c0 + 32);
+          uint32_t v[16];
+          tmem_ld16(lanes + acc * kMaxTokens + c - 16 * half, v);
+          uint16_t now[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) now[j] = res[j];
+          const float fx_now = fx;
+          ahead(c + 64);
           tc::tmem_wait_ld();
-          finish<uint16_t, 32>(a.l.a, m, nm, oc, live, fw, bias, fx, v);
+          if (nm == 16)
+            finish_with<uint16_t, 16, true>(a.l.a, m, nm, oc, live, fw, bias, fx_now, v, now);
+          else
+            finish_with<uint16_t, 16>(a.l.a, m, nm, oc, live, fw, bias, fx_now, v, now);
         }
         tc::tc_fence_before();
         __syncwarp();
@@ -721,24 +760,26 @@ int tile_tokens(int64_t M, int64_t out_dim, int pairs) {
 
 // Whether the weights are unpacked inside the product (k_linfused.cu): for up to
 // 256 tokens always (there it needs a small workspace only), beyond while its
-// clocks are fewer than this way's.  These are a fit too: 8000 around it, 900 per
-// million weights and token values laid out (twice the weights for an fp32 y;
-// 1900 beyond 20 million, which L2 does not keep), and the waves' blocks.
-// Inside against laid out first, 4096 x 4096, 4-bit: bf16 y, 256 tokens 20.8 and
-// 26.5 us, 320 tokens 22.1 and 27.2, 480 tokens 28.5 and 28.6, 768 tokens 43.1
-// and 35.6; fp32 y, 256 tokens 26.7 and 50.3, 400 tokens 45.5 and 52.0, 640
-// tokens 69.7 and 55.9.
+// clocks are fewer than this way's.  These are a fit too, to the same calls (6 %
+// off in the mean): the operands laid out, 1550 per million values; the waves'
+// blocks, the epilogue of their tokens, and the first tile's latency per block.
+// The choice so made is within 0.5 % of the better way in the mean, 10 % at worst.
+// Inside against laid out first, 4-bit, residual: 4096 x 4096, bf16 y, 320 tokens
+// 22.1 and 27.2 us, 480 tokens 28.5 and 28.6, 768 tokens 43.1 and 35.6; 512 x 2048,
+// 1200 tokens 12.8 and 11.0; fp32 y, 15.7 and 17.8, 3000 tokens 34.4 and 30.5.
 bool unpack_inside(int64_t M, int64_t in_dim, int64_t out_dim, int out_type) {
   const LinPlan plan = linear_fused_plan(M, in_dim, out_dim, out_type);
   if (plan.tokens == 0) return false;
   if (M <= 256) return true;
   const int64_t pairs = 74, n = tile_tokens(M, out_dim, (int)pairs);
   const int64_t tiles = (M + n - 1) / n * ((out_dim + 2 * kTile - 1) / (2 * kTile));
-  const int parts = out_type == MOEQ_F32 ? 2 : 1;
-  const double laid = 1e-6 * (double)(in_dim * (out_dim * parts + M));  // millions
-  const double clocks =
-      8000 + 900 * laid + (laid > 20 ? 1000 * (laid - 20) : 0) +
-      (double)((tiles + pairs - 1) / pairs * ((in_dim + kBK - 1) / kBK) * (256 + n) * parts);
+  const int64_t waves = (tiles + pairs - 1) / pairs, blocks = (in_dim + kBK - 1) / kBK;
+  const bool two = out_type == MOEQ_F32;
+  const int parts = two ? 2 : 1;
+  const double clocks = (two ? 8300 : 9000) +
+                        1550e-6 * (double)(in_dim * (out_dim * parts + M)) +
+                        (two ? 0.6 : 0.5) * (double)(waves * blocks * (256 + n) * parts) +
+                        (double)((two ? 99 : 49) * waves * n) + (double)((two ? 58 : 37) * blocks);
   return plan.clocks <= clocks;
 }
 

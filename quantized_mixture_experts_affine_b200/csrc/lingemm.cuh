@@ -95,12 +95,16 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
 // A warp's N tokens from m0 (nm of them real) of output column o: lane j's
 // fx is token j's power.  mul and the residual are read together, before the
 // stores that might overlap them, so that their latency is paid once.
-template <typename T, int N>
+// (Strides of at most 2^28 elements, kMaxStride: a row's address is one
+// instruction.)  FULL: nm is N.
+template <bool FULL = false, typename T, int N>
 __device__ __forceinline__ void column(const void* p, int64_t stride, int64_t m0, int nm, int o,
                                        T (&r)[N]) {
-  const T* c = reinterpret_cast<const T*>(p) + m0 * stride + o;
+  const char* c = reinterpret_cast<const char*>(reinterpret_cast<const T*>(p) + m0 * stride + o);
+  const int step = (int)stride * (int)sizeof(T);
 #pragma unroll
-  for (int j = 0; j < N; ++j) r[j] = j < nm ? c[j * stride] : (T)0;
+  for (int j = 0; j < N; ++j)
+    r[j] = FULL || j < nm ? *reinterpret_cast<const T*>(c + (int64_t)step * j) : (T)0;
 }
 __device__ __forceinline__ float as_float(float v) { return v; }
 __device__ __forceinline__ float as_float(uint16_t v) { return bf16_bits_to_float(v); }
@@ -112,7 +116,7 @@ __device__ __forceinline__ void as_out(float v, uint16_t* p) {
 // T: the type of y, mul and the residual (uint16_t: bf16 bits).  r: the
 // residual's values, read ahead (unused without one).  (The two powers first:
 // huge weights and tiny tokens make up for one another.)
-template <typename T, int N>
+template <typename T, int N, bool FULL = false>
 __device__ __forceinline__ void finish_with(const moeq_linear_args& a, int64_t m0, int nm, int o,
                                             bool live, float fw, float bias, float fx,
                                             const uint32_t (&acc)[N], const T (&r)[N]) {
@@ -123,7 +127,7 @@ __device__ __forceinline__ void finish_with(const moeq_linear_args& a, int64_t m
   act_all(y, a.act);
   if (a.mul) {
     T f[N];
-    column(a.mul, a.mul_stride, m0, nm, o, f);
+    column<FULL>(a.mul, a.mul_stride, m0, nm, o, f);
 #pragma unroll
     for (int j = 0; j < N; ++j) y[j] *= as_float(f[j]);
   }
@@ -131,20 +135,21 @@ __device__ __forceinline__ void finish_with(const moeq_linear_args& a, int64_t m
 #pragma unroll
     for (int j = 0; j < N; ++j) y[j] += as_float(r[j]);
   }
-  T* c = reinterpret_cast<T*>(a.y) + m0 * a.y_stride + o;
+  char* c = reinterpret_cast<char*>(reinterpret_cast<T*>(a.y) + m0 * a.y_stride + o);
+  const int step = (int)a.y_stride * (int)sizeof(T);
   if (live) {
 #pragma unroll
     for (int j = 0; j < N; ++j)
-      if (j < nm) as_out(y[j], c + j * a.y_stride);
+      if (FULL || j < nm) as_out(y[j], reinterpret_cast<T*>(c + (int64_t)step * j));
   }
 }
-template <typename T, int N>
+template <typename T, int N, bool FULL = false>
 __device__ __forceinline__ void finish(const moeq_linear_args& a, int64_t m0, int nm, int o,
                                        bool live, float fw, float bias, float fx,
                                        const uint32_t (&acc)[N]) {
   T r[N];
-  if (a.residual) column(a.residual, a.residual_stride, m0, nm, o, r);
-  finish_with<T, N>(a, m0, nm, o, live, fw, bias, fx, acc, r);
+  if (a.residual) column<FULL>(a.residual, a.residual_stride, m0, nm, o, r);
+  finish_with<T, N, FULL>(a, m0, nm, o, live, fw, bias, fx, acc, r);
 }
 
 // [parts][rows][cols] fp16, boxes of 64 columns x `box` rows, 128-byte swizzle;

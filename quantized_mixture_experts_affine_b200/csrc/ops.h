@@ -50,6 +50,9 @@ struct LinArgs {
   int scales_wide;  // (k_linear.cu) a row's scales can be loaded four spans at a time
 };
 
+// Largest row stride of y, mul and the residual (elements).
+constexpr int64_t kMaxStride = 1 << 28;
+
 cudaError_t launch_linear_small(const LinArgs& l, cudaStream_t st);
 
 // Many tokens: operand layout and product, over a workspace; *launches: how

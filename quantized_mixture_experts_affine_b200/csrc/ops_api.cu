@@ -164,6 +164,9 @@ MOEQ_API moeq_status moeq_linear(const moeq_qtensor* t, int32_t expert, const mo
   TRY(check_rows(a->y, a->out_type, a->y_stride, t->out_dim));
   if (a->mul) TRY(check_rows(a->mul, a->out_type, a->mul_stride, t->out_dim));
   if (a->residual) TRY(check_rows(a->residual, a->out_type, a->residual_stride, t->out_dim));
+  if (a->y_stride > kMaxStride || (a->mul && a->mul_stride > kMaxStride) ||
+      (a->residual && a->residual_stride > kMaxStride))
+    return MOEQ_ERR_UNSUPPORTED;
   const size_t need = moeq_linear_workspace_bytes(t, M, a->x_type, a->out_type);
   if (need > 0) {
     if (!ws || ws_bytes < need) return MOEQ_ERR_WORKSPACE;

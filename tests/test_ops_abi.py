@@ -105,6 +105,9 @@ def test_linear_refusals():
     assert rc_linear(x_type=moeq.E4M3, x_scales=A + 2) == moeq.ERR_ALIGNMENT
     assert rc_linear(out_type=moeq.I8) == moeq.ERR_UNSUPPORTED
     assert rc_linear(y_stride=127) == moeq.ERR_INVALID_ARG
+    assert rc_linear(y_stride=2 ** 28 + 1) == moeq.ERR_UNSUPPORTED
+    assert rc_linear(mul=A, mul_stride=2 ** 40) == moeq.ERR_UNSUPPORTED
+    assert rc_linear(residual=A, residual_stride=2 ** 28 + 8) == moeq.ERR_UNSUPPORTED
     assert rc_linear(y=A + 2) == moeq.ERR_ALIGNMENT
     assert rc_linear(bias=A + 1) == moeq.ERR_ALIGNMENT
     assert rc_linear(mul=A, mul_stride=1) == moeq.ERR_INVALID_ARG
