@@ -9,7 +9,9 @@
 // the whole row again.  Such rows are under 1 % of 512 normal logits.
 //
 // A row of up to 512 experts is held in registers by a warp, or with many rows
-// by 8 or 16 lanes; any other shape (k_route_any) lives in shared memory.  Few
+// by 8 or 16 lanes, groups padded to a power of two of quads (300 rows of 160 in
+// 8 groups: 8.5 us in shared memory, 4.3 so); what is larger (k_route_any) lives
+// in shared memory.  Few
 // rows are bound by the chain of load, exponential and K picks (3.8 us for one
 // row, 5.8 us for 2048 rows of 256 experts in 8 groups), many by instruction
 // issue (16,068 rows of 128 in 8 groups, top-8: 11.2 us; 15.4 us with picks
@@ -34,7 +36,9 @@ struct RouteArgs {
   int M;
   int lanes_per_group;  // power of two
   int slot;             // 8-byte words of shared memory per warp
-  int group_quads;      // registers path: quads per group, a power of two
+  // Registers path, with groups: quads laid out for one, a power of two, and
+  // its experts (which may leave the last quads empty or end inside one).
+  int group_quads, group_size;
 };
 
 // Order-preserving keys.  0: dropped or taken; 1: an expert that is out (its
@@ -327,7 +331,8 @@ __device__ bool route_row(const RouteArgs& a, int m, typename Keys<T>::K* keys, 
   return true;
 }
 
-// ---- registers: up to 512 experts, groups that are a power of two of quads
+// ---- registers: up to 512 experts, counting what groups are padded with (GROUPS
+// 2; 1: they are a power of two of whole quads)
 // L lanes hold a row (a warp holds 32 / L rows): lane l of them the quads
 // l + L j, experts 4 q .. 4 q + 3.  Same steps as route_row<float>; a group's
 // members are neighbouring lanes, so its two largest keys come from a
@@ -385,7 +390,7 @@ __device__ __forceinline__ uint32_t seg_ballot(bool p) {
 // write it).  slots: 96 words of the warp's shared memory, then 4 NQ words for
 // each lane.  Returns false
 // in every lane of a segment whose row is not settled (nothing is written).
-template <int L, int NQ, bool GROUPS, bool BIAS>
+template <int L, int NQ, int GROUPS, bool BIAS>
 __device__ __forceinline__ bool route_regs(const RouteArgs& a, int m, bool store,
                                            uint32_t* slots) {
   using KT = Keys<float>;
@@ -393,25 +398,42 @@ __device__ __forceinline__ bool route_regs(const RouteArgs& a, int m, bool store
   const int lane = threadIdx.x & (L - 1), E = r.n_experts;
   const int64_t row = (int64_t)m * a.stride;
   const bool softmax = r.score == MOEQ_SCORE_SOFTMAX;
+  // first expert of quad q, and how many it has
+  auto quad = [&](int q, int& n) -> int {
+    if (GROUPS == 2) {
+      const int lg = 31 - __clz(a.group_quads), g = q >> lg, i = q & (a.group_quads - 1);
+      n = g < r.n_groups ? a.group_size - 4 * i : 0;
+      return g * a.group_size + 4 * i;
+    }
+    n = E - 4 * q;
+    return 4 * q;
+  };
+  auto expert = [&](int place) -> int {  // of place 4 q + c
+    int n;
+    return GROUPS == 2 ? quad(place >> 2, n) + (place & 3) : place;
+  };
   float l[NQ][4], b[NQ][4];
   {
     const size_t item = a.bf16 ? 2 : 4;
     const uintptr_t base = (uintptr_t)a.logits + (size_t)row * item;
-    const bool vec = (base & (4 * item - 1)) == 0, bvec = ((uintptr_t)a.bias & 15) == 0;
+    const bool even = GROUPS != 2 || (a.group_size & 3) == 0;
+    const bool vec = even && (base & (4 * item - 1)) == 0,
+               bvec = even && ((uintptr_t)a.bias & 15) == 0;
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
-      const int q = lane + L * j;
+      int n;
+      const int e0 = quad(lane + L * j, n);
 #pragma unroll
       for (int c = 0; c < 4; ++c) l[j][c] = -INFINITY, b[j][c] = 0.0f;
-      if (vec && 4 * q + 4 <= E) {
+      if (vec && n >= 4) {
         if (a.bf16) {
-          const uint2 v = *reinterpret_cast<const uint2*>(base + (size_t)q * 8);
+          const uint2 v = *reinterpret_cast<const uint2*>(base + (size_t)e0 * 2);
           l[j][0] = __uint_as_float(v.x << 16);
           l[j][1] = __uint_as_float(v.x & 0xFFFF0000u);
           l[j][2] = __uint_as_float(v.y << 16);
           l[j][3] = __uint_as_float(v.y & 0xFFFF0000u);
         } else {
-          const float4 v = *reinterpret_cast<const float4*>(base + (size_t)q * 16);
+          const float4 v = *reinterpret_cast<const float4*>(base + (size_t)e0 * 4);
           l[j][0] = v.x;
           l[j][1] = v.y;
           l[j][2] = v.z;
@@ -420,11 +442,11 @@ __device__ __forceinline__ bool route_regs(const RouteArgs& a, int m, bool store
       } else {
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          if (4 * q + c < E) l[j][c] = logit_at(a, row, 4 * q + c);
+          if (c < n) l[j][c] = logit_at(a, row, e0 + c);
       }
       if (BIAS) {
-        if (bvec && 4 * q + 4 <= E) {
-          const float4 v = *reinterpret_cast<const float4*>(a.bias + 4 * q);
+        if (bvec && n >= 4) {
+          const float4 v = *reinterpret_cast<const float4*>(a.bias + e0);
           b[j][0] = v.x;
           b[j][1] = v.y;
           b[j][2] = v.z;
@@ -432,7 +454,7 @@ __device__ __forceinline__ bool route_regs(const RouteArgs& a, int m, bool store
         } else {
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            if (4 * q + c < E) b[j][c] = a.bias[4 * q + c];
+            if (c < n) b[j][c] = a.bias[e0 + c];
         }
       }
     }
@@ -463,13 +485,15 @@ __device__ __forceinline__ bool route_regs(const RouteArgs& a, int m, bool store
 
   uint32_t k[NQ][4];
 #pragma unroll
-  for (int j = 0; j < NQ; ++j)
+  for (int j = 0; j < NQ; ++j) {
+    int n;
+    quad(lane + L * j, n);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const int e = 4 * (lane + L * j) + c;
       const float v = BIAS ? fast_numerator(r, l[j][c], mx) * inv + b[j][c] : l[j][c];
-      k[j][c] = e >= E ? 0u : is_out(l[j][c]) ? 1u : BIAS ? KT::of(v) : key_of(v);
+      k[j][c] = c >= n ? 0u : is_out(l[j][c]) ? 1u : BIAS ? KT::of(v) : key_of(v);
     }
+  }
 
   bool sure = true;
   if (GROUPS) {
@@ -582,7 +606,7 @@ __device__ __forceinline__ bool route_regs(const RouteArgs& a, int m, bool store
     }
     if (lane == i) {
       my_k = top;
-      my_e = win == kNoExpert ? 0 : win;
+      my_e = win == kNoExpert ? 0 : expert(win);
     }
   }
   const bool mine = lane < r.top_k;
@@ -651,16 +675,18 @@ __device__ __forceinline__ bool route_regs(const RouteArgs& a, int m, bool store
           for (int j = 0; j < NQ; ++j)
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-              if (near & (1u << (4 * j + c))) put(at++, 4 * (lane + L * j) + c, l[j][c], b[j][c]);
+              if (near & (1u << (4 * j + c)))
+                put(at++, expert(4 * (lane + L * j) + c), l[j][c], b[j][c]);
           double z = 1.0;
           if (softmax) {
             z = 0.0;
 #pragma unroll 1
             for (int j = 0; j < NQ; ++j) {
               // (registers are not indexed: the row is read again)
+              int n;
+              const int e0 = quad(lane + L * j, n);
               for (int c = 0; c < 4; ++c) {
-                const int e = 4 * (lane + L * j) + c;
-                const float le = e < E ? logit_at(a, row, e) : -INFINITY;
+                const float le = c < n ? logit_at(a, row, e0 + c) : -INFINITY;
                 if (!is_out(le)) z += numerator<double>(r, le, mx);
               }
             }
@@ -724,13 +750,13 @@ __device__ __forceinline__ uint64_t* warp_slots(const RouteArgs& a, float*& raw)
 }
 
 // The rows a warp's segments could not settle, with all its lanes.
-template <int NQ, bool GROUPS, bool BIAS>
+template <int NQ, int GROUPS, bool BIAS>
 __device__ __noinline__ void route_again(const RouteArgs& a, int m, uint64_t* mine, float* raw) {
   if (!route_regs<32, NQ, GROUPS, BIAS>(a, m, true, reinterpret_cast<uint32_t*>(mine)))
     route_row64(a, m, mine, raw);
 }
 
-template <int L, int NQ, bool GROUPS, bool BIAS>
+template <int L, int NQ, int GROUPS, bool BIAS>
 __global__ void __launch_bounds__(256) k_route_regs(const __grid_constant__ RouteArgs a) {
   // (the next kernel's CTAs are not let in early: routing 16,068 rows again they
   // filled the SMs unevenly, 11.2 -> 13.1 us)
@@ -766,16 +792,17 @@ __global__ void __launch_bounds__(256) k_route_any(const __grid_constant__ Route
   if (!route_row<float>(a, m, reinterpret_cast<uint32_t*>(mine), raw)) route_row64(a, m, mine, raw);
 }
 
+template <int L, int NQ, int GROUPS>
+cudaError_t run_regs(const RouteArgs& a, int blocks, int threads, size_t smem, cudaStream_t st) {
+  auto* kernel = a.bias ? k_route_regs<L, NQ, GROUPS, true> : k_route_regs<L, NQ, GROUPS, false>;
+  return launch_after(kernel, dim3(blocks), threads, smem, st, a);
+}
 template <int L, int NQ>
-cudaError_t run_regs(const RouteArgs& a, bool groups, int blocks, int threads, size_t smem,
-              cudaStream_t st) {
-  if (groups) {
-    if (a.bias) return launch_after(k_route_regs<L, NQ, true, true>, dim3(blocks), threads, smem, st, a);
-    return launch_after(k_route_regs<L, NQ, true, false>, dim3(blocks), threads, smem, st, a);
-  } else {
-    if (a.bias) return launch_after(k_route_regs<L, NQ, false, true>, dim3(blocks), threads, smem, st, a);
-    return launch_after(k_route_regs<L, NQ, false, false>, dim3(blocks), threads, smem, st, a);
-  }
+cudaError_t run_regs(const RouteArgs& a, int groups, int blocks, int threads, size_t smem,
+                     cudaStream_t st) {
+  if (groups == 0) return run_regs<L, NQ, 0>(a, blocks, threads, smem, st);
+  if (groups == 1) return run_regs<L, NQ, 1>(a, blocks, threads, smem, st);
+  return run_regs<L, NQ, 2>(a, blocks, threads, smem, st);
 }
 
 }  // namespace
@@ -794,13 +821,17 @@ cudaError_t launch_route_groups(const moeq_routing& r, const void* logits, int l
   a.M = M;
   a.lanes_per_group = 1;
   while (a.lanes_per_group * 2 * r.n_groups <= 32) a.lanes_per_group *= 2;
-  const int nq = (r.n_experts + 3) / 4;
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  const bool groups = r.topk_groups < r.n_groups;
-  const int gs = r.n_experts / r.n_groups, gq = gs / 4;
+  // 1: groups that are a power of two of whole quads; 2: others, padded to that
+  const int gs = r.n_experts / r.n_groups;
+  int gq = 1;
+  while (gq * 4 < gs) gq *= 2;
+  const int groups = r.topk_groups == r.n_groups ? 0 : gs == 4 * gq ? 1 : 2;
+  const int quads = (r.n_experts + 3) / 4, nq = groups == 2 ? r.n_groups * gq : quads;
   a.group_quads = gq;
-  const bool regs = nq <= 128 && !(groups && (gs % 4 || gq > 32 || (gq & (gq - 1))));
+  a.group_size = gs;
+  const bool regs = nq <= 128 && !(groups && gq > 32);
   // Many rows of at most 128 (256) experts: four (two) rows share a warp, a
   // lane holds four quads; the picks sit one per lane.
   int lanes = 32;
@@ -811,7 +842,7 @@ cudaError_t launch_route_groups(const moeq_routing& r, const void* logits, int l
   const int64_t rows = ((int64_t)M + 32 / lanes - 1) / (32 / lanes);  // warps
   // 48 bytes per quad of experts and warp (48 KB hold one row of 4096); in
   // registers 384 for a row's candidates and 64 per lane for its keys
-  const size_t slot = regs && nq < 51 ? 384 + 32 * 64 : (size_t)nq * 48;
+  const size_t slot = regs && quads < 51 ? 384 + 32 * 64 : (size_t)quads * 48;
   a.slot = (int)(slot / 8);
   // few rows: spread over the SMs first
   int warps = (int)(rows > 8 * (int64_t)sms ? 8 : (rows + sms - 1) / sms);

@@ -185,3 +185,17 @@ def test_as_many_rows_as_an_int_counts():
     moeq.moeq_route_groups(moeq.routing(1, 1), l, idx, w)
     assert int(idx.max()) == 0 and int(idx.min()) == 0
     assert float(w.max()) == 1 and float(w.min()) == 1
+
+
+@pytest.mark.parametrize("M", [7, 2600])
+@pytest.mark.parametrize("with_bias,score", [(True, "sigmoid"), (False, "softmax")])
+@pytest.mark.parametrize("E,groups,keep,top,K", [
+    (240, 4, 2, 2, 16), (60, 12, 3, 1, 8), (96, 32, 7, 2, 10), (33, 11, 5, 2, 6), (7, 7, 3, 1, 3),
+    (368, 16, 12, 2, 6), (500, 5, 2, 2, 9), (26, 2, 1, 1, 8), (130, 2, 1, 2, 8), (300, 20, 6, 2, 8)])
+def test_groups_of_any_size(E, groups, keep, top, K, with_bias, score, M):
+    l, b = draw(M, E, E + groups + M, torch.bfloat16 if M == 7 else torch.float32)
+    l[0] = float("-inf")
+    l[1, : E // groups + 1] = float("nan")
+    l[2] = l[2, 0].item()
+    l[3, 1:] = float("-inf")
+    check(l, K, b if with_bias else None, score, groups, keep, top)
