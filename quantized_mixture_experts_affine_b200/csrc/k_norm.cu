@@ -3,10 +3,10 @@
 //
 // A CTA holds a row in registers (8-element vectors, 16-byte accesses), so
 // x and the residual are read once and each output is written once.  Few rows
-// are bound by the trip to memory and the block reduction (1 x 4096: 3.3 us),
+// are bound by the trip to memory and the block reduction (1 x 4096: 3.1 us),
 // many by HBM (16,068 x 4096, fp32 streams, e4m3 by 128: 129 us, the copy
-// rate) or, on bf16 streams, nearly so (96 us, 4.8 TB/s, 74 % of it; the rest
-// is instruction issue: the codes are taken twice).
+// rate) or, on bf16 streams, nearly so (93 us, 5.0 TB/s, 76 % of it; the rest
+// is instruction issue: taking the codes twice is 14 us of it).
 //
 // The codes do not depend on the norm's factor: with t = r gamma and
 // a = max |t| over the row (or 128 columns), n / scale = t top / a, top = 127
@@ -28,6 +28,7 @@ struct NormArgs {
   moeq_norm_args n;
   int H, vecs;   // vecs: 8-element vectors of a row, the last one partial when H % 8
   int n_scales;  // scales per row
+  float per_column;  // 1 / H
   // 16-byte accesses per operand (8 bytes for q) where pointer and stride allow
   bool vx, vr, vro, vg, vy, vq;
 };
@@ -221,7 +222,7 @@ template <int NV, int XT, int RT, bool FULL, int MAXT>
 __global__ void __launch_bounds__(MAXT) k_add_rmsnorm(const __grid_constant__ NormArgs a) {
   tc::grid_dep_wait();
   constexpr bool ANY = XT == kAny;
-  __shared__ float red[32], red_max[32];
+  __shared__ __align__(16) float red[32], red_max[32];
   __shared__ unsigned long long red_key[32];
   const moeq_norm_args& n = a.n;
   const int T = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = T >> 5;
@@ -312,20 +313,28 @@ __global__ void __launch_bounds__(MAXT) k_add_rmsnorm(const __grid_constant__ No
       red[warp] = ss;
       red_max[warp] = row_max;
       red_key[warp] = row_key;
+    } else if (tid == 1) {  // (up to the next four)
+      for (int i = nw; i & 3; ++i) red[i] = red_max[i] = 0.0f;
     }
     __syncthreads();
     ss = 0.0f;
-    for (int i = 0; i < nw; ++i) ss += red[i];
+    for (int i = 0; i < nw; i += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(red + i);
+      ss += (v.x + v.y) + (v.z + v.w);
+    }
     if (whole) {
       if (exact) {
-        for (int i = 0; i < nw; ++i) row_max = max_nan(row_max, red_max[i]);
+        for (int i = 0; i < nw; i += 4) {
+          const float4 v = *reinterpret_cast<const float4*>(red_max + i);
+          row_max = max_nan(row_max, max_nan(max_nan(v.x, v.y), max_nan(v.z, v.w)));
+        }
       } else {
         for (int i = 0; i < nw; ++i) row_key = red_key[i] > row_key ? red_key[i] : row_key;
       }
     }
   }
   if (whole && !exact) row_max = __uint_as_float((uint32_t)(row_key >> 32));
-  const float inv = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(ss, (float)a.H) + n.eps));
+  const float inv = rsqrtf(__fmaf_rn(ss, a.per_column, n.eps));
   const float top = i8 ? 127.0f : 448.0f, to_scale = inv * (i8 ? 1.0f / 127.0f : 1.0f / 448.0f);
 
 #pragma unroll
@@ -406,6 +415,7 @@ cudaError_t launch_add_rmsnorm(const moeq_norm_args& n, int M, int H, cudaStream
   NormArgs a;
   a.n = n;
   a.H = H;
+  a.per_column = 1.0f / (float)H;
   a.vecs = (H + 7) / 8;
   a.n_scales = n.q_group ? (H + kQGroup - 1) / kQGroup : 1;
   a.vx = wide(n.x, n.x_stride, size_of(n.x_type), 16);
