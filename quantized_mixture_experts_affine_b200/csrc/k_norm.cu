@@ -1,8 +1,10 @@
 // RMS norm of r = x + residual with the new residual stream, a bf16 output
 // and an 8-bit output with scales, in one pass over the row.
 //
-// A CTA holds a row in registers (8-element vectors, 16-byte accesses), so
-// x and the residual are read once and each output is written once.  Few rows
+// A CTA holds a row in registers (8-element vectors, 16-byte accesses; rows of
+// other lengths and alignments one by one, neighbours across a warp: 848 x 4959
+// 22.3 -> 12.5 us against eight neighbours per lane), so x and the residual are
+// read once and each output is written once.  Few rows
 // are bound by the trip to memory and the block reduction (1 x 4096: 3.1 us),
 // many by HBM (16,068 x 4096, fp32 streams, e4m3 by 128: 129 us, the copy
 // rate) or, on bf16 streams, nearly so (93 us, 5.0 TB/s, 76 % of it; the rest
@@ -26,40 +28,41 @@ constexpr int kQGroup = 128;
 
 struct NormArgs {
   moeq_norm_args n;
-  int H, vecs;   // vecs: 8-element vectors of a row, the last one partial when H % 8
+  int H, vecs;   // vecs: eights of a row's columns, the last one partial when H % 8
   int n_scales;  // scales per row
   float per_column;  // 1 / H
-  // 16-byte accesses per operand (8 bytes for q) where pointer and stride allow
-  bool vx, vr, vro, vg, vy, vq;
 };
 
-__device__ __forceinline__ void load8(const void* p, int type, int64_t at, int n, bool vec,
-                                      float (&v)[8]) {
-  if (vec && n == 8) {
-    if (type == MOEQ_F32) {
-      const float4* f = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + at);
-      const float4 a = f[0], b = f[1];
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
-      const uint4 a = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p) + at);
-      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+// Eight values of a row, in whole aligned vectors (n is 8 or 0), or (ANY) one by
+// one, 32 apart, so that a warp's accesses are neighbours at any alignment: those
+// below n, counted from the first.
+template <bool ANY>
+__device__ __forceinline__ void load8(const void* p, int type, int64_t at, int n, float (&v)[8]) {
+  if (ANY) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-      }
-    }
+    for (int i = 0; i < 8; ++i)
+      v[i] = 32 * i >= n ? 0.0f
+             : type == MOEQ_F32
+                 ? reinterpret_cast<const float*>(p)[at + 32 * i]
+                 : bf16_bits_to_float(reinterpret_cast<const uint16_t*>(p)[at + 32 * i]);
     return;
   }
+  if (n <= 0) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-  if (n <= 0) return;
+    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+  } else if (type == MOEQ_F32) {
+    const float4* f = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + at);
+    const float4 a = f[0], b = f[1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+    const uint4 a = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p) + at);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (i < n)
-      v[i] = type == MOEQ_F32 ? reinterpret_cast<const float*>(p)[at + i]
-                              : bf16_bits_to_float(reinterpret_cast<const uint16_t*>(p)[at + i]);
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
   }
 }
 
@@ -68,9 +71,16 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-__device__ __forceinline__ void store8(void* p, int type, int64_t at, int n, bool vec,
-                                       const float (&v)[8]) {
-  if (vec && n == 8) {
+template <bool ANY>
+__device__ __forceinline__ void store8(void* p, int type, int64_t at, int n, const float (&v)[8]) {
+  if (ANY) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (32 * i < n) {
+        if (type == MOEQ_F32) reinterpret_cast<float*>(p)[at + 32 * i] = v[i];
+        else reinterpret_cast<__nv_bfloat16*>(p)[at + 32 * i] = __float2bfloat16_rn(v[i]);
+      }
+  } else if (n > 0) {
     if (type == MOEQ_F32) {
       float4* f = reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + at);
       f[0] = make_float4(v[0], v[1], v[2], v[3]);
@@ -80,15 +90,7 @@ __device__ __forceinline__ void store8(void* p, int type, int64_t at, int n, boo
           make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]),
                      bf16_pair(v[6], v[7]));
     }
-    return;
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < n) {
-      if (type == MOEQ_F32) reinterpret_cast<float*>(p)[at + i] = v[i];
-      else
-        reinterpret_cast<__nv_bfloat16*>(p)[at + i] = __float2bfloat16_rn(v[i]);
-    }
 }
 
 // Magnitude of t = r gamma exactly, as a key that orders like it: the fp32
@@ -131,11 +133,11 @@ __device__ __forceinline__ void unpack8(const uint4& w, float (&g)[8]) {
 }
 
 // `code` with the bytes that differ from `other` (all of them for a tiny
-// maximum) decided in fp64; a: the exact largest |r gamma|.
-__device__ __noinline__ uint2 settle(bool i8, uint2 code, uint2 other, bool tiny, float r0,
-                                     float r1, float r2, float r3, float r4, float r5, float r6,
-                                     float r7, uint4 gp, double a) {
-  const float r[8] = {r0, r1, r2, r3, r4, r5, r6, r7};
+// maximum) decided in fp64; a: the exact largest |r gamma|, of the first and the
+// last four.  (Out of line: it is seldom called.)
+__device__ __forceinline__ uint2 settle(bool i8, uint2 code, uint2 other, const bool (&tiny)[2],
+                                        const float (&r)[8], const uint4& gp,
+                                        const double (&a)[2]) {
   float g[8];
   unpack8(gp, g);
   uint32_t out[2] = {code.x, code.y};
@@ -143,23 +145,34 @@ __device__ __noinline__ uint2 settle(bool i8, uint2 code, uint2 other, bool tiny
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int sh = 8 * (j & 3);
-    if (tiny || ((diff[j / 4] >> sh) & 255u))
-      out[j / 4] = (out[j / 4] & ~(255u << sh)) | code64(i8, r[j], g[j], a) << sh;
+    if (tiny[j / 4] || ((diff[j / 4] >> sh) & 255u))
+      out[j / 4] = (out[j / 4] & ~(255u << sh)) | code64(i8, r[j], g[j], a[j / 4]) << sh;
   }
   return make_uint2(out[0], out[1]);
+}
+__device__ __noinline__ uint2 settle_one(bool i8, uint2 code, uint2 other, bool tiny, float r0,
+                                         float r1, float r2, float r3, float r4, float r5,
+                                         float r6, float r7, uint4 gp, double a) {
+  return settle(i8, code, other, {tiny, tiny}, {r0, r1, r2, r3, r4, r5, r6, r7}, gp, {a, a});
+}
+__device__ __noinline__ uint2 settle_two(bool i8, uint2 code, uint2 other, bool tiny0, bool tiny1,
+                                         float r0, float r1, float r2, float r3, float r4,
+                                         float r5, float r6, float r7, uint4 gp, double a0,
+                                         double a1) {
+  return settle(i8, code, other, {tiny0, tiny1}, {r0, r1, r2, r3, r4, r5, r6, r7}, gp, {a0, a1});
 }
 
 // fp32 cannot hold top / a below this (and r gamma may have lost bits)
 constexpr float kTinyMax = 1e-28f;
 
-// Eight codes of t f in fp32.
-__device__ __forceinline__ uint2 codes8(bool i8, const float (&t)[8], float f) {
+// Eight codes of t f in fp32 (f0 for the first four).
+__device__ __forceinline__ uint2 codes8(bool i8, const float (&t)[8], float f0, float f1) {
   uint32_t out[2];
   if (i8) {
     // t f + 1.5 2^23 rounds t f to the nearest whole number, in the low bits
     uint32_t q[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) q[j] = __float_as_uint(__fmaf_rn(t[j], f, 12582912.0f));
+    for (int j = 0; j < 8; ++j) q[j] = __float_as_uint(__fmaf_rn(t[j], j < 4 ? f0 : f1, 12582912.0f));
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       out[h] = __byte_perm(__byte_perm(q[4 * h], q[4 * h + 1], 0x0040u),
@@ -167,6 +180,7 @@ __device__ __forceinline__ uint2 codes8(bool i8, const float (&t)[8], float f) {
   } else {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+      const float f = h ? f1 : f0;
       asm("{\n\t.reg .b16 a, b;\n\t"
           "cvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\t"
           "cvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\t"
@@ -185,11 +199,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
-// Largest |r gamma| of a thread's eight values as a key (see mag_key).
-__device__ __forceinline__ unsigned long long max8_key(const float (&r)[8], const float (&g)[8]) {
+// Largest |r gamma| of a thread's values from FIRST to LAST as a key (see mag_key).
+template <int FIRST, int LAST>
+__device__ __forceinline__ unsigned long long max_key(const float (&r)[8], const float (&g)[8]) {
   unsigned long long key = 0;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = FIRST; j <= LAST; ++j) {
     const unsigned long long k = mag_key(r[j], g[j]);
     key = k > key ? k : key;
   }
@@ -232,35 +247,33 @@ __global__ void __launch_bounds__(MAXT) k_add_rmsnorm(const __grid_constant__ No
   // r gamma of a bf16 stream (8 + 8 bits) is exact in fp32
   const bool exact = (res ? rt : xt) == MOEQ_BF16;
   const bool whole = n.q && n.q_group == 0, i8 = n.q_type == MOEQ_I8;
-  auto count = [&](int i) -> int {
-    const int v = tid + i * T;
-    return FULL ? 8 : v >= a.vecs ? 0 : ANY ? min(8, a.H - 8 * v) : 8;
+  // first column of a thread's vector i, and how many columns it has from there
+  auto column = [&](int i) -> int {
+    return ANY ? 256 * (warp + i * nw) + lane : 8 * (tid + i * T);
   };
+  auto count = [&](int i) -> int { return FULL ? 8 : a.H - column(i); };
   float r[NV][8];
   uint4 gp[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int v = tid + i * T, cnt = count(i);
-    load8(n.x, xt, m * n.x_stride + 8 * v, cnt, !ANY || a.vx, r[i]);
-  }
+  for (int i = 0; i < NV; ++i)
+    load8<ANY>(n.x, xt, m * n.x_stride + column(i), count(i), r[i]);
   float s[NV][8];
   if (res) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      load8(n.residual, rt, m * n.r_stride + 8 * (tid + i * T), count(i), !ANY || a.vr, s[i]);
+      load8<ANY>(n.residual, rt, m * n.r_stride + column(i), count(i), s[i]);
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int v = tid + i * T, cnt = count(i);
     gp[i] = make_uint4(0u, 0u, 0u, 0u);
-    if ((!ANY || a.vg) && cnt == 8) {
-      gp[i] = *reinterpret_cast<const uint4*>(n.gamma + 8 * v);
-    } else if (ANY) {
+    if (ANY) {
       uint32_t h[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) h[j] = j < cnt ? n.gamma[8 * v + j] : 0u;
+      for (int j = 0; j < 8; ++j) h[j] = 32 * j < count(i) ? n.gamma[column(i) + 32 * j] : 0u;
       gp[i] = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16,
                          h[6] | h[7] << 16);
+    } else if (count(i) > 0) {
+      gp[i] = *reinterpret_cast<const uint4*>(n.gamma + column(i));
     }
   }
   if (res) {
@@ -268,21 +281,19 @@ __global__ void __launch_bounds__(MAXT) k_add_rmsnorm(const __grid_constant__ No
     for (int i = 0; i < NV; ++i) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) r[i][j] += s[i][j];
-      const int cnt = count(i);
       // the norm is of the stream as it is stored
       if (rt == MOEQ_BF16) {
         const uint4 p = make_uint4(bf16_pair(r[i][0], r[i][1]), bf16_pair(r[i][2], r[i][3]),
                                    bf16_pair(r[i][4], r[i][5]), bf16_pair(r[i][6], r[i][7]));
         unpack8(p, r[i]);
         if (!ANY) {
-          if (n.r_out && cnt > 0)
+          if (n.r_out && count(i) > 0)
             *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(n.r_out) + m * n.r_out_stride +
-                                      8 * (tid + i * T)) = p;
+                                      column(i)) = p;
           continue;
         }
       }
-      if (n.r_out && cnt > 0)
-        store8(n.r_out, rt, m * n.r_out_stride + 8 * (tid + i * T), cnt, !ANY || a.vro, r[i]);
+      if (n.r_out) store8<ANY>(n.r_out, rt, m * n.r_out_stride + column(i), count(i), r[i]);
     }
   }
   float ss = 0.0f, row_max = 0.0f;
@@ -298,7 +309,7 @@ __global__ void __launch_bounds__(MAXT) k_add_rmsnorm(const __grid_constant__ No
 #pragma unroll
         for (int j = 0; j < 8; ++j) row_max = max_nan(row_max, fabsf(r[i][j] * g[j]));
       } else {
-        const unsigned long long k = max8_key(r[i], g);
+        const unsigned long long k = max_key<0, 7>(r[i], g);
         row_key = k > row_key ? k : row_key;
       }
     }
@@ -339,50 +350,83 @@ __global__ void __launch_bounds__(MAXT) k_add_rmsnorm(const __grid_constant__ No
 
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int v = tid + i * T, cnt = count(i);
+    const int c0 = column(i), cnt = count(i);
     float g[8];
     unpack8(gp[i], g);
-    if (n.y && cnt > 0) {
+    if (n.y) {
       float o[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = r[i][j] * inv * g[j];
-      store8(n.y, MOEQ_BF16, m * n.y_stride + 8 * v, cnt, !ANY || a.vy, o);
+      store8<ANY>(n.y, MOEQ_BF16, m * n.y_stride + c0, cnt, o);
     }
     if (!n.q) continue;
-    float t[8], am = row_max;
+    // The largest of the row, or of 128 columns: 16 neighbouring lanes hold them,
+    // or (ANY) the warp its first and its last four values.
+    float t[8], a0 = row_max;
 #pragma unroll
     for (int j = 0; j < 8; ++j) t[j] = r[i][j] * g[j];
-    if (!whole) {  // 16 neighbouring lanes hold 128 columns
-      am = 0.0f;
+    float a1 = a0;
+    if (!whole) {
+      a0 = a1 = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) am = max_nan(am, fabsf(t[j]));
-      am = lanes_max<8>(am);
+      for (int j = 0; j < 8; ++j) {
+        if (ANY && j >= 4) a1 = max_nan(a1, fabsf(t[j]));
+        else a0 = max_nan(a0, fabsf(t[j]));
+      }
+      a0 = lanes_max<ANY ? 16 : 8>(a0);
+      a1 = ANY ? lanes_max<16>(a1) : a0;
     }
     // t f is off by three roundings and the division's 2 ulp (2^-21 relative);
     // where moving it by 2^-20 either way changes a code, fp64 decides
-    const float f = __fdividef(top, am);
-    uint2 code = codes8(i8, t, f * (1.0f + 9.5367431640625e-7f));
-    const uint2 other = codes8(i8, t, f * (1.0f - 9.5367431640625e-7f));
-    const bool finite = am < INFINITY, tiny = am < kTinyMax;
-    const bool doubt = finite && (tiny || code.x != other.x || code.y != other.y);
-    unsigned long long key = row_key;
-    if (!exact && !whole && __any_sync(0xffffffffu, doubt)) key = lanes_max<8>(max8_key(r[i], g));
-    if (doubt)
-      code = settle(i8, code, other, tiny, r[i][0], r[i][1], r[i][2], r[i][3], r[i][4], r[i][5],
-                    r[i][6], r[i][7], gp[i], exact ? (double)am : mag_value(key));
-    if (!finite) code = make_uint2(0u, 0u);
-    if (cnt > 0) {
-      if (whole ? v == 0 : (v & 15) == 0)
-        n.q_scales[m * a.n_scales + (whole ? 0 : v >> 4)] =
-            finite ? am * to_scale : __uint_as_float(0x7FC00000u);
-      uint8_t* q = reinterpret_cast<uint8_t*>(n.q) + m * n.q_stride + 8 * v;
-      if (!ANY || (a.vq && cnt == 8)) {
-        *reinterpret_cast<uint2*>(q) = code;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j < cnt) q[j] = (uint8_t)((j < 4 ? code.x : code.y) >> (8 * (j & 3)));
+    const float up = 1.0f + 9.5367431640625e-7f, down = 1.0f - 9.5367431640625e-7f;
+    const float f0 = __fdividef(top, a0), f1 = ANY ? __fdividef(top, a1) : f0;
+    uint2 code = codes8(i8, t, f0 * up, f1 * up);
+    const uint2 other = codes8(i8, t, f0 * down, f1 * down);
+    if (ANY) {
+      const bool doubt0 = cnt > 0 && a0 < INFINITY && (a0 < kTinyMax || code.x != other.x);
+      const bool doubt1 = cnt > 128 && a1 < INFINITY && (a1 < kTinyMax || code.y != other.y);
+      unsigned long long key0 = row_key, key1 = row_key;
+      if (!exact && !whole && __any_sync(0xffffffffu, doubt0 || doubt1)) {
+        key0 = lanes_max<16>(max_key<0, 3>(r[i], g));
+        key1 = lanes_max<16>(max_key<4, 7>(r[i], g));
       }
+      if (doubt0 || doubt1)
+        code = settle_two(i8, code, other, a0 < kTinyMax, a1 < kTinyMax, r[i][0], r[i][1], r[i][2],
+                          r[i][3], r[i][4], r[i][5], r[i][6], r[i][7], gp[i],
+                          exact ? (double)a0 : mag_value(key0),
+                          exact ? (double)a1 : mag_value(key1));
+      if (!(a0 < INFINITY)) code.x = 0u;
+      if (!(a1 < INFINITY)) code.y = 0u;
+    } else {
+      const bool finite = a0 < INFINITY;
+      const bool doubt = finite && (a0 < kTinyMax || code.x != other.x || code.y != other.y);
+      unsigned long long key = row_key;
+      if (!exact && !whole && __any_sync(0xffffffffu, doubt))
+        key = lanes_max<8>(max_key<0, 7>(r[i], g));
+      if (doubt)
+        code = settle_one(i8, code, other, a0 < kTinyMax, r[i][0], r[i][1], r[i][2], r[i][3],
+                          r[i][4], r[i][5], r[i][6], r[i][7], gp[i],
+                          exact ? (double)a0 : mag_value(key));
+      if (!finite) code = make_uint2(0u, 0u);
+    }
+    auto scale = [&](int at, float am) {
+      n.q_scales[m * a.n_scales + at] = am < INFINITY ? am * to_scale : __uint_as_float(0x7FC00000u);
+    };
+    if (whole) {
+      if (i == 0 && tid == 0) scale(0, a0);
+    } else if (ANY) {
+      if (lane == 0 && cnt > 0) scale(c0 >> 7, a0);
+      if (lane == 0 && cnt > 128) scale((c0 >> 7) + 1, a1);
+    } else if ((c0 & 127) == 0 && cnt > 0) {
+      scale(c0 >> 7, a0);
+    }
+    uint8_t* q = reinterpret_cast<uint8_t*>(n.q) + m * n.q_stride + c0;
+    if (ANY) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (32 * j < cnt) q[32 * j] = (uint8_t)((j < 4 ? code.x : code.y) >> (8 * (j & 3)));
+    } else if (cnt > 0) {
+      *reinterpret_cast<uint2*>(q) = code;
     }
   }
 }
@@ -405,7 +449,7 @@ cudaError_t run(const NormArgs& a, int M, int sms, cudaStream_t st) {
 }
 
 bool wide(const void* p, int64_t stride, int item, int bytes) {
-  return p && ((uintptr_t)p % bytes) == 0 && ((stride * item) % bytes) == 0;
+  return ((uintptr_t)p % bytes) == 0 && ((stride * item) % bytes) == 0;
 }
 int size_of(int type) { return type == MOEQ_F32 ? 4 : type == MOEQ_BF16 ? 2 : 1; }
 
@@ -418,15 +462,12 @@ cudaError_t launch_add_rmsnorm(const moeq_norm_args& n, int M, int H, cudaStream
   a.per_column = 1.0f / (float)H;
   a.vecs = (H + 7) / 8;
   a.n_scales = n.q_group ? (H + kQGroup - 1) / kQGroup : 1;
-  a.vx = wide(n.x, n.x_stride, size_of(n.x_type), 16);
-  a.vr = wide(n.residual, n.r_stride, size_of(n.r_type), 16);
-  a.vro = wide(n.r_out, n.r_out_stride, size_of(n.r_type), 16);
-  a.vg = wide(n.gamma, 0, 2, 16);
-  a.vy = wide(n.y, n.y_stride, 2, 16);
-  a.vq = wide(n.q, n.q_stride, 1, 8);
   const int sms = sm_count();
-  const bool vec = H % 8 == 0 && a.vx && a.vg && (!n.residual || a.vr) && (!n.r_out || a.vro) &&
-                   (!n.y || a.vy) && (!n.q || a.vq);
+  const bool vec = H % 8 == 0 && wide(n.x, n.x_stride, size_of(n.x_type), 16) &&
+                   wide(n.gamma, 0, 2, 16) &&
+                   (!n.residual || wide(n.residual, n.r_stride, size_of(n.r_type), 16)) &&
+                   (!n.r_out || wide(n.r_out, n.r_out_stride, size_of(n.r_type), 16)) &&
+                   (!n.y || wide(n.y, n.y_stride, 2, 16)) && (!n.q || wide(n.q, n.q_stride, 1, 8));
   const bool xb = n.x_type == MOEQ_BF16, rb = n.r_type == MOEQ_BF16;
   if (!vec) return run<kAny, kAny>(a, M, sms, st);
   if (!n.residual && xb) return run<MOEQ_BF16, kNone>(a, M, sms, st);
