@@ -177,6 +177,74 @@ def test_calls_one_after_the_other(M):
             assert torch.equal(a, b)
 
 
+def ops_on(M):
+    """x -> (norm, its codes through a projection, that through a router)."""
+    H, O = 512, 640
+    g = torch.Generator(device="cuda").manual_seed(M)
+    w = ref.matrix(O, H, 4, 64, g)
+    t = moeq.qtensor(w["w"], w["s"], w["b"], O, H, 4, 64)
+    gamma = torch.ones(H, device="cuda", dtype=torch.bfloat16)
+    R = moeq.routing(O, 8, moeq.SCORE_SIGMOID, 8, 4, 2)
+    need = max(moeq.moeq_linear_workspace_bytes(t, M, torch.int8, torch.float32),
+               moeq.moeq_linear_workspace_bytes(t, M, torch.bfloat16, torch.bfloat16))
+    ws = torch.empty(max(need, 1), dtype=torch.uint8, device="cuda")
+
+    def run(x, keep=w):  # (the operands live as long as the calls)
+        _, y, q, s = add_rmsnorm(x, gamma, 1e-6, q_dtype=torch.int8)
+        l = linear(t, q, torch.float32, x_scales=s, ws=ws)
+        return [y, q, s, l, linear(t, y, torch.bfloat16, ws=ws), *route_groups(R, l)]
+    xs = [torch.randn(M, H, device="cuda", generator=g) for _ in range(2)]
+    return run, xs
+
+
+@pytest.mark.parametrize("M", [3, 100, 2600])
+def test_inputs_from_another_stream(M):
+    """A call waits for an event of another stream, with kernels of its own
+    stream right before it."""
+    run, xs = ops_on(M)
+    want = [run(x) for x in xs]
+    torch.cuda.synchronize()
+    side, x = torch.cuda.Stream(), torch.zeros_like(xs[0])
+    for i in range(6):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200000)
+            x.copy_(xs[i % 2])
+        y = [v * 2 for v in xs]  # kernels of this stream, before the wait
+        torch.cuda.current_stream().wait_stream(side)
+        got = run(x)
+        side.wait_stream(torch.cuda.current_stream())
+        for a, b in zip(got, want[i % 2]):
+            assert torch.equal(a, b)
+        del y
+
+
+@pytest.mark.parametrize("M", [3, 100, 2600])
+def test_a_fork_and_a_copy_in_a_graph(M):
+    """Captured calls after a copy, and after branches that join before them."""
+    run, xs = ops_on(M)
+    want = [run(2 * x) for x in xs]
+    src, x, side = xs[0].clone(), torch.empty_like(xs[0]), torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(100000)
+            x.copy_(src)
+            x += src
+        z = src * 3
+        main.wait_stream(side)
+        got = run(x)
+        z += 1
+    for k in (1, 0, 1):
+        src.copy_(xs[k])
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want[k]):
+            assert torch.equal(a, b)
+
+
 FIRST = """
 import sys
 sys.path[:0] = {path!r}
