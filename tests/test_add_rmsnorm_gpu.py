@@ -1,9 +1,11 @@
 """moeq_add_rmsnorm against the 64-bit reference.
 
 The residual stream and the codes are equal to the reference's.  Scales: the
-sum of squares has at most 32 + 5 + 32 additions in a row in fp32 (69 * 2^-24,
-halved by the root) and six more roundings: 2.5e-6 relative.  y: that, three
-roundings of the product and one half step of bf16 (2^-8 relative at most).
+sum of squares has at most 32 + 5 + 10 additions in a row in fp32 (47 * 2^-24,
+halved by the root); 1 / H and the sum with eps (halved too), the reciprocal
+root's 2 ulp and three more roundings are 8 * 2^-24: 1.9e-6 relative, under the
+2.5e-6 asked for.  y: that, three roundings of the product and one half step of
+bf16 (2^-8 relative at most).
 """
 import pytest
 
