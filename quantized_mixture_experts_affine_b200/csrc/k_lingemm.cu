@@ -536,7 +536,10 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* tmap,
 // 16 columns comes out about n 2^-27 too small.  A bf16 y does not show it;
 // for an fp32 y (SUMS) the accumulator is read after every kChunk blocks and
 // the parts are added in registers, rounded to nearest: the two accumulators
-// then take turns within a tile too.
+// then take turns within a tile too.  The products of the rests come first,
+// while the accumulator is small and little is cut off: 202 x 1920 x 640, 4-bit,
+// int8 by 128 columns, relative error 1.0e-6 with them last, 3.7e-7 so (the plain
+// fp32 product 5.3e-7).
 constexpr int kChunk = 8;
 constexpr int gemm_threads(bool sums) { return 640; }
 
@@ -583,7 +586,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(SUMS), 
       const int o0 = item % a.tiles_o * (2 * kTile) + (int)rank * kTile;
       const int m0 = item / a.tiles_o * BN + (int)rank * (BN / 2);
       for (int k0 = 0; k0 < KB; k0 += chunk)
-        for (int prod = 0; prod < a.products; ++prod)
+        for (int prod = a.products - 1; prod >= 0; --prod)
           for (int kb = k0; kb < min(k0 + chunk, KB); ++kb, ++it) {
             const uint32_t s = it % ST, ph = (it / ST) & 1u;
             if (!wait_bar(&empty[s], ph ^ 1u, a.status)) goto done;
