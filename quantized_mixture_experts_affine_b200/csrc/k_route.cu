@@ -89,6 +89,10 @@ __device__ __forceinline__ float logit_at(const RouteArgs& a, int64_t row, int e
 
 __device__ __forceinline__ bool is_out(float l) { return !(l > -INFINITY); }
 
+// Where a row's largest score is below this, smaller ones leave fp32's normal
+// range and what decides is taken in fp64.
+constexpr float kTinyScore = 1e-30f;
+
 // Score of a logit: sigmoid, or the softmax's numerator relative to the
 // row's largest logit.
 template <typename T>
@@ -160,13 +164,17 @@ __device__ bool route_row(const RouteArgs& a, int m, typename Keys<T>::K* keys, 
       }
     sum = warp_sum_t(z);
   }
-  // bound on the fp32 error of a score: a few roundings, the exponent's own
-  // (|d| 2^-24, and e^-d d stays under 0.37) and the normaliser's additions
-  // (nq / 8 + 5 of them in a row), all relative to the largest score
+  // bound on the fp32 error of a score, relative to the largest: a few roundings,
+  // the exponential and the normaliser's additions (nq / 8 + 5 of them in a row);
+  // a softmax's exponents d count from the largest (e^-d d stays under 0.37, the
+  // normaliser's mean of d under ln 4096), a sigmoid's do not: where the largest
+  // logit is below zero, all scores are off by its exponent's rounding
   T tol_s = (T)0;
   if (!exact64) {
     const T s_max = is_out(mx) ? (T)0 : numerator<T>(r, mx, mx) / (softmax ? sum : (T)1);
-    tol_s = ((T)1.2e-6f + (softmax ? (T)6e-8f * (T)(nq / 8 + 12) : (T)0)) * s_max;
+    const T far = softmax ? (T)6e-8f * (T)(nq / 8 + 12)
+                          : (T)1.2e-7f * (T)fmaxf(0.0f, -r.router_scale * mx);
+    tol_s = s_max < (T)kTinyScore ? (T)INFINITY : ((T)1.2e-6f + far) * s_max;
   }
 
   // ---- keys
@@ -341,10 +349,15 @@ __device__ bool route_row(const RouteArgs& a, int m, typename Keys<T>::K* keys, 
 // scored in fp64, one per lane, and ranked again.
 
 // 1 / (1 + e^-z) and e^d; the fast exponential and division are within 2 ulp,
-// but for the exponent's rounding.
+// but for the exponent's rounding.  EXACT_EXP: the softmax's by expf, since beside
+// a bias the normaliser's error counts (2048 x 256 in 8 groups: with the fast
+// one's bound more rows are in doubt, 10.4 against 7.9 us).
+template <bool EXACT_EXP>
 __device__ __forceinline__ float fast_numerator(const moeq_routing& r, float l, float mx) {
   if (r.score == MOEQ_SCORE_SIGMOID) return __fdividef(1.0f, 1.0f + __expf(-r.router_scale * l));
-  return l == mx ? 1.0f : __expf(r.router_scale * (l - mx));
+  if (l == mx) return 1.0f;
+  const float d = r.router_scale * (l - mx);
+  return EXACT_EXP ? expf(d) : __expf(d);
 }
 
 // Keys<float>::of for what is not NaN (v + 0 makes one zero of both).
@@ -473,15 +486,23 @@ __device__ __forceinline__ bool route_regs(const RouteArgs& a, int m, bool store
     for (int j = 0; j < NQ; ++j)
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        if (!is_out(l[j][c])) z += fast_numerator(r, l[j][c], mx);
+        if (!is_out(l[j][c])) z += fast_numerator<BIAS>(r, l[j][c], mx);
     sum = seg_sum<L>(z);
   }
   const float inv = __fdividef(1.0f, sum);
-  // Error of a score relative to the largest: exponential 2^-22, division 2^-22, the
-  // exponent's and the last roundings under 2^-22 (e^-d d < 0.37), and the
-  // normaliser's additions
-  const float s_max = is_out(mx) ? 0.0f : fast_numerator(r, mx, mx) * inv;
-  const float tol_s = (7.2e-7f + (softmax ? 6e-8f * (4 * NQ + 8) : 0.0f)) * s_max;
+  // Error of a score relative to the largest, in units of 2^-23 (1.2e-7).
+  // Sigmoid: the exponential 2 + 1.18 |z| and half of |z| for its exponent's
+  // rounding, times 1 - s; the sum and the division 3; above zero that is under 6,
+  // below it 1.68 |z| of the largest logit come on top.  Softmax, x counted from the
+  // largest: the exponential 2 + 1.18 x (expf: 2), its exponent's roundings x, all
+  // that times e^-x, which is 2.1; the last rounding 0.5.  With a bias the
+  // normaliser counts too: its terms 2 + x, whose mean is at most ln(E / sum) (an
+  // entropy is at most ln E), half of its 4 NQ + 5 additions, and the division 2.
+  const float s_max = is_out(mx) ? 0.0f : fast_numerator<BIAS>(r, mx, mx) * inv;
+  float far = 0.0f;
+  if (!softmax) far = 2.4e-7f * fmaxf(0.0f, -r.router_scale * mx);
+  else if (BIAS) far = 1.2e-7f * __logf((float)E * 1.01f * inv) + 6e-8f * (4 * NQ + 7);
+  const float tol_s = s_max < kTinyScore ? INFINITY : (7.2e-7f + far) * s_max;
 
   uint32_t k[NQ][4];
 #pragma unroll
@@ -490,7 +511,7 @@ __device__ __forceinline__ bool route_regs(const RouteArgs& a, int m, bool store
     quad(lane + L * j, n);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      const float v = BIAS ? fast_numerator(r, l[j][c], mx) * inv + b[j][c] : l[j][c];
+      const float v = BIAS ? fast_numerator<BIAS>(r, l[j][c], mx) * inv + b[j][c] : l[j][c];
       k[j][c] = c >= n ? 0u : is_out(l[j][c]) ? 1u : BIAS ? KT::of(v) : key_of(v);
     }
   }
@@ -512,10 +533,10 @@ __device__ __forceinline__ bool route_regs(const RouteArgs& a, int m, bool store
       }
       gk[j] = k1;
       if (r.group_top == 2 && k1 > 1) {
-        const float v1 = BIAS ? KT::value(k1) : fast_numerator(r, KT::value(k1), mx) * inv;
+        const float v1 = BIAS ? KT::value(k1) : fast_numerator<BIAS>(r, KT::value(k1), mx) * inv;
         const float v2 = k2 <= 1 ? 0.0f
                          : BIAS  ? KT::value(k2)
-                                 : fast_numerator(r, KT::value(k2), mx) * inv;
+                                 : fast_numerator<BIAS>(r, KT::value(k2), mx) * inv;
         gk[j] = KT::of(v1 + v2);
       }
     }

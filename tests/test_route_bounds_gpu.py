@@ -1,0 +1,66 @@
+"""moeq_route_groups where fp32 scores are least able to tell: sigmoid rows far
+below zero, whose scores are off by their logits' size times fp32's rounding.
+
+Weights: a score's relative error there is the rounding of the scaled logit,
+|z| 2^-24 with |z| <= 91 (5.5e-6), and 8 * 2^-24 of the exponential and the
+division; the sum it is divided by has the same and five additions: under
+1.25e-5 in all.
+"""
+import pytest
+
+import ops_reference as ref
+from quantized_mixture_experts_affine_b200 import moeq
+from quantized_mixture_experts_affine_b200.layer import route_groups
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+REL = 1.25e-5
+STEP = 2.0 ** -17  # a whole number of units in the last place of every logit here
+
+
+def check(logits, K, bias=None, groups=1, keep=1, group_top=1, scale=1.0, renorm=True):
+    r = moeq.routing(logits.shape[1], K, moeq.SCORE_SIGMOID, groups, keep, group_top, renorm,
+                     scale, 1.0)
+    idx, w = route_groups(r, logits, bias)
+    torch.cuda.synchronize()
+    ri, rw = ref.route(logits, K, "sigmoid", bias, groups, keep, group_top, renorm,
+                       float(torch.tensor(scale)), 1.0)
+    assert torch.equal(idx.cpu(), ri)
+    err = (w.cpu().double() - rw).abs()
+    assert bool((err <= REL * rw.abs() + 1e-37).all()), float(err.max())
+
+
+def paired(M, E, groups, z, scale, seed):
+    """Rows whose groups hold z + i STEP and z - i STEP, another i in each, the
+    rest lower: the sums of two differ by i^2 STEP^2 relative, 64-bit arithmetic
+    alone can order them."""
+    g = torch.Generator().manual_seed(seed)
+    z0 = round(z / scale / STEP) * STEP
+    l = torch.full((M, groups, E // groups), z0 - 3.0)
+    for m in range(M):
+        i = torch.randperm(5 * groups, generator=g)[:groups] * STEP
+        l[m, :, 0] = z0 + i
+        l[m, :, 1] = z0 - i
+    return l.view(M, E).cuda()
+
+
+@pytest.mark.parametrize("z", [-12.0, -30.0, -45.0, -60.0, -85.0, -88.0])
+@pytest.mark.parametrize("scale", [1.0, 0.7])
+@pytest.mark.parametrize("M,E,groups,keep,K", [
+    (40, 8, 4, 2, 2), (30, 256, 8, 4, 8), (20, 512, 16, 5, 4), (2400, 128, 8, 3, 4),
+    (2400, 256, 16, 6, 4), (20, 1024, 32, 11, 4), (20, 60, 12, 4, 4)])
+def test_two_best_of_groups_far_below_zero(z, scale, M, E, groups, keep, K):
+    check(paired(M, E, groups, z, scale, E - int(z)), K, None, groups, keep, 2, scale)
+
+
+@pytest.mark.parametrize("z", [-30.0, -60.0, -85.0])
+@pytest.mark.parametrize("M,E,K", [(24, 64, 8), (2400, 64, 8), (24, 512, 8), (8, 640, 6)])
+def test_biased_picks_far_below_zero(z, M, E, K):
+    """Biases that even the scores out but for one part in 10^7 or less."""
+    l = z / 0.7 + torch.linspace(-0.5, 0.5, E).roll(7)
+    s = torch.sigmoid(0.7 * l.double())
+    b = (s.max() - s).float()
+    rows = torch.stack([l] * M).cuda()
+    check(rows, K, b.cuda(), scale=0.7)
+    check(rows, K, b.cuda(), 4, 2, 2, scale=0.7)
