@@ -715,16 +715,18 @@ __device__ __forceinline__ bool route_regs(const RouteArgs& a, int m, bool store
           }
           __syncwarp();
           const bool cand = lane < n;
-          const int e = cand ? (int)slots[lane] : kNoExpert;
+          const int e = cand ? (int)slots[lane] : 0;
           const float le = cand ? __uint_as_float(slots[32 + lane]) : -INFINITY;
           const double v64 = is_out(le) ? -INFINITY
                                         : numerator<double>(r, le, mx) / z +
                                               (double)__uint_as_float(slots[64 + lane]);
+          // (an expert that is out comes after one whose bias is -infinity)
+          const int order = is_out(le) ? e + kMaxE : e;
           int rank = 0;
           for (int p = 0; p < n; ++p) {
             const double vp = __shfl_sync(0xffffffffu, v64, p);
-            const int ep = __shfl_sync(0xffffffffu, e, p);
-            rank += (vp > v64 || (vp == v64 && ep < e)) ? 1 : 0;
+            const int op = __shfl_sync(0xffffffffu, order, p);
+            rank += (vp > v64 || (vp == v64 && op < order)) ? 1 : 0;
           }
           __syncwarp();
           if (cand) {

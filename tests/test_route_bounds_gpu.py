@@ -64,3 +64,25 @@ def test_biased_picks_far_below_zero(z, M, E, K):
     rows = torch.stack([l] * M).cuda()
     check(rows, K, b.cuda(), scale=0.7)
     check(rows, K, b.cuda(), 4, 2, 2, scale=0.7)
+
+
+@pytest.mark.parametrize("M", [3, 2400])
+@pytest.mark.parametrize("E", [16, 64, 300])
+def test_experts_under_a_bias_of_minus_infinity(M, E):
+    """They come after every other, before those whose logits are out."""
+    g = torch.Generator(device="cuda").manual_seed(E)
+    l = torch.randn(M, E, device="cuda", generator=g)
+    b = torch.zeros(E, device="cuda")
+    l[:, : E - 6] = float("nan")
+    l[1, 2] = float("-inf")
+    b[E - 3:] = float("-inf")
+    idx = list(range(E - 6, E - 3)) + list(range(E - 3, E)) + [0, 1]
+    check(l, 8, b)
+    r = moeq.routing(E, 8, moeq.SCORE_SIGMOID)
+    got, w = route_groups(r, l, b)
+    assert got[0].tolist()[3:] == idx[3:] and w[0, 6:].abs().sum() == 0 and (w[0, :6] > 0).all()
+    # fewer experts than picks, and a bias that masks all but two
+    b[:] = float("-inf")
+    b[E - 2:] = 0.25
+    check(l, 8, b)
+    check(torch.randn(M, E, device="cuda", generator=g), 6, b)
