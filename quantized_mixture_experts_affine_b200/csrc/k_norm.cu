@@ -110,10 +110,10 @@ __device__ __forceinline__ double mag_value(unsigned long long k) {
   return (double)__uint_as_float((uint32_t)(k >> 32)) + (double)rest;
 }
 
-// Code of one value from fp64: the value next to a border, or a tiny maximum.
-__device__ __forceinline__ uint32_t code64(bool i8, float r, float g, double a) {
-  if (r * g == 0.0f) return 0u;
-  const double v = (double)r * (double)g * (i8 ? 127.0 : 448.0) / a;
+// Code of one value t = r gamma (exact in fp64).
+__device__ __forceinline__ uint32_t code64(bool i8, double t, double a) {
+  if (t == 0.0) return 0u;
+  const double v = t * (i8 ? 127.0 : 448.0) / a;
   if (i8) return (uint32_t)(int)rint(fmin(fmax(v, -127.0), 127.0)) & 255u;
   int e = (int)((__double_as_longlong(v) >> 52) & 2047) - 1023;
   if (e < -6) e = -6;
@@ -132,12 +132,11 @@ __device__ __forceinline__ void unpack8(const uint4& w, float (&g)[8]) {
   }
 }
 
-// `code` with the bytes that differ from `other` (all of them for a tiny
-// maximum) decided in fp64; a: the exact largest |r gamma|, of the first and the
-// last four.  (Out of line: it is seldom called.)
-__device__ __forceinline__ uint2 settle(bool i8, uint2 code, uint2 other, const bool (&tiny)[2],
-                                        const float (&r)[8], const uint4& gp,
-                                        const double (&a)[2]) {
+// `code` with the bytes that differ from `other` decided in fp64; a: the exact
+// largest |r gamma|, of the first and the last four.  (Out of line: it is seldom
+// called.)
+__device__ __forceinline__ uint2 settle(bool i8, uint2 code, uint2 other, const float (&r)[8],
+                                        const uint4& gp, const double (&a)[2]) {
   float g[8];
   unpack8(gp, g);
   uint32_t out[2] = {code.x, code.y};
@@ -145,25 +144,28 @@ __device__ __forceinline__ uint2 settle(bool i8, uint2 code, uint2 other, const 
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int sh = 8 * (j & 3);
-    if (tiny[j / 4] || ((diff[j / 4] >> sh) & 255u))
-      out[j / 4] = (out[j / 4] & ~(255u << sh)) | code64(i8, r[j], g[j], a[j / 4]) << sh;
+    if ((diff[j / 4] >> sh) & 255u)
+      out[j / 4] = (out[j / 4] & ~(255u << sh)) | code64(i8, (double)r[j] * (double)g[j], a[j / 4]) << sh;
   }
   return make_uint2(out[0], out[1]);
 }
-__device__ __noinline__ uint2 settle_one(bool i8, uint2 code, uint2 other, bool tiny, float r0,
-                                         float r1, float r2, float r3, float r4, float r5,
-                                         float r6, float r7, uint4 gp, double a) {
-  return settle(i8, code, other, {tiny, tiny}, {r0, r1, r2, r3, r4, r5, r6, r7}, gp, {a, a});
+__device__ __noinline__ uint2 settle_one(bool i8, uint2 code, uint2 other, float r0, float r1,
+                                         float r2, float r3, float r4, float r5, float r6,
+                                         float r7, uint4 gp, double a) {
+  return settle(i8, code, other, {r0, r1, r2, r3, r4, r5, r6, r7}, gp, {a, a});
 }
-__device__ __noinline__ uint2 settle_two(bool i8, uint2 code, uint2 other, bool tiny0, bool tiny1,
-                                         float r0, float r1, float r2, float r3, float r4,
-                                         float r5, float r6, float r7, uint4 gp, double a0,
-                                         double a1) {
-  return settle(i8, code, other, {tiny0, tiny1}, {r0, r1, r2, r3, r4, r5, r6, r7}, gp, {a0, a1});
+__device__ __noinline__ uint2 settle_two(bool i8, uint2 code, uint2 other, float r0, float r1,
+                                         float r2, float r3, float r4, float r5, float r6,
+                                         float r7, uint4 gp, double a0, double a1) {
+  return settle(i8, code, other, {r0, r1, r2, r3, r4, r5, r6, r7}, gp, {a0, a1});
 }
 
-// fp32 cannot hold top / a below this (and r gamma may have lost bits)
-constexpr float kTinyMax = 1e-28f;
+// fp32 cannot hold top / a below the first (and r gamma may have lost bits); above
+// the second the fast division gives 0, and products may have overflowed.  Rows and
+// groups whose largest |r gamma| lies outside of them (zeros, infinities and NaN
+// among them) are done again in fp64 (odd_row).
+constexpr float kTinyMax = 1e-24f, kHugeMax = 4.2535296e37f;  // (2^125)
+__device__ __forceinline__ bool is_odd(float a) { return !(a >= kTinyMax && a <= kHugeMax); }
 
 // Eight codes of t f in fp32 (f0 for the first four).
 __device__ __forceinline__ uint2 codes8(bool i8, const float (&t)[8], float f0, float f1) {
@@ -231,6 +233,95 @@ __device__ __forceinline__ float lanes_max(float k) {
 // kNone: there is none), for rows of whole, aligned vectors; kAny: any.
 // MAXT: threads of the largest block.
 constexpr int kAny = -1, kNone = -2;
+
+// The 8-bit output of the warp's columns again, everything from fp64, which holds
+// every product: codes and scales of a row or of groups outside of fp32's range.  r
+// is read from where it was written, or added up again.  Rows with one scale: all
+// threads of the block are here.
+template <bool ANY>
+__device__ __noinline__ void odd_row(const NormArgs& a, int nv, float to_scale,
+                                     unsigned long long* red_key) {
+  const moeq_norm_args& n = a.n;
+  const int T = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = T >> 5;
+  const int64_t m = blockIdx.x;
+  const bool whole = n.q_group == 0, i8 = n.q_type == MOEQ_I8;
+  // first column of vector i (see k_add_rmsnorm), its products, and their largest
+  // from `first` to `last` as an ordered integer, NaN above all
+  auto column = [&](int i) { return ANY ? 256 * (warp + i * nw) + lane : 8 * (tid + i * T); };
+  auto products = [&](int i, double (&t)[8]) {
+    const int c0 = column(i), cnt = a.H - c0;
+    float r[8], s[8];
+    if (n.r_out) {
+      load8<ANY>(n.r_out, n.r_type, m * n.r_out_stride + c0, cnt, r);
+    } else {
+      load8<ANY>(n.x, n.x_type, m * n.x_stride + c0, cnt, r);
+      if (n.residual) {
+        load8<ANY>(n.residual, n.r_type, m * n.r_stride + c0, cnt, s);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          r[j] += s[j];
+          if (n.r_type == MOEQ_BF16) r[j] = __bfloat162float(__float2bfloat16_rn(r[j]));
+        }
+      }
+    }
+    load8<ANY>(n.gamma, MOEQ_BF16, c0, cnt, s);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t[j] = (double)r[j] * (double)s[j];
+  };
+  auto largest = [](const double (&t)[8], int first, int last) {
+    unsigned long long key = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const unsigned long long k = (unsigned long long)__double_as_longlong(fabs(t[j]));
+      if (j >= first && j <= last && k > key) key = k;
+    }
+    return key;
+  };
+  double t[8];
+  unsigned long long row = 0;
+  if (whole) {
+#pragma unroll 1
+    for (int i = 0; i < nv; ++i) {
+      products(i, t);
+      const unsigned long long k = largest(t, 0, 7);
+      row = k > row ? k : row;
+    }
+    row = lanes_max<16>(row);
+    __syncthreads();
+    if (lane == 0) red_key[warp] = row;
+    __syncthreads();
+    for (int i = 0; i < nw; ++i) row = red_key[i] > row ? red_key[i] : row;
+    if (row == 0) return;  // zeros: scale and codes are written
+  }
+#pragma unroll 1
+  for (int i = 0; i < nv; ++i) {
+    products(i, t);
+    const int c0 = column(i), cnt = a.H - c0;
+    unsigned long long key[2] = {row, row};  // of the first and the last four
+    if (!whole) {
+      key[0] = lanes_max<ANY ? 16 : 8>(largest(t, 0, ANY ? 3 : 7));
+      key[1] = ANY ? lanes_max<16>(largest(t, 4, 7)) : key[0];
+      if (__all_sync(0xffffffffu, (key[0] | key[1]) == 0)) continue;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const double top = __longlong_as_double((long long)key[h]);
+      const bool finite = top < INFINITY;
+      const float scale =
+          finite ? (float)(top * (double)to_scale) : __uint_as_float(0x7FC00000u);
+      const int c = ANY ? c0 + 128 * h : c0;  // first of the four, in the row
+      if (whole ? i + h + tid == 0 : (c & 127) == 0 && c < a.H && (ANY || h == 0))
+        n.q_scales[m * a.n_scales + (whole ? 0 : c >> 7)] = scale;
+#pragma unroll
+      for (int j = 4 * h; j < 4 * h + 4; ++j) {
+        const int at = ANY ? 32 * j : j;
+        if (at < cnt)
+          reinterpret_cast<uint8_t*>(n.q)[m * n.q_stride + c0 + at] =
+              (uint8_t)(finite ? code64(i8, t[j], top) : 0u);
+      }
+    }
+  }
+}
 
 // FULL: every thread has NV whole vectors.
 template <int NV, int XT, int RT, bool FULL, int MAXT>
@@ -348,6 +439,7 @@ __global__ void __launch_bounds__(MAXT) k_add_rmsnorm(const __grid_constant__ No
   const float inv = rsqrtf(__fmaf_rn(ss, a.per_column, n.eps));
   const float top = i8 ? 127.0f : 448.0f, to_scale = inv * (i8 ? 1.0f / 127.0f : 1.0f / 448.0f);
 
+  bool odd = whole && is_odd(row_max);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c0 = column(i), cnt = count(i);
@@ -375,50 +467,43 @@ __global__ void __launch_bounds__(MAXT) k_add_rmsnorm(const __grid_constant__ No
       }
       a0 = lanes_max<ANY ? 16 : 8>(a0);
       a1 = ANY ? lanes_max<16>(a1) : a0;
+      odd |= cnt > 0 && (is_odd(a0) || (ANY && cnt > 128 && is_odd(a1)));
     }
     // t f is off by three roundings and the division's 2 ulp (2^-21 relative);
     // where moving it by 2^-20 either way changes a code, fp64 decides
     const float up = 1.0f + 9.5367431640625e-7f, down = 1.0f - 9.5367431640625e-7f;
-    const float f0 = __fdividef(top, a0), f1 = ANY ? __fdividef(top, a1) : f0;
+    // (plus 2^-115, which only a tiny largest feels: the codes of zeros are zeros)
+    const float least = 2.40741243e-35f;
+    const float f0 = __fdividef(top, a0 + least), f1 = ANY ? __fdividef(top, a1 + least) : f0;
     uint2 code = codes8(i8, t, f0 * up, f1 * up);
     const uint2 other = codes8(i8, t, f0 * down, f1 * down);
+    const bool doubt = code.x != other.x || code.y != other.y;
     if (ANY) {
-      const bool doubt0 = cnt > 0 && a0 < INFINITY && (a0 < kTinyMax || code.x != other.x);
-      const bool doubt1 = cnt > 128 && a1 < INFINITY && (a1 < kTinyMax || code.y != other.y);
       unsigned long long key0 = row_key, key1 = row_key;
-      if (!exact && !whole && __any_sync(0xffffffffu, doubt0 || doubt1)) {
+      if (!exact && !whole && __any_sync(0xffffffffu, doubt)) {
         key0 = lanes_max<16>(max_key<0, 3>(r[i], g));
         key1 = lanes_max<16>(max_key<4, 7>(r[i], g));
       }
-      if (doubt0 || doubt1)
-        code = settle_two(i8, code, other, a0 < kTinyMax, a1 < kTinyMax, r[i][0], r[i][1], r[i][2],
-                          r[i][3], r[i][4], r[i][5], r[i][6], r[i][7], gp[i],
-                          exact ? (double)a0 : mag_value(key0),
+      if (doubt)
+        code = settle_two(i8, code, other, r[i][0], r[i][1], r[i][2], r[i][3], r[i][4], r[i][5],
+                          r[i][6], r[i][7], gp[i], exact ? (double)a0 : mag_value(key0),
                           exact ? (double)a1 : mag_value(key1));
-      if (!(a0 < INFINITY)) code.x = 0u;
-      if (!(a1 < INFINITY)) code.y = 0u;
     } else {
-      const bool finite = a0 < INFINITY;
-      const bool doubt = finite && (a0 < kTinyMax || code.x != other.x || code.y != other.y);
       unsigned long long key = row_key;
       if (!exact && !whole && __any_sync(0xffffffffu, doubt))
         key = lanes_max<8>(max_key<0, 7>(r[i], g));
       if (doubt)
-        code = settle_one(i8, code, other, a0 < kTinyMax, r[i][0], r[i][1], r[i][2], r[i][3],
-                          r[i][4], r[i][5], r[i][6], r[i][7], gp[i],
-                          exact ? (double)a0 : mag_value(key));
-      if (!finite) code = make_uint2(0u, 0u);
+        code = settle_one(i8, code, other, r[i][0], r[i][1], r[i][2], r[i][3], r[i][4], r[i][5],
+                          r[i][6], r[i][7], gp[i], exact ? (double)a0 : mag_value(key));
     }
-    auto scale = [&](int at, float am) {
-      n.q_scales[m * a.n_scales + at] = am < INFINITY ? am * to_scale : __uint_as_float(0x7FC00000u);
-    };
+    float* scale = n.q_scales + m * a.n_scales;
     if (whole) {
-      if (i == 0 && tid == 0) scale(0, a0);
+      if (i == 0 && tid == 0) scale[0] = a0 * to_scale;
     } else if (ANY) {
-      if (lane == 0 && cnt > 0) scale(c0 >> 7, a0);
-      if (lane == 0 && cnt > 128) scale((c0 >> 7) + 1, a1);
+      if (lane == 0 && cnt > 0) scale[c0 >> 7] = a0 * to_scale;
+      if (lane == 0 && cnt > 128) scale[(c0 >> 7) + 1] = a1 * to_scale;
     } else if ((c0 & 127) == 0 && cnt > 0) {
-      scale(c0 >> 7, a0);
+      scale[c0 >> 7] = a0 * to_scale;
     }
     uint8_t* q = reinterpret_cast<uint8_t*>(n.q) + m * n.q_stride + c0;
     if (ANY) {
@@ -429,6 +514,8 @@ __global__ void __launch_bounds__(MAXT) k_add_rmsnorm(const __grid_constant__ No
       *reinterpret_cast<uint2*>(q) = code;
     }
   }
+  // (a row is odd in all threads or none, a group in all of its lanes)
+  if (n.q && __any_sync(0xffffffffu, odd)) odd_row<ANY>(a, NV, to_scale, red_key);
 }
 
 template <int NV, int XT, int RT, int MAXT>

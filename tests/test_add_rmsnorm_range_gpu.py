@@ -1,0 +1,60 @@
+"""moeq_add_rmsnorm at the ends of fp32's range, and row by row against a batch.
+
+Tolerances as in test_add_rmsnorm_gpu: scales 2.5e-6 relative (what is added here
+are exact products by powers of two), y one half step of bf16 more; values below
+fp32's normal range are off by its smallest step.
+"""
+import pytest
+
+import ops_reference as ref
+from test_add_rmsnorm_gpu import SCALE, T, Y, draw
+from quantized_mixture_experts_affine_b200.layer import add_rmsnorm
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+TINY = 2.0 ** -149
+
+
+def check(x, gamma, q, group, eps=1e-6, residual=None):
+    r, y, c, s = add_rmsnorm(x, gamma, eps, residual, True, T[q], group)
+    torch.cuda.synchronize()
+    want = ref.add_rmsnorm(x, gamma, float(torch.tensor(eps)), residual, q, group)
+    if residual is not None:
+        assert torch.equal(r, want["r"])
+    assert torch.equal(c.float().double(), want["codes"])
+    assert bool(((s.double() - want["scales"]).abs() <= SCALE * want["scales"] + TINY).all())
+    assert bool(((y.double() - want["y"]).abs() <= Y * want["y"].abs() + 1e-38).all())
+
+
+CASES = [(q, group, xt, H) for q in ("int8", "e4m3") for group in (0, 128)
+         for xt in ("f32", "bf16") for H in (64, 1001, 4096)]
+
+
+@pytest.mark.parametrize("q,group,xt,H", CASES)
+def test_large_products(q, group, xt, H):
+    """|r gamma| next to fp32's largest value, and beyond it."""
+    x, gamma, _ = draw(4, H, "f32", None, H)
+    x = (x.clamp(-8, 8) * 1e16).to(T[xt])
+    check(x, (gamma.float().clamp(0.5, 1.5) * 2.0 ** 70).to(torch.bfloat16), q, group)
+    check(x, (gamma.float() * 1e25).to(torch.bfloat16), q, group)
+
+
+@pytest.mark.parametrize("q,group,xt,H", CASES + [("int8", 0, "f32", 32768),
+                                                  ("e4m3", 128, "bf16", 8200)])
+def test_small_products(q, group, xt, H):
+    """|r gamma| below fp32's normal range: codes and scales all the same."""
+    x, gamma, _ = draw(4, H, "f32", None, H + 1)
+    for xs, gs in ((1e-20, 1e-19), (1e-24, 1e-20), (1e-30, 1e-18), (1e-36, 1.0)):
+        check((x * xs).to(T[xt]), (gamma.float() * gs).to(torch.bfloat16), q, group, eps=1e-30)
+
+
+def test_zero_rows_and_groups_beside_others():
+    x, gamma, _ = draw(40, 2048, "f32", None, 9)
+    x[::3] = 0
+    x[1, 128:300] = 0
+    x[4, :1024] = 0
+    for q, group in (("int8", 0), ("e4m3", 128)):
+        check(x, gamma, q, group)
+        check(x[:, :1001].contiguous(), gamma[:1001].contiguous(), q, group)
+        check(x.to(torch.bfloat16), gamma, q, group, residual=torch.zeros_like(x))
