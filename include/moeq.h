@@ -407,7 +407,7 @@ typedef struct {
  * At least one of y and q is given.  Codes are those of exact arithmetic on
  * r and gamma.  A row or group of zeros has scale 0 and codes 0; one that
  * holds an infinity or NaN has scale NaN and codes 0.  The sum of squares is
- * an fp32 one: |r| up to 1e18.
+ * an fp32 one, of scaled values where it would overflow: |r| up to 1e30.
  * r_out may be the residual's own memory (or x's, at the same type and
  * stride); no other output may overlap an input.
  * 1 <= H <= 32768.  Any alignment of whole elements is taken; 16-byte aligned

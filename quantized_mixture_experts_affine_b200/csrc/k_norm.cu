@@ -163,7 +163,7 @@ __device__ __noinline__ uint2 settle_two(bool i8, uint2 code, uint2 other, float
 // fp32 cannot hold top / a below the first (and r gamma may have lost bits); above
 // the second the fast division gives 0, and products may have overflowed.  Rows and
 // groups whose largest |r gamma| lies outside of them (zeros, infinities and NaN
-// among them) are done again in fp64 (odd_row).
+// among them) are done again in fp64 (redo).
 constexpr float kTinyMax = 1e-24f, kHugeMax = 4.2535296e37f;  // (2^125)
 __device__ __forceinline__ bool is_odd(float a) { return !(a >= kTinyMax && a <= kHugeMax); }
 
@@ -234,28 +234,29 @@ __device__ __forceinline__ float lanes_max(float k) {
 // MAXT: threads of the largest block.
 constexpr int kAny = -1, kNone = -2;
 
-// The 8-bit output of the warp's columns again, everything from fp64, which holds
-// every product: codes and scales of a row or of groups outside of fp32's range.  r
-// is read from where it was written, or added up again.  Rows with one scale: all
-// threads of the block are here.
+// What fp32's range does not hold, done again: r is read from where it was written,
+// or added up again.  Rows whose squares overflow (inv not above 0) are norm'd with
+// the squares of r 2^-80.  Then the 8-bit output of the warp's columns, everything
+// from fp64, which holds every product.  For such a row, and for rows with one
+// scale, all threads of the block are here.
 template <bool ANY>
-__device__ __noinline__ void odd_row(const NormArgs& a, int nv, float to_scale,
-                                     unsigned long long* red_key) {
+__device__ __noinline__ void redo(const NormArgs& a, int nv, float inv, float* red,
+                                  unsigned long long* red_key) {
   const moeq_norm_args& n = a.n;
   const int T = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = T >> 5;
   const int64_t m = blockIdx.x;
   const bool whole = n.q_group == 0, i8 = n.q_type == MOEQ_I8;
-  // first column of vector i (see k_add_rmsnorm), its products, and their largest
-  // from `first` to `last` as an ordered integer, NaN above all
+  // first column of vector i (see k_add_rmsnorm), its stream, its products, and their
+  // largest from `first` to `last` as an ordered integer, NaN above all
   auto column = [&](int i) { return ANY ? 256 * (warp + i * nw) + lane : 8 * (tid + i * T); };
-  auto products = [&](int i, double (&t)[8]) {
+  auto stream = [&](int i, float (&r)[8]) {
     const int c0 = column(i), cnt = a.H - c0;
-    float r[8], s[8];
     if (n.r_out) {
       load8<ANY>(n.r_out, n.r_type, m * n.r_out_stride + c0, cnt, r);
     } else {
       load8<ANY>(n.x, n.x_type, m * n.x_stride + c0, cnt, r);
       if (n.residual) {
+        float s[8];
         load8<ANY>(n.residual, n.r_type, m * n.r_stride + c0, cnt, s);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -264,9 +265,13 @@ __device__ __noinline__ void odd_row(const NormArgs& a, int nv, float to_scale,
         }
       }
     }
-    load8<ANY>(n.gamma, MOEQ_BF16, c0, cnt, s);
+  };
+  auto products = [&](int i, double (&t)[8]) {
+    float r[8], g[8];
+    stream(i, r);
+    load8<ANY>(n.gamma, MOEQ_BF16, column(i), a.H - column(i), g);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) t[j] = (double)r[j] * (double)s[j];
+    for (int j = 0; j < 8; ++j) t[j] = (double)r[j] * (double)g[j];
   };
   auto largest = [](const double (&t)[8], int first, int last) {
     unsigned long long key = 0;
@@ -277,6 +282,36 @@ __device__ __noinline__ void odd_row(const NormArgs& a, int nv, float to_scale,
     }
     return key;
   };
+  if (!(inv > 0.0f)) {
+    const float down = 8.27180613e-25f;  // 2^-80
+    float ss = 0.0f;
+#pragma unroll 1
+    for (int i = 0; i < nv; ++i) {
+      float r[8];
+      stream(i, r);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss = __fmaf_rn(r[j] * down, r[j] * down, ss);
+    }
+    ss = warp_sum(ss);
+    __syncthreads();
+    if (lane == 0) red[warp] = ss;
+    __syncthreads();
+    ss = 0.0f;
+    for (int i = 0; i < nw; ++i) ss += red[i];
+    inv = rsqrtf(__fmaf_rn(ss, a.per_column, n.eps * down * down)) * down;
+#pragma unroll 1
+    for (int i = 0; n.y && i < nv; ++i) {
+      const int c0 = column(i), cnt = a.H - c0;
+      float r[8], g[8];
+      stream(i, r);
+      load8<ANY>(n.gamma, MOEQ_BF16, c0, cnt, g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[j] = r[j] * inv * g[j];
+      store8<ANY>(n.y, MOEQ_BF16, m * n.y_stride + c0, cnt, g);
+    }
+  }
+  if (!n.q) return;
+  const double to_scale = (double)inv / (i8 ? 127.0 : 448.0);
   double t[8];
   unsigned long long row = 0;
   if (whole) {
@@ -291,7 +326,7 @@ __device__ __noinline__ void odd_row(const NormArgs& a, int nv, float to_scale,
     if (lane == 0) red_key[warp] = row;
     __syncthreads();
     for (int i = 0; i < nw; ++i) row = red_key[i] > row ? red_key[i] : row;
-    if (row == 0) return;  // zeros: scale and codes are written
+    if (row == 0) return;  // zeros: scale and codes are there
   }
 #pragma unroll 1
   for (int i = 0; i < nv; ++i) {
@@ -307,8 +342,7 @@ __device__ __noinline__ void odd_row(const NormArgs& a, int nv, float to_scale,
     for (int h = 0; h < 2; ++h) {
       const double top = __longlong_as_double((long long)key[h]);
       const bool finite = top < INFINITY;
-      const float scale =
-          finite ? (float)(top * (double)to_scale) : __uint_as_float(0x7FC00000u);
+      const float scale = finite ? (float)(top * to_scale) : __uint_as_float(0x7FC00000u);
       const int c = ANY ? c0 + 128 * h : c0;  // first of the four, in the row
       if (whole ? i + h + tid == 0 : (c & 127) == 0 && c < a.H && (ANY || h == 0))
         n.q_scales[m * a.n_scales + (whole ? 0 : c >> 7)] = scale;
@@ -439,7 +473,7 @@ __global__ void __launch_bounds__(MAXT) k_add_rmsnorm(const __grid_constant__ No
   const float inv = rsqrtf(__fmaf_rn(ss, a.per_column, n.eps));
   const float top = i8 ? 127.0f : 448.0f, to_scale = inv * (i8 ? 1.0f / 127.0f : 1.0f / 448.0f);
 
-  bool odd = whole && is_odd(row_max);
+  bool odd = whole && is_odd(row_max);  // (whole: there is an 8-bit output)
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c0 = column(i), cnt = count(i);
@@ -514,8 +548,8 @@ __global__ void __launch_bounds__(MAXT) k_add_rmsnorm(const __grid_constant__ No
       *reinterpret_cast<uint2*>(q) = code;
     }
   }
-  // (a row is odd in all threads or none, a group in all of its lanes)
-  if (n.q && __any_sync(0xffffffffu, odd)) odd_row<ANY>(a, NV, to_scale, red_key);
+  // (inv is the same in all threads, a row odd in all or none, a group in all its lanes)
+  if (__any_sync(0xffffffffu, odd || !(inv > 0.0f))) redo<ANY>(a, NV, inv, red, red_key);
 }
 
 template <int NV, int XT, int RT, int MAXT>

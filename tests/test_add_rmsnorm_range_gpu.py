@@ -58,3 +58,24 @@ def test_zero_rows_and_groups_beside_others():
         check(x, gamma, q, group)
         check(x[:, :1001].contiguous(), gamma[:1001].contiguous(), q, group)
         check(x.to(torch.bfloat16), gamma, q, group, residual=torch.zeros_like(x))
+
+
+@pytest.mark.parametrize("H", [8, 1001, 4096, 8200, 32768])
+@pytest.mark.parametrize("q,group", [("int8", 0), ("e4m3", 128)])
+@pytest.mark.parametrize("xt,rt", [("f32", None), ("bf16", "f32"), ("bf16", "bf16")])
+def test_large_rows(H, q, group, xt, rt):
+    """The squares' sum passes fp32's range; the norm does not."""
+    x, gamma, res = draw(3, H, "f32", rt, H + 2)
+    x = x.clamp(-10, 10)
+    for top in (1e17, 1e18, 1e24, 1e29):
+        r = None if res is None else (res.float() * (top / 100)).to(T[rt])
+        check((x * top).to(T[xt]), gamma, q, group, residual=r)
+
+
+def test_large_rows_beside_ordinary_ones():
+    x, gamma, _ = draw(6, 4096, "f32", None, 5)
+    x[1] *= 1e25
+    x[3] *= 1e18
+    x[4, 100] = 1e22
+    check(x, gamma, "int8", 0)
+    check(x, gamma, "e4m3", 128)
