@@ -332,7 +332,8 @@ size_t moeq_static_workspace_capacity(void);
  * keep nothing between calls and touch only the M rows they are given.
  * Row strides are in elements, at least the row's length, so rows may be
  * parts of wider ones.  Sums are fp32 in a fixed order: results are
- * deterministic.
+ * deterministic.  A norm's row of given alignment does not change with M; the
+ * last bits of a linear's and of routing weights may, with the way M rows take.
  */
 typedef enum { MOEQ_F32 = 0, MOEQ_BF16 = 1, MOEQ_I8 = 2, MOEQ_E4M3 = 3 } moeq_dtype;
 

@@ -243,12 +243,14 @@ template <bool ANY>
 __device__ __noinline__ void redo(const NormArgs& a, int nv, float inv, float* red,
                                   unsigned long long* red_key) {
   const moeq_norm_args& n = a.n;
-  const int T = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = T >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
   const int64_t m = blockIdx.x;
   const bool whole = n.q_group == 0, i8 = n.q_type == MOEQ_I8;
   // first column of vector i (see k_add_rmsnorm), its stream, its products, and their
   // largest from `first` to `last` as an ordered integer, NaN above all
-  auto column = [&](int i) { return ANY ? 256 * (warp + i * nw) + lane : 8 * (tid + i * T); };
+  auto column = [&](int i) {
+    return ANY ? 256 * (warp + i * nw) + lane : 256 * (warp * nv + i) + 8 * lane;
+  };
   auto stream = [&](int i, float (&r)[8]) {
     const int c0 = column(i), cnt = a.H - c0;
     if (n.r_out) {
@@ -284,20 +286,24 @@ __device__ __noinline__ void redo(const NormArgs& a, int nv, float inv, float* r
   };
   if (!(inv > 0.0f)) {
     const float down = 8.27180613e-25f;  // 2^-80
-    float ss = 0.0f;
+    // (in k_add_rmsnorm's order, for one vector a thread and for two)
+    const int sums = nv == 2 ? 2 * nw : nw;
+    float part = 0.0f;
+    __syncthreads();
 #pragma unroll 1
     for (int i = 0; i < nv; ++i) {
-      float r[8];
+      float r[8], sum = 0.0f;
       stream(i, r);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = __fmaf_rn(r[j] * down, r[j] * down, ss);
+      for (int j = 0; j < 8; ++j) sum = __fmaf_rn(r[j] * down, r[j] * down, sum);
+      part = warp_sum(sum) + (nv > 2 ? part : 0.0f);
+      if (lane == 0) red[nv > 2 ? warp : ANY ? warp + i * nw : warp * nv + i] = part;
     }
-    ss = warp_sum(ss);
+    if (tid == 1)
+      for (int i = sums; i & 3; ++i) red[i] = 0.0f;
     __syncthreads();
-    if (lane == 0) red[warp] = ss;
-    __syncthreads();
-    ss = 0.0f;
-    for (int i = 0; i < nw; ++i) ss += red[i];
+    float ss = 0.0f;
+    for (int i = 0; i < sums; i += 4) ss += (red[i] + red[i + 1]) + (red[i + 2] + red[i + 3]);
     inv = rsqrtf(__fmaf_rn(ss, a.per_column, n.eps * down * down)) * down;
 #pragma unroll 1
     for (int i = 0; n.y && i < nv; ++i) {
@@ -365,7 +371,7 @@ __global__ void __launch_bounds__(MAXT) k_add_rmsnorm(const __grid_constant__ No
   __shared__ __align__(16) float red[32], red_max[32];
   __shared__ unsigned long long red_key[32];
   const moeq_norm_args& n = a.n;
-  const int T = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = T >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
   const int64_t m = blockIdx.x;
   const int xt = ANY ? n.x_type : XT, rt = ANY ? n.r_type : RT;
   const bool res = ANY ? n.residual != nullptr : RT != kNone;
@@ -374,7 +380,7 @@ __global__ void __launch_bounds__(MAXT) k_add_rmsnorm(const __grid_constant__ No
   const bool whole = n.q && n.q_group == 0, i8 = n.q_type == MOEQ_I8;
   // first column of a thread's vector i, and how many columns it has from there
   auto column = [&](int i) -> int {
-    return ANY ? 256 * (warp + i * nw) + lane : 8 * (tid + i * T);
+    return ANY ? 256 * (warp + i * nw) + lane : 256 * (warp * NV + i) + 8 * lane;
   };
   auto count = [&](int i) -> int { return FULL ? 8 : a.H - column(i); };
   float r[NV][8];
@@ -421,12 +427,17 @@ __global__ void __launch_bounds__(MAXT) k_add_rmsnorm(const __grid_constant__ No
       if (n.r_out) store8<ANY>(n.r_out, rt, m * n.r_out_stride + column(i), count(i), r[i]);
     }
   }
-  float ss = 0.0f, row_max = 0.0f;
+  // The squares are added up over 32 neighbouring vectors, then over those in pairs,
+  // then over two pairs: the same whether a thread has one vector or two, so that a
+  // row's norm does not change with the batch (see run).
+  constexpr bool TWO = NV == 2;
+  float ss = 0.0f, ss2 = 0.0f, row_max = 0.0f;
   unsigned long long row_key = 0;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
+    float& sum = TWO && i == 1 ? ss2 : ss;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ss = __fmaf_rn(r[i][j], r[i][j], ss);
+    for (int j = 0; j < 8; ++j) sum = __fmaf_rn(r[i][j], r[i][j], sum);
     if (whole) {
       float g[8];
       unpack8(gp[i], g);
@@ -439,24 +450,41 @@ __global__ void __launch_bounds__(MAXT) k_add_rmsnorm(const __grid_constant__ No
       }
     }
   }
-  ss = warp_sum(ss);
+  if (TWO) {  // lanes below 16 add the first up, the others the second
+    const float mine = lane & 16 ? ss2 : ss, other = lane & 16 ? ss : ss2;
+    ss = mine + __shfl_xor_sync(0xffffffffu, other, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    // the pair (ANY: another warp has the second's neighbour)
+    if (!ANY || nw == 1) ss += __shfl_xor_sync(0xffffffffu, ss, 16);
+  } else {
+    ss = warp_sum(ss);
+  }
   if (whole) {
     if (exact) row_max = lanes_max<16>(row_max);
     else row_key = lanes_max<16>(row_key);
   }
   if (nw > 1) {
+    const int sums = TWO && ANY ? 2 * nw : nw;
+    if (TWO && ANY && lane == 16) red[warp + nw] = ss;
     if (lane == 0) {
       red[warp] = ss;
       red_max[warp] = row_max;
       red_key[warp] = row_key;
     } else if (tid == 1) {  // (up to the next four)
-      for (int i = nw; i & 3; ++i) red[i] = red_max[i] = 0.0f;
+      for (int i = sums; i & 3; ++i) red[i] = 0.0f;
+      for (int i = nw; i & 3; ++i) red_max[i] = 0.0f;
     }
     __syncthreads();
     ss = 0.0f;
-    for (int i = 0; i < nw; i += 4) {
+    for (int i = 0; i < sums; i += 4) {
       const float4 v = *reinterpret_cast<const float4*>(red + i);
-      ss += (v.x + v.y) + (v.z + v.w);
+      if (TWO && !ANY) {
+        ss += v.x + v.y;
+        ss += v.z + v.w;
+      } else {
+        ss += (v.x + v.y) + (v.z + v.w);
+      }
     }
     if (whole) {
       if (exact) {

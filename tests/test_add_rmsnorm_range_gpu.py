@@ -79,3 +79,19 @@ def test_large_rows_beside_ordinary_ones():
     x[4, 100] = 1e22
     check(x, gamma, "int8", 0)
     check(x, gamma, "e4m3", 128)
+
+
+@pytest.mark.parametrize("H", [8, 1000, 1001, 2048, 2056, 4096, 4091, 6000])
+@pytest.mark.parametrize("xt,rt", [("bf16", "bf16"), ("f32", None)])
+@pytest.mark.parametrize("q,group", [("int8", 0), ("e4m3", 128)])
+def test_rows_are_those_of_a_large_batch(H, xt, rt, q, group):
+    """One row and 1300 run other variants of the kernel: the same bits."""
+    x, gamma, res = draw(1300, H, xt, rt, H)
+    x[700] = x[700].float().clamp(-10, 10) * 1e24  # squares beyond fp32
+    many = add_rmsnorm(x, gamma, 1e-6, res, True, T[q], group)
+    for m in (0, 1, 700, 1299):
+        one = add_rmsnorm(x[m:m + 1].clone(), gamma, 1e-6,
+                          None if res is None else res[m:m + 1].clone(), True, T[q], group)
+        for a, b in zip(one, many):
+            if b is not None:
+                assert torch.equal(a[0].view(torch.uint8), b[m].view(torch.uint8))
