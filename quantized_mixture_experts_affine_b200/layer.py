@@ -6,6 +6,7 @@ generator; real weights can be wrapped the same way with ``moeq.qtensor``.
 """
 from __future__ import annotations
 
+import contextlib
 from dataclasses import dataclass, field
 
 from . import moeq
@@ -79,19 +80,66 @@ class Workspace:
         self.buf = torch.empty(self.bytes, dtype=torch.uint8, device=device)
 
 
+class _Buffers:
+    """Where a call on `stream` (None: the current one; a stream object or a raw
+    handle) gets its buffers: from that stream's own memory, so that neither a
+    workspace nor a dropped result is handed out again before `stream` is past
+    the call.  What the caller keeps is recorded on the current stream as well.
+    Inputs are the caller's: they have to outlive the call."""
+
+    def __init__(self, stream, device):
+        self.device, self.side = device, None
+        if stream is None:
+            return
+        import torch
+        handle = int(stream if isinstance(stream, int) else stream.cuda_stream)
+        self.current = torch.cuda.current_stream(device)
+        if handle == self.current.cuda_stream:
+            return
+        if isinstance(stream, torch.cuda.Stream):
+            self.side = stream
+        elif handle in (0, 1):  # (the legacy default stream has two names)
+            self.side = torch.cuda.default_stream(device)
+        else:
+            self.side = torch.cuda.ExternalStream(handle, device)
+
+    def scope(self):
+        """Allocations in it are the stream's."""
+        import torch
+        return contextlib.nullcontext() if self.side is None else torch.cuda.stream(self.side)
+
+    def scratch(self, nbytes: int):
+        import torch
+        with self.scope():
+            return torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+
+    def workspace(self, L: "DeviceLayer", M: int, mode: int) -> Workspace:
+        with self.scope():
+            return Workspace(L, M, mode, self.device)
+
+    def result(self, shape, dtype):
+        import torch
+        if self.side is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with self.scope():
+            t = torch.empty(shape, dtype=dtype, device=self.device)
+        t.record_stream(self.current)
+        return t
+
+
 def layer_forward(L: DeviceLayer, x, y=None, residual=None, idx=None, w=None, ws=None,
                   mode: int = moeq.MODE_AUTO, stream=None):
     """y = layer(x) for bf16 x [M][H] on the device; returns (y, idx, w)."""
     import torch
-    M = x.shape[0]
+    M, buf = x.shape[0], _Buffers(stream, x.device)
     if y is None:
-        y = torch.empty((M, L.cfg.H), dtype=torch.float32, device=x.device)
+        y = buf.result((M, L.cfg.H), torch.float32)
     if idx is None:
-        idx = torch.empty((M, L.cfg.K), dtype=torch.int32, device=x.device)
+        idx = buf.result((M, L.cfg.K), torch.int32)
     if w is None:
-        w = torch.empty((M, L.cfg.K), dtype=torch.float32, device=x.device)
+        w = buf.result((M, L.cfg.K), torch.float32)
     if ws is None:
-        ws = Workspace(L, M, mode, x.device)
+        ws = buf.workspace(L, M, mode)
     moeq.moeq_layer_forward(L.desc, x, M, y, residual, idx, w, ws.buf, ws.bytes, mode, stream)
     return y, idx, w
 
@@ -101,17 +149,17 @@ def layer_forward_norm(L: DeviceLayer, x, gamma, eps: float, y=None, y_norm=None
     """y = layer(x) and y_norm = bf16 RMS norm of y with weights gamma (bf16
     [H]); returns (y, y_norm, idx, w)."""
     import torch
-    M = x.shape[0]
+    M, buf = x.shape[0], _Buffers(stream, x.device)
     if y is None:
-        y = torch.empty((M, L.cfg.H), dtype=torch.float32, device=x.device)
+        y = buf.result((M, L.cfg.H), torch.float32)
     if y_norm is None:
-        y_norm = torch.empty((M, L.cfg.H), dtype=torch.bfloat16, device=x.device)
+        y_norm = buf.result((M, L.cfg.H), torch.bfloat16)
     if idx is None:
-        idx = torch.empty((M, L.cfg.K), dtype=torch.int32, device=x.device)
+        idx = buf.result((M, L.cfg.K), torch.int32)
     if w is None:
-        w = torch.empty((M, L.cfg.K), dtype=torch.float32, device=x.device)
+        w = buf.result((M, L.cfg.K), torch.float32)
     if ws is None:
-        ws = Workspace(L, M, mode, x.device)
+        ws = buf.workspace(L, M, mode)
     moeq.moeq_layer_forward_norm(L.desc, x, M, y, gamma, eps, y_norm, residual, idx, w, ws.buf,
                                  ws.bytes, mode, stream)
     return y, y_norm, idx, w
@@ -120,30 +168,21 @@ def layer_forward_norm(L: DeviceLayer, x, gamma, eps: float, y=None, y_norm=None
 def expert_ffn(L: DeviceLayer, x, idx, w, y=None, residual=None, ws=None,
                mode: int = moeq.MODE_AUTO, stream=None):
     import torch
-    M = x.shape[0]
+    M, buf = x.shape[0], _Buffers(stream, x.device)
     if y is None:
-        y = torch.empty((M, L.cfg.H), dtype=torch.float32, device=x.device)
+        y = buf.result((M, L.cfg.H), torch.float32)
     if ws is None:
-        ws = Workspace(L, M, mode, x.device)
+        ws = buf.workspace(L, M, mode)
     moeq.moeq_expert_ffn(L.desc, x, M, idx, w, residual, y, ws.buf, ws.bytes, mode, stream)
     return y
-
-
-def _scratch(nbytes: int, device, stream):
-    """A workspace for one call, reusable by others once `stream` is past it."""
-    import torch
-    if isinstance(stream, torch.cuda.Stream):
-        with torch.cuda.stream(stream):
-            return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 def route_groups(r: moeq.Routing, logits, bias=None, stream=None):
     """Routing `r` of logits [M][E]; returns (idx, w)."""
     import torch
-    M = logits.shape[0]
-    idx = torch.empty((M, r.top_k), dtype=torch.int32, device=logits.device)
-    w = torch.empty((M, r.top_k), dtype=torch.float32, device=logits.device)
+    M, buf = logits.shape[0], _Buffers(stream, logits.device)
+    idx = buf.result((M, r.top_k), torch.int32)
+    w = buf.result((M, r.top_k), torch.float32)
     moeq.moeq_route_groups(r, logits, idx, w, bias, stream)
     return idx, w
 
@@ -155,14 +194,13 @@ def add_rmsnorm(x, gamma, eps: float, residual=None, want_y: bool = True, q_dtyp
     in q_dtype (torch.int8 or torch.float8_e4m3fn) with their scales."""
     import torch
     M, H = x.shape
-    r = torch.empty_like(residual, memory_format=torch.contiguous_format) \
-        if residual is not None else None
-    y = torch.empty((M, H), dtype=torch.bfloat16, device=x.device) if want_y else None
+    buf = _Buffers(stream, x.device)
+    r = buf.result(residual.shape, residual.dtype) if residual is not None else None
+    y = buf.result((M, H), torch.bfloat16) if want_y else None
     q = qs = None
     if q_dtype is not None:
-        q = torch.empty((M, H), dtype=q_dtype, device=x.device)
-        qs = torch.empty((M, -(-H // q_group) if q_group else 1), dtype=torch.float32,
-                         device=x.device)
+        q = buf.result((M, H), q_dtype)
+        qs = buf.result((M, -(-H // q_group) if q_group else 1), torch.float32)
     moeq.moeq_add_rmsnorm(x, gamma, eps, residual, r, y, q, qs, q_group, stream)
     return r, y, q, qs
 
@@ -173,13 +211,13 @@ def linear(t: moeq.QTensor, x, out_dtype=None, expert: int = 0, x_scales=None, x
     """y = act(x W^T + bias) * mul + residual (out_dtype: fp32 or, by default,
     bf16); returns y.  The workspace is allocated where none is given."""
     import torch
-    M = x.shape[0]
+    M, buf = x.shape[0], _Buffers(stream, x.device)
     if y is None:
-        y = torch.empty((M, t.out_dim), dtype=out_dtype or torch.bfloat16, device=x.device)
+        y = buf.result((M, t.out_dim), out_dtype or torch.bfloat16)
     if ws is None:
         need = moeq.moeq_linear_workspace_bytes(t, M, x.dtype, y.dtype)
         if need:
-            ws = _scratch(need, x.device, stream)
+            ws = buf.scratch(need)
     moeq.moeq_linear(t, expert, x, y, x_scales, x_group, bias, act, mul, residual, ws, stream)
     return y
 
@@ -189,12 +227,12 @@ def layer_forward_routed(L: DeviceLayer, r: moeq.Routing, x, bias=None, residual
     """y = layer(x) under routing `r`; returns (y, idx, w).  ws: uint8 buffer of
     moeq_routed_workspace_bytes."""
     import torch
-    M = x.shape[0]
-    y = torch.empty((M, L.cfg.H), dtype=torch.float32, device=x.device)
-    idx = torch.empty((M, L.cfg.K), dtype=torch.int32, device=x.device)
-    w = torch.empty((M, L.cfg.K), dtype=torch.float32, device=x.device)
+    M, buf = x.shape[0], _Buffers(stream, x.device)
+    y = buf.result((M, L.cfg.H), torch.float32)
+    idx = buf.result((M, L.cfg.K), torch.int32)
+    w = buf.result((M, L.cfg.K), torch.float32)
     if ws is None:
-        ws = _scratch(moeq.moeq_routed_workspace_bytes(L.desc, M, mode), x.device, stream)
+        ws = buf.scratch(moeq.moeq_routed_workspace_bytes(L.desc, M, mode))
     moeq.moeq_layer_forward_routed(L.desc, r, x, M, y, bias, residual, idx, w, ws, ws.numel(),
                                    mode, stream)
     return y, idx, w
