@@ -233,6 +233,18 @@ def _dense(name, t, shape, dtype, device):
     return t.data_ptr()
 
 
+def _first_rows(name, t, M, n, dtype, device):
+    """Address of a contiguous tensor of at least M rows of n elements (None and
+    raw addresses as they are)."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.dim() != 2 or t.shape[0] < M or t.shape[1] != n or t.dtype != dtype \
+            or not t.is_contiguous() or (device is not None and t.get_device() != device):
+        raise ValueError(f"{name}: expected contiguous {dtype} [{M}][{n}] on device {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+    return t.data_ptr()
+
+
 # The argument structs packed in one step (native alignment; a null pointer
 # is 0): several times faster than filling a ctypes Structure.
 _NORM_ARGS = struct.Struct("@PiqPiqPqPfPqPiqPi0q")
@@ -361,11 +373,30 @@ def moeq_routed_workspace_bytes(L: Layer, M: int, mode: int = MODE_AUTO) -> int:
 def moeq_layer_forward_routed(L: Layer, r: Routing, x, M: int, y, bias=None, residual=None,
                               idx_out=None, w_out=None, ws=None, ws_bytes: int = 0,
                               mode: int = MODE_AUTO, stream=None) -> None:
-    """moeq_layer_forward with routing `r` (and its balance bias)."""
+    """moeq_layer_forward with routing `r` and its balance bias (fp32 [E]).  x:
+    bf16 [M][H]; y, residual: fp32 [M][H]; idx_out: int32 [M][K]; w_out: fp32
+    [M][K], at least M rows of each; ws: uint8 buffer of at least ws_bytes.  Raw
+    addresses are taken as they are."""
+    if not _DTYPES:
+        _load_torch()
+    dev = None if x is None or isinstance(x, int) else _device("x", x)
+    H, E, K = L.hidden, L.n_experts, L.top_k
+    px = _first_rows("x", x, M, H, _bfloat16, dev)
+    py = _first_rows("y", y, M, H, _float32, dev)
+    pr = _first_rows("residual", residual, M, H, _float32, dev)
+    pi = _first_rows("idx_out", idx_out, M, K, _int32, dev)
+    pw = _first_rows("w_out", w_out, M, K, _float32, dev)
+    pb = _ptr(bias)
+    if bias is not None and not isinstance(bias, int):
+        pb = _dense("bias", bias, (E,), _float32, bias.get_device() if dev is None else dev)
+    if ws is not None and not isinstance(ws, int):
+        if not ws.is_contiguous() or ws.nbytes < ws_bytes or \
+                (dev is not None and ws.get_device() != dev):
+            raise ValueError(f"ws: expected {ws_bytes} contiguous bytes on device {dev}, got "
+                             f"{ws.nbytes} on {ws.device}")
     _check("moeq_layer_forward_routed",
-           _lib.moeq_layer_forward_routed(C.byref(L), C.byref(r), _ptr(bias), _ptr(x), M, _ptr(y),
-                                          _ptr(residual), _ptr(idx_out), _ptr(w_out), _ptr(ws),
-                                          ws_bytes, mode, _stream(stream)))
+           _lib.moeq_layer_forward_routed(C.byref(L), C.byref(r), pb, px, M, py, pr, pi, pw,
+                                          _ptr(ws), ws_bytes, mode, _stream(stream)))
 
 
 def moeq_workspace_bytes(L: Layer, M: int, mode: int = MODE_AUTO) -> int:
