@@ -778,10 +778,10 @@ namespace moeq {
 // The argument checks every layer entry point runs before its workspace
 // check: the layer, M, the mode, and the token, output and residual pointers.
 moeq_status forward_arg_check(const moeq_layer* L, const uint16_t* x, int32_t M, float* y,
-                              const float* residual, int32_t mode) {
+                              const float* residual, int32_t mode, bool empty) {
   moeq_status s = check_layer(L);
   if (s != MOEQ_OK) return s;
-  if (M < 0 || !x || !y) return MOEQ_ERR_INVALID_ARG;
+  if (M < 0 || ((!x || !y) && !(empty && M == 0))) return MOEQ_ERR_INVALID_ARG;
   if (mode < MOEQ_MODE_AUTO || mode > MOEQ_MODE_PREFILL) return MOEQ_ERR_INVALID_ARG;
   if (M == 0) return MOEQ_OK;
   if (!aligned(x, 16) || (L->hidden * 2) % 16 || !aligned(y, 16) || L->hidden % 4)

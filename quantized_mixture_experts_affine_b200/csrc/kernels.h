@@ -11,8 +11,9 @@ namespace moeq {
 
 // Argument checks shared by the layer entry points (api.cu): the layer, M,
 // the mode, and the x / y / residual pointers, before any workspace check.
+// empty: a batch of no tokens may come without buffers.
 moeq_status forward_arg_check(const moeq_layer* L, const uint16_t* x, int32_t M, float* y,
-                              const float* residual, int32_t mode);
+                              const float* residual, int32_t mode, bool empty = false);
 
 // Whether the layer's shapes run in `mode` (resolved for M > 0 tokens); after
 // forward_arg_check (api.cu).

@@ -212,7 +212,7 @@ MOEQ_API moeq_status moeq_layer_forward_routed(const moeq_layer* L, const moeq_r
                                                float* y, const float* residual, int32_t* idx_out,
                                                float* w_out, void* ws, size_t ws_bytes,
                                                int32_t mode, void* stream) {
-  TRY(forward_arg_check(L, x, M, y, residual, mode));
+  TRY(forward_arg_check(L, x, M, y, residual, mode, /*empty=*/true));
   TRY(check_routing(r));
   if (r->n_experts != L->n_experts || r->top_k != L->top_k) return MOEQ_ERR_INVALID_ARG;
   if (!on(bias, 4) || !on(idx_out, 4) || !on(w_out, 4)) return MOEQ_ERR_ALIGNMENT;

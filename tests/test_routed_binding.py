@@ -67,3 +67,14 @@ def test_one_device_for_all(call, other, monkeypatch):
     none.pop(other)
     with pytest.raises(ValueError):
         call(**none)
+
+
+def test_an_empty_batch_needs_no_buffers(call):
+    """Empty tensors have no address: nothing is launched, nothing refused."""
+    z = dict(x=torch.zeros(0, H, dtype=torch.bfloat16), y=torch.zeros(0, H),
+             residual=torch.zeros(0, H), idx_out=torch.zeros(0, K, dtype=torch.int32),
+             w_out=torch.zeros(0, K), ws=torch.zeros(0, dtype=torch.uint8), ws_bytes=0)
+    assert z["x"].data_ptr() == 0
+    call(m=0, **z)
+    with pytest.raises(moeq.MoeqError):
+        call(m=-1)
