@@ -42,7 +42,7 @@ struct PrepArgs {
   __half* w16;  // [w_parts][out_dim][in_dim]
   float* fw;    // [out_dim]
   int x_parts, w_parts;
-  int x_blocks;  // first blocks of the grid: tokens; the others: weights
+  int x_blocks;  // (k_lin_tokens) first blocks of the grid: tokens; the others: weights
   // For the product that unpacks the weights itself: rows padded with zeros
   // to x_row columns, eights of columns moved as its threads take them
   // (64 neighbours of 256 go to four blocks of 64), and with x_split each
@@ -326,9 +326,9 @@ __device__ __forceinline__ void prep_8bit_row(const PrepArgs& p, int64_t m) {
   for (int c = 256 * RV; c + 8 * lane < p.x_row; c += 256) put(c, read(c));
 }
 
-// A token row by the whole CTA; up to 8 * NV values of a thread stay in
-// registers between the maximum and the conversion, longer rows are read
-// again (from L1).
+// A token row by the whole CTA, in the layout of the product that unpacks the
+// weights; up to 8 * NV values of a thread stay in registers between the maximum
+// and the conversion, longer rows are read again (from L1).
 constexpr int NV = 2;
 __device__ __forceinline__ void prep_tokens(const PrepArgs& p, int64_t m) {
   __shared__ float red[32];
@@ -339,7 +339,6 @@ __device__ __forceinline__ void prep_tokens(const PrepArgs& p, int64_t m) {
   const bool by128 = type != MOEQ_BF16 && l.a.x_group == 128;
   const float* xs = l.a.x_scales + m * (by128 ? (K + 127) / 128 : 1);
   __half* out = p.x16 + m * p.x_row;
-  const int64_t part = (int64_t)l.M * p.x_row;
   auto load = [&](int c, float (&v)[8]) {
     load_x8(row, type, c, v);
     if (by128) {
@@ -384,15 +383,10 @@ __device__ __forceinline__ void prep_tokens(const PrepArgs& p, int64_t m) {
   auto put = [&](int c, float (&u)[8]) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) u[j] *= f;
-    if (p.x_runs) {
-      c = run_column(c);
-      if (p.x_split) {
-        const float w[8] = {u[0], u[4], u[1], u[5], u[2], u[6], u[3], u[7]};
-        store_halves(out + c, part, false, w);
-        return;
-      }
-    }
-    store_halves(out + c, part, p.x_parts == 2, u);
+    c = run_column(c);
+    const float w[8] = {u[0], u[4], u[1], u[5], u[2], u[6], u[3], u[7]};
+    if (p.x_split) store_halves(out + c, 0, false, w);
+    else store_halves(out + c, 0, false, u);
   };
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -530,7 +524,7 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* tmap,
       : "memory");
 }
 
-// Warps 0: TMA, 1: MMA (rank 0), 2: TMEM; 4..11 (SUMS: 4..19): epilogue.
+// Warps 0: TMA, 1: MMA (rank 0), 2: TMEM; 4..19: epilogue.
 //
 // The tensor cores cut their sums off (towards zero): a chain of n products of
 // 16 columns comes out about n 2^-27 too small.  A bf16 y does not show it;
@@ -541,10 +535,10 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* tmap,
 // int8 by 128 columns, relative error 1.0e-6 with them last, 3.7e-7 so (the plain
 // fp32 product 5.3e-7).
 constexpr int kChunk = 8;
-constexpr int gemm_threads(bool sums) { return 640; }
+constexpr int kGemmThreads = 640;
 
 template <bool SUMS>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads(SUMS), 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     k_lin_gemm(const __grid_constant__ GemmArgs a) {
   using S = GemmSmem;
   const int BN = a.tokens;
@@ -824,8 +818,7 @@ cudaError_t run_gemm(GemmArgs& g, int sms, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int64_t items = (int64_t)g.tiles_o * g.tiles_m;
   const int64_t units = items < sms / 2 ? items : sms / 2;
-  return launch_after(k_lin_gemm<SUMS>, (unsigned)(2 * units), gemm_threads(SUMS), bytes, st,
-                      g);
+  return launch_after(k_lin_gemm<SUMS>, (unsigned)(2 * units), kGemmThreads, bytes, st, g);
 }
 
 }  // namespace
@@ -857,9 +850,8 @@ cudaError_t launch_linear_gemm(const LinArgs& l, void* ws, int* status, int* lau
   p.fx = (float*)(base + lay.fx);
   p.w16 = (__half*)(base + lay.w16);
   p.fw = (float*)(base + lay.fw);
-  p.x_blocks = l.M;
   p.x_row = l.in_dim;
-  p.x_runs = p.x_split = 0;
+  p.x_blocks = p.x_runs = p.x_split = 0;
   if (unpack_inside(l.M, l.in_dim, l.out_dim, l.a.out_type) && p.x_parts == 1) {
     const FusedLayout fl = fused_layout(l.M, l.in_dim, l.out_dim, l.G);
     p.x16 = (__half*)(base + fl.x16);
@@ -872,10 +864,11 @@ cudaError_t launch_linear_gemm(const LinArgs& l, void* ws, int* status, int* lau
     // a token row per CTA, for the latency, or per warp: 616 x 4480 x 128 13.2
     // against 14.3 us, 1868 x 384 x 960 17.7 against 12.3
     const bool warps = l.M > 1024;
-    if (warps) p.x_blocks = (l.M + 7) / 8;
+    p.x_blocks = warps ? (l.M + 7) / 8 : l.M;
     *launches = 2;
-    const cudaError_t e = launch_after(
-        warps ? k_lin_tokens<true> : k_lin_tokens<false>, (unsigned)(p.x_blocks + (l.out_dim + 7) / 8), 256, 0, st, p);
+    const cudaError_t e =
+        launch_after(warps ? k_lin_tokens<true> : k_lin_tokens<false>,
+                     (unsigned)(p.x_blocks + (l.out_dim + 7) / 8), 256, 0, st, p);
     return e != cudaSuccess ? e : launch_linear_fused(l, p.x16, p.fx, p.fw, p.sb, status, st);
   }
   GemmArgs g;
