@@ -7,8 +7,9 @@ fp32's normal range are off by its smallest step.
 import pytest
 
 import ops_reference as ref
-from test_add_rmsnorm_gpu import SCALE, T, Y, draw
+from quantized_mixture_experts_affine_b200 import moeq
 from quantized_mixture_experts_affine_b200.layer import add_rmsnorm
+from test_add_rmsnorm_gpu import SCALE, T, Y, draw
 
 pytestmark = pytest.mark.gpu
 
@@ -95,3 +96,41 @@ def test_rows_are_those_of_a_large_batch(H, xt, rt, q, group):
         for a, b in zip(one, many):
             if b is not None:
                 assert torch.equal(a[0].view(torch.uint8), b[m].view(torch.uint8))
+
+
+@pytest.mark.parametrize("H", [256, 1001])
+@pytest.mark.parametrize("rt", ["f32", "bf16"])
+def test_ends_of_the_range_in_place_strided_and_without_a_new_stream(H, rt):
+    """Rows out of range beside ordinary ones: the stream in place, the stream not
+    written at all, rows that are parts of wider ones, y alone."""
+    x, gamma, res = draw(12, H, "f32", rt, H + 4)
+    scale = torch.tensor([1.0, 1e-30, 1e24, 0.0, 1e-20, 1e29], device="cuda").repeat(2)[:, None]
+    x, res = x.clamp(-10, 10) * scale, (res.float() * scale).to(T[rt])
+    x[7] = float("nan")
+    res[7] = 0
+    x[8, 3] = float("inf")
+    fine = [m for m in range(12) if m not in (7, 8)]
+    for q, group in (("int8", 0), ("e4m3", 128)):
+        want = ref.add_rmsnorm(x, gamma, 1e-6, res, q, group)
+        n = -(-H // group) if group else 1
+        wide = torch.zeros(12, H + 3, dtype=T[rt], device="cuda")
+        for stream in ("in place", "none"):
+            wide[:, 1:H + 1] = res
+            r = wide[:, 1:H + 1]
+            y = torch.zeros(12, H + 5, dtype=torch.bfloat16, device="cuda")
+            c = torch.zeros(12, H + 7, dtype=torch.int8, device="cuda").view(T[q])
+            s = torch.zeros(12, n, device="cuda")
+            moeq.moeq_add_rmsnorm(x, gamma, 1e-6, r, r if stream == "in place" else None,
+                                  y[:, 2:H + 2], c[:, 3:H + 3], s, group)
+            torch.cuda.synchronize()
+            after = want["r"] if stream == "in place" else res
+            assert torch.equal(r[fine], after[fine])
+            assert torch.equal(c[:, 3:H + 3].float().double()[fine], want["codes"][fine])
+            for got, ref_, rel, least in ((s, want["scales"], SCALE, TINY),
+                                          (y[:, 2:H + 2], want["y"], Y, 1e-38)):
+                d = (got.double() - ref_).abs()[fine]
+                assert bool((d <= rel * ref_.abs()[fine] + least).all())
+            assert torch.isnan(s[7]).all() and bool((c[7].float() == 0).all())
+            assert torch.isnan(s[8, 0]) and bool((c[8, 3:128].float() == 0).all())
+        y1 = add_rmsnorm(x, gamma, 1e-6, res)[1]
+        assert torch.equal(y1[fine], y[:, 2:H + 2][fine])

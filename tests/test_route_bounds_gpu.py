@@ -86,3 +86,21 @@ def test_experts_under_a_bias_of_minus_infinity(M, E):
     b[E - 2:] = 0.25
     check(l, 8, b)
     check(torch.randn(M, E, device="cuda", generator=g), 6, b)
+
+
+@pytest.mark.parametrize("M,E,K,groups,keep", [(16, 512, 8, 1, 1), (16, 512, 8, 8, 4),
+                                               (2400, 128, 8, 8, 3), (8, 2048, 8, 16, 8)])
+def test_biased_softmax_of_many_like_logits(M, E, K, groups, keep):
+    """Hundreds of terms of the normaliser with one exponent, and so one rounding;
+    biases that even the scores out but for their own rounding."""
+    for d in (2.7, 4.9, 6.3):
+        l = torch.full((E,), -d)
+        l[7] = 0.0
+        l -= torch.linspace(0, 1e-3, E).roll(11)
+        p = torch.softmax(l.double(), 0)
+        b = (p.max() - p).float()
+        rows = torch.stack([l] * M).cuda()
+        r = moeq.routing(E, K, moeq.SCORE_SOFTMAX, groups, keep, 2, True)
+        idx, _ = route_groups(r, rows, b.cuda())
+        ri, _ = ref.route(rows, K, "softmax", b.cuda(), groups, keep, 2, True)
+        assert torch.equal(idx.cpu(), ri)
