@@ -362,8 +362,8 @@ typedef struct {
  *   w = s_k (/ sum of the K s_k when renorm) * routed_scale.
  * A group's value is its largest v (group_top 1) or the sum of its two
  * largest v (group_top 2; without a bias v is s there).  The choice is that
- * of real arithmetic: where fp32 scores are too close to tell, the token is
- * routed again in fp64.
+ * of fp64 scores: where fp32 ones are too close to tell, the token is routed
+ * again in fp64 (a score that underflows there is 0, and so is its weight).
  * A logit of NaN or -inf takes its expert out: it scores 0 and is chosen
  * only when fewer than K others are left in the kept groups, lowest index
  * first, with weight 0.  A token whose every logit is out gets weights 0.
@@ -450,11 +450,13 @@ typedef struct {
  * blocks between MoE layers (mul holds the up projection when this call is
  * the gate's), router logits of a whole prompt.  An I8 or E4M3 x with its
  * scales is moeq_add_rmsnorm's output.
- * Sums are fp32 throughout.  Few tokens multiply the codes themselves
- * (exact products; |x| up to 2^110, the sums are of codes times x).  Many
- * tokens with a bf16 y take weights rounded to fp16 (relative 2^-11, an eighth
- * of y's own rounding); with an fp32 y the weights keep 22 bits.  Neither has
- * a range limit: rows are scaled by powers of two.
+ * Sums are fp32 throughout.  Few tokens (up to 16, and while 16 x 16 tiles of y
+ * are no more than the SMs, twice that with an fp32 y) multiply the codes
+ * themselves (exact products; |x| up to 2^110, the sums are of codes times x).
+ * More tokens with a bf16 y take weights rounded to fp16 (relative 2^-11, an
+ * eighth of y's own rounding), and so are the values of an 8-bit x times their
+ * scales where these change along the row (x_group 128).  With an fp32 y both
+ * keep 22 bits.  Neither has a range limit: rows are scaled by powers of two.
  * An x row that holds an infinity or NaN gives a row of unspecified values
  * and leaves the others untouched.
  *   y may be mul's or residual's memory (same stride); it may not overlap x.

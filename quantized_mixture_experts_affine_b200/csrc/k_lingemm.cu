@@ -6,7 +6,8 @@
 // value is out of fp16's range; the powers are undone in the epilogue.  A
 // token value of bf16 or 8 bits is exact in fp16 unless it lies 2^-28 below
 // its row's largest; a weight is rounded once (relative 2^-11; y rounds by up
-// to 2^-8 in bf16).  For an fp32 y the weights keep a second fp16 (22 bits),
+// to 2^-8 in bf16), and so is an 8-bit value times its scale where that changes
+// along the row.  For an fp32 y the weights keep a second fp16 (22 bits),
 // and so do tokens whose scales change along the row; the product is then the
 // sum of the parts' products.
 //

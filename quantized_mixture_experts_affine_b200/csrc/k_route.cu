@@ -1,22 +1,24 @@
 // Grouped top-k routing: softmax or sigmoid scores, a balance bias that only
 // the selection sees, group-limited choice, renormalised weights.
 //
-// The selection is exact: it gives what real arithmetic would.  Without a bias
+// The selection is exact: it gives what fp64 scores would.  Without a bias
 // the experts are ordered by their logits.  With one (and for the sums of two
 // that rank groups) the scores are taken in fp32 first, with a bound on their
 // error; where two candidates that decide something lie closer than that, fp64
 // decides: for picks among the few experts concerned, one per lane, for groups
-// the whole row again.  Such rows are under 1 % of 512 normal logits.
+// the whole row again.  Such rows are about 1 % of 512 normal logits.
 //
 // A row of up to 512 experts is held in registers by a warp, or with many rows
 // by 8 or 16 lanes, groups padded to a power of two of quads (300 rows of 160 in
 // 8 groups: 8.5 us in shared memory, 4.3 so); what is larger (k_route_any) lives
 // in shared memory.  Few
 // rows are bound by the chain of load, exponential and K picks (3.8 us for one
-// row, 5.8 us for 2048 rows of 256 experts in 8 groups), many by instruction
-// issue (16,068 rows of 128 in 8 groups, top-8: 11.2 us; 15.4 us with picks
-// that scanned 16 registers instead of a quad in shared memory, 24.3 us with a
-// warp per row).
+// row, 5.9 us for 2048 rows of 256 experts in 8 groups).  Many rows (16,068 of 128
+// in 8 groups, top-8: 11.2 us; 15.4 us with picks that scanned 16 registers instead
+// of a quad in shared memory, 24.3 us with a warp per row) take 423 warp
+// instructions each, 6 us of issue at one a clock; the schedulers issue in 58 % of
+// their clocks, the rest are the dependent steps of a pick (shuffles, shared
+// memory) with six warps to hide them.
 #include "common.cuh"
 #include "ops.h"
 #include "route.cuh"
