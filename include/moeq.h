@@ -366,7 +366,8 @@ typedef struct {
  * again in fp64 (a score that underflows there is 0, and so is its weight).
  * A logit of NaN or -inf takes its expert out: it scores 0 and is chosen
  * only when fewer than K others are left in the kept groups, lowest index
- * first, with weight 0; a group with no expert left ranks last.  A token whose every logit is out gets weights 0.
+ * first, with weight 0; a group with no expert left ranks last.  A token whose
+ * every logit is out gets weights 0.
  *   logits: fp32 or bf16 (logit_type) [M][E], rows logit_stride apart;
  *   bias: nullable fp32 [E], without NaN; idx: int32 [M][K]; w: fp32 [M][K].
  * idx and w are moeq_expert_ffn's inputs.  Errors: INVALID_ARG, UNSUPPORTED
